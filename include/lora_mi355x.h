@@ -374,6 +374,182 @@ int lora_apply_group_noalloc(lora_ctx *ctx, int32_t n, const int32_t *modules,
                              const void *const *x, void *const *y,
                              const int32_t *token_slot_idx, int32_t n_tokens, void *stream);
 
+/*
+ * The frozen part of a layer around its adapters: base products whose weights
+ * are held in 4 bits, the gated feed-forward on them, and rotary positions.
+ * An adapter's update is added to the base output of its module (y of
+ * lora_apply), so these calls write the y that lora_apply then updates, or take
+ * the update that it has formed.  They use no plan and no slot, and neither
+ * lora_stats nor lora_profile counts them.
+ */
+
+/*
+ * Give `module` its base weight in 4 bits with one scale, and optionally one
+ * zero point, per group of inputs of each output feature:
+ *
+ *     W[n,k] = (q[n,k] - zero[n, k / group_size]) * scale[n, k / group_size]
+ *
+ *   q           [d_out][d_in / 2] bytes, row-major: two inputs a byte, the even
+ *               one in the low half; values 0..15
+ *   scale       [d_out][groups] floats, groups = ceil(d_in / group_size); the
+ *               last group of a row may be short
+ *   zero        [d_out][groups] bytes (their low 4 bits are read), or NULL: 8
+ *   group_size  32, 64 or a multiple of 128, or 0: one group a row
+ *   bias        [d_out] values of the ctx dtype, or NULL
+ * q, scale, zero and bias are pinned host or device memory, and stay unmodified
+ * until lora_sync_loads returns (or a later call on a stream that waited for the
+ * load has completed).  A bf16 ctx holds scales with 16 significant bits: exact
+ * for scales that came from fp16 or bf16, else off by at most 2^-16 of their
+ * value.  Asynchronous on the ctx's side stream, with the ordering and the
+ * capture rule of lora_slot_load; a load over a weight in use waits for the
+ * base products already enqueued.  Storage (d_out x d_in / 2 bytes and 4 or 8
+ * bytes per scale, the sizes rounded up to 16 and 128) is allocated at the
+ * module's first load, and again by a load whose scales need more; all of it is
+ * kept until lora_slots_destroy.  A graph captured before a reload sees the new
+ * weights if group_size and the presence of a bias are as before; any other
+ * reload needs a new capture.  A load does not touch slots, adapters or saved
+ * modules.
+ * Errors: LORA_ERR_BAD_MODULE; q or scale NULL or a bad group_size ->
+ * LORA_ERR_INVALID_ARGUMENT; LORA_ERR_HOST_NOT_PINNED; LORA_ERR_OUT_OF_MEMORY.
+ */
+int lora_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scale,
+                   const uint8_t *zero, int32_t group_size, const void *bias);
+
+/*
+ * y[t,n] = round( sum_k x[t,k] * W[n,k] + bias[n] + add[t,n] ) for t < n_tokens.
+ *   x    [n_tokens][d_in], y [n_tokens][d_out], row-major, device, ctx dtype
+ *   add  [n_tokens][d_out] (a residual stream, say), or NULL; it may be y itself
+ * y must not overlap x, and add must be y or apart from it.  Rows from n_tokens
+ * on are left as they are; n_tokens == 0 is a no-op.  Products of x with q - zero
+ * are summed in fp32 over each group, and the groups' sums are scaled and summed
+ * in fp32; bf16 results are rounded once.  Infinities and NaNs in x give what
+ * the formula gives.
+ * Errors: a module without a base weight, n_tokens < 0, NULL x or y, overlapping
+ * buffers -> LORA_ERR_INVALID_ARGUMENT; LORA_ERR_BAD_MODULE;
+ * n_tokens > max_tokens -> LORA_ERR_TOO_MANY_TOKENS.
+ */
+int lora_base(lora_ctx *ctx, const void *x, const void *add, void *y, int32_t n_tokens,
+              int32_t module, void *stream);
+
+/*
+ * lora_base for n (1..LORA_MAX_GROUP) modules of one batch in one call, e.g. q, k
+ * and v of a layer: modules with the same scale storage (group sizes 32; 64;
+ * every other) share a launch.  add may be NULL, as may its entries.  A module
+ * may appear more than once.  No y may overlap another member's x, add or y.
+ * Results equal n single-module calls.
+ */
+int lora_base_group(lora_ctx *ctx, int32_t n, const int32_t *modules, const void *const *x,
+                    const void *const *add, void *const *y, int32_t n_tokens, void *stream);
+
+/* Activations of lora_base_gated. */
+enum {
+    LORA_ACT_SILU = 0,       /* g / (1 + exp(-g)) */
+    LORA_ACT_GELU = 1,       /* g / 2 * (1 + erf(g / sqrt(2))) */
+    LORA_ACT_GELU_TANH = 2   /* g / 2 * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3))) */
+};
+
+/*
+ * The first half of a gated feed-forward in one kernel, both products, the
+ * activation and the product of the two:
+ *
+ *     g[t,n] = sum_k x[t,k] * Wg[n,k] + bias_g[n] + gate_add[t,n]
+ *     u[t,n] = sum_k x[t,k] * Wu[n,k] + bias_u[n] + up_add[t,n]
+ *     y[t,n] = round( act(g[t,n]) * u[t,n] )
+ *
+ * with g and u kept in fp32.  gate_module and up_module are two modules of the
+ * same shape with base weights of the same scale storage (group size 32; 64;
+ * any other).  gate_add and up_add, [n_tokens][d_out] or NULL, take what
+ * adapters add to the two modules: lora_apply onto zeroed buffers.  (Saved
+ * modules replace the base output and have no place here: their tokens need
+ * lora_base and lora_apply.)  y may be gate_add or up_add, and must not overlap
+ * x.  Otherwise as lora_base; an unknown activation or two modules that do not
+ * fit each other -> LORA_ERR_INVALID_ARGUMENT.
+ */
+int lora_base_gated(lora_ctx *ctx, int32_t gate_module, int32_t up_module, const void *x,
+                    const void *gate_add, const void *up_add, void *y, int32_t n_tokens,
+                    int32_t activation, void *stream);
+
+/* Limit of lora_rotary_params.rotary_dim. */
+#define LORA_ROTARY_MAX_DIM 256
+
+enum {
+    LORA_ROTARY_HALF = 0,         /* pair p is elements p and p + rotary_dim / 2 of a head */
+    LORA_ROTARY_INTERLEAVED = 1   /* pair p is elements 2p and 2p + 1 */
+};
+
+/*
+ * How the rate f_p = base^(-2p / rotary_dim) of pair p (radians a position) is
+ * scaled for contexts longer than the model's first training:
+ *   NONE    f_p
+ *   LINEAR  f_p / factor (positions squeezed by factor)
+ *   YARN    pairs that turn more than beta_fast times over original_positions
+ *           keep f_p, those that turn less than beta_slow times get f_p / factor,
+ *           with a linear ramp over the pair index between the two indices
+ *           (rounded outwards), and cosine and sine are multiplied by
+ *           attention_factor, 0.1 ln(factor) + 1 where that is 0 ("YaRN:
+ *           Efficient Context Window Extension of Large Language Models", Peng
+ *           et al. 2023)
+ *   BANDED  with r = original_positions * f_p / (2 pi) turns: r > high_factor
+ *           keeps f_p, r < low_factor gets f_p / factor, and between them the
+ *           two are mixed linearly in r
+ */
+enum {
+    LORA_ROTARY_SCALE_NONE = 0,
+    LORA_ROTARY_SCALE_LINEAR = 1,
+    LORA_ROTARY_SCALE_YARN = 2,
+    LORA_ROTARY_SCALE_BANDED = 3
+};
+
+typedef struct {
+    int32_t head_dim;             /* elements of a head, even */
+    int32_t rotary_dim;           /* elements that turn, the first of each head: even,
+                                     2..min(head_dim, LORA_ROTARY_MAX_DIM) */
+    int32_t layout;               /* LORA_ROTARY_HALF or LORA_ROTARY_INTERLEAVED */
+    int32_t scaling;              /* LORA_ROTARY_SCALE_* */
+    double base;                  /* > 1, 10000 in most models */
+    double factor;                /* >= 1 (not read for NONE) */
+    double original_positions;    /* > 0 (YARN, BANDED) */
+    double beta_fast, beta_slow;  /* beta_fast > beta_slow > 0 (YARN) */
+    double attention_factor;      /* >= 0 (YARN) */
+    double low_factor, high_factor;   /* high_factor > low_factor > 0 (BANDED) */
+} lora_rotary_params;
+
+/* A model's rotary positions, formed by lora_rotary_init.  Plain data of the
+ * caller: it can be copied, and calls take it by value. */
+typedef struct {
+    int32_t head_dim, rotary_dim, layout;
+    float amplitude;                            /* factor on cosine and sine */
+    double turns[LORA_ROTARY_MAX_DIM / 2];      /* turns a position of each pair */
+} lora_rotary;
+
+/* Form *out from *params, in double, on the host.  Needs no device.  Errors: NULL
+ * or a value outside the ranges above -> LORA_ERR_INVALID_ARGUMENT, with the
+ * detail in lora_last_error(NULL). */
+int lora_rotary_init(lora_rotary *out, const lora_rotary_params *params);
+
+/*
+ * Turn the heads of n (1..LORA_MAX_GROUP) modules' outputs by their tokens'
+ * positions, e.g. q and k after their adapters' updates: for head h of token t
+ * and pair p of elements (a, b),
+ *
+ *     a' = amplitude * (a cos w - b sin w),  b' = amplitude * (b cos w + a sin w),
+ *     w = 2 pi * positions[t] * turns[p]
+ *
+ * and the elements from rotary_dim on are copied.
+ *   x, y        per member [n_tokens][d_out of the module], device, ctx dtype;
+ *               y[i] is x[i] (in place) or apart from every x and every other y
+ *   positions   int32[n_tokens], device.  Negative positions turn back: the
+ *               inverse rotation, which is also the gradient's (with the same
+ *               amplitude)
+ * The angle is formed and reduced in double, so far positions lose nothing.  The
+ * d_out of each module must be a multiple of head_dim.  n_tokens == 0 is a no-op.
+ * Errors as lora_base; a *rotary that lora_rotary_init did not form, or a d_out
+ * that is not whole heads -> LORA_ERR_INVALID_ARGUMENT.
+ */
+int lora_rotary_group(lora_ctx *ctx, const lora_rotary *rotary, int32_t n,
+                      const int32_t *modules, const void *const *x, void *const *y,
+                      const int32_t *positions, int32_t n_tokens, void *stream);
+
 /* Wait for the streams the ctx has launched on (not for the whole device),
  * return the sticky LORA_FLAG_* bits in *flags and clear them. */
 int lora_get_device_flags(lora_ctx *ctx, uint32_t *flags);
@@ -402,8 +578,9 @@ int lora_profile_end(lora_ctx *ctx, lora_profile *out);
 /* Static text for a status code. */
 const char *lora_status_string(int status);
 
-/* Detail of the last error on ctx (or of the last failed lora_slots_create
- * when ctx is NULL); empty string if none.  Valid until the next call. */
+/* Detail of the last error on ctx (or of the last failed lora_slots_create or
+ * lora_rotary_init when ctx is NULL); empty string if none.  Valid until the next
+ * call. */
 const char *lora_last_error(lora_ctx *ctx);
 
 #ifdef __cplusplus

@@ -43,10 +43,21 @@ EXPORTS = ("lora_slots_create", "lora_slots_destroy", "lora_slot_load", "lora_sl
            "lora_expand", "lora_apply",
            "lora_shrink_group", "lora_expand_group", "lora_apply_group",
            "lora_apply_group_noalloc", "lora_apply_group_fused",
+           "lora_base_load", "lora_base", "lora_base_group", "lora_base_gated",
+           "lora_rotary_init", "lora_rotary_group",
            "lora_get_device_flags", "lora_get_stats", "lora_profile_begin", "lora_profile_end",
            "lora_status_string", "lora_last_error")
 
 LORA_MAX_GROUP = 8
+
+LORA_ACT_SILU = 0
+LORA_ACT_GELU = 1
+LORA_ACT_GELU_TANH = 2
+ACTIVATIONS = {"silu": LORA_ACT_SILU, "gelu": LORA_ACT_GELU, "gelu_tanh": LORA_ACT_GELU_TANH}
+
+LORA_ROTARY_MAX_DIM = 256
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "yarn": 2, "banded": 3}
 
 
 class LoraError(RuntimeError):
@@ -67,6 +78,20 @@ class _Profile(ctypes.Structure):
 class _Stats(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in
                 ("loads", "clears", "bytes_loaded", "plans", "shrinks", "expands", "tokens")]
+
+
+class _RotaryParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("head_dim", "rotary_dim", "layout", "scaling")] +
+                [(n, ctypes.c_double) for n in
+                 ("base", "factor", "original_positions", "beta_fast", "beta_slow",
+                  "attention_factor", "low_factor", "high_factor")])
+
+
+class Rotary(ctypes.Structure):
+    """A model's rotary positions (lora_rotary), formed by lora_rotary_init."""
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("turns", ctypes.c_double * (LORA_ROTARY_MAX_DIM // 2))]
 
 
 _lib = None
@@ -106,6 +131,15 @@ def load_library(path: str = LIB_PATH):
                                       ctypes.POINTER(P), P, I32, P], ctypes.c_int),
         "lora_apply_group_fused": ([P, I32, ctypes.POINTER(I32), ctypes.POINTER(P),
                                     ctypes.POINTER(P), P, I32, P], ctypes.c_int),
+        "lora_base_load": ([P, I32, P, P, P, I32, P], ctypes.c_int),
+        "lora_base": ([P, P, P, P, I32, I32, P], ctypes.c_int),
+        "lora_base_group": ([P, I32, ctypes.POINTER(I32), ctypes.POINTER(P), ctypes.POINTER(P),
+                             ctypes.POINTER(P), I32, P], ctypes.c_int),
+        "lora_base_gated": ([P, I32, I32, P, P, P, P, I32, I32, P], ctypes.c_int),
+        "lora_rotary_init": ([ctypes.POINTER(Rotary), ctypes.POINTER(_RotaryParams)],
+                             ctypes.c_int),
+        "lora_rotary_group": ([P, ctypes.POINTER(Rotary), I32, ctypes.POINTER(I32),
+                               ctypes.POINTER(P), ctypes.POINTER(P), P, I32, P], ctypes.c_int),
         "lora_get_device_flags": ([P, ctypes.POINTER(ctypes.c_uint32)], ctypes.c_int),
         "lora_get_stats": ([P, ctypes.POINTER(_Stats)], ctypes.c_int),
         "lora_profile_begin": ([P, I32], ctypes.c_int),
@@ -346,6 +380,121 @@ def lora_apply_group_fused(ctx, modules: Sequence[int], x: Sequence, y: Sequence
                                                  int(n_tokens), _stream(stream)), ctx)
 
 
+# the frozen part of a layer
+
+def lora_base_load(ctx, module: int, q, scale, zero=None, group_size: int = 128,
+                   bias=None) -> None:
+    """A module's 4-bit base weight: q uint8 [d_out][d_in / 2], scale float32 and zero
+    uint8 (or None: 8) [d_out][groups], bias [d_out] of the ctx dtype or None; pinned
+    host or device tensors.  Device tensors may still be in the making on the current
+    stream of their device: this call waits for it on the host."""
+    import torch
+    for name, t, dtype in (("q", q, torch.uint8), ("scale", scale, torch.float32),
+                           ("zero", zero, torch.uint8), ("bias", bias, None)):
+        if t is None or isinstance(t, int):
+            continue
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.is_cuda:
+            torch.cuda.current_stream(t.device).synchronize()
+    _check(load_library().lora_base_load(ctx, int(module), _ptr(q), _ptr(scale), _ptr(zero),
+                                         int(group_size), _ptr(bias)), ctx)
+
+
+def _add_ptrs(n, add):
+    if add is None:
+        return None
+    if len(add) != n:
+        raise ValueError("add: one tensor or None per module")
+    for t in add:
+        if t is not None:
+            _require_cuda(t, "add")
+    return (ctypes.c_void_p * max(n, 1))(*[_ptr(t) for t in add])
+
+
+def _rows(t, n_tokens):
+    """n_tokens, or the rows of t where none is given."""
+    return int(t.shape[0]) if n_tokens is None else int(n_tokens)
+
+
+def lora_base(ctx, x, y, module: int, add=None, n_tokens: Optional[int] = None,
+              stream=None) -> None:
+    """y = x W^T + bias + add with the module's 4-bit base weight."""
+    for name, t in (("x", x), ("y", y), ("add", add)):
+        if t is not None:
+            _require_cuda(t, name)
+    _check(load_library().lora_base(ctx, _ptr(x), _ptr(add), _ptr(y), _rows(x, n_tokens),
+                                    int(module), _stream(stream)), ctx)
+
+
+def lora_base_group(ctx, modules: Sequence[int], x: Sequence, y: Sequence,
+                    add: Optional[Sequence] = None, n_tokens: Optional[int] = None,
+                    stream=None) -> None:
+    """lora_base for several modules of one batch."""
+    n, mods, xp = _group(modules, x, "x")
+    _, _, yp = _group(modules, y, "y")
+    _check(load_library().lora_base_group(ctx, n, mods, xp, _add_ptrs(n, add), yp,
+                                          _rows(x[0], n_tokens), _stream(stream)), ctx)
+
+
+def _activation(activation) -> int:
+    if isinstance(activation, str):
+        if activation not in ACTIVATIONS:
+            raise ValueError(f"activation {activation!r} is not one of {sorted(ACTIVATIONS)}")
+        return ACTIVATIONS[activation]
+    return int(activation)
+
+
+def lora_base_gated(ctx, gate_module: int, up_module: int, x, y, gate_add=None, up_add=None,
+                    activation="silu", n_tokens: Optional[int] = None, stream=None) -> None:
+    """y = act(x Wg^T + bias_g + gate_add) * (x Wu^T + bias_u + up_add) in one kernel."""
+    for name, t in (("x", x), ("y", y), ("gate_add", gate_add), ("up_add", up_add)):
+        if t is not None:
+            _require_cuda(t, name)
+    _check(load_library().lora_base_gated(ctx, int(gate_module), int(up_module), _ptr(x),
+                                          _ptr(gate_add), _ptr(up_add), _ptr(y),
+                                          _rows(x, n_tokens), _activation(activation),
+                                          _stream(stream)), ctx)
+
+
+def lora_rotary_init(head_dim: int, rotary_dim: Optional[int] = None, layout="half",
+                     base: float = 10000.0, scaling="none", factor: float = 1.0,
+                     original_positions: float = 0.0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, attention_factor: float = 0.0,
+                     low_factor: float = 1.0, high_factor: float = 4.0) -> Rotary:
+    """A model's rotary positions.  layout: "half" or "interleaved"; scaling: "none",
+    "linear", "yarn" or "banded" (the header's formulas).  Needs no device."""
+    for name, value, known in (("layout", layout, ROTARY_LAYOUTS),
+                               ("scaling", scaling, ROTARY_SCALINGS)):
+        if isinstance(value, str) and value not in known:
+            raise ValueError(f"{name} {value!r} is not one of {sorted(known)}")
+    p = _RotaryParams(int(head_dim), int(head_dim if rotary_dim is None else rotary_dim),
+                      ROTARY_LAYOUTS.get(layout, layout), ROTARY_SCALINGS.get(scaling, scaling),
+                      float(base), float(factor), float(original_positions), float(beta_fast),
+                      float(beta_slow), float(attention_factor), float(low_factor),
+                      float(high_factor))
+    out = Rotary()
+    _check(load_library().lora_rotary_init(ctypes.byref(out), ctypes.byref(p)), None)
+    return out
+
+
+def lora_rotary_group(ctx, rotary: Rotary, modules: Sequence[int], x: Sequence, y: Sequence,
+                      positions, n_tokens: Optional[int] = None, stream=None) -> None:
+    """Turn the heads of the modules' outputs x[i] by positions (int32, one a token) into
+    y[i], which may be x[i]."""
+    import torch
+    if n_tokens is None:
+        n_tokens = positions.numel()
+    if n_tokens:
+        _require_cuda(positions, "positions", torch.int32, n_tokens)
+    n, mods, xp = _group(modules, x, "x")
+    _, _, yp = _group(modules, y, "y")
+    _check(load_library().lora_rotary_group(ctx, ctypes.byref(rotary), n, mods, xp, yp,
+                                            _ptr(positions), int(n_tokens), _stream(stream)), ctx)
+
+
 def lora_get_device_flags(ctx) -> int:
     v = ctypes.c_uint32(0)
     _check(load_library().lora_get_device_flags(ctx, ctypes.byref(v)), ctx)
@@ -430,6 +579,111 @@ class Slots:
 
     def apply_group_noalloc(self, modules, x, y, idx, n_tokens=None, stream=None):
         lora_apply_group_noalloc(self.ctx, modules, x, y, idx, n_tokens, stream)
+
+    def load_base(self, module, q, scale, zero=None, group_size=128, bias=None):
+        d_in, d_out = self.modules[module]
+        groups = -(-d_in // (group_size or d_in)) if group_size >= 0 else 1
+        for name, t, shape in (("q", q, (d_out, d_in // 2)), ("scale", scale, (d_out, groups)),
+                               ("zero", zero, (d_out, groups)), ("bias", bias, (d_out,))):
+            if t is not None and not isinstance(t, int) and tuple(t.shape) != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        if bias is not None and not isinstance(bias, int) and bias.dtype != self.torch_dtype():
+            raise ValueError(f"bias has dtype {bias.dtype}, expected {self.torch_dtype()}")
+        lora_base_load(self.ctx, module, q, scale, zero, group_size, bias)
+
+    def torch_dtype(self):
+        import torch
+        return torch.bfloat16 if self.dtype == "bf16" else torch.float32
+
+    def _check_rows(self, name, t, n_tokens, width):
+        if t is not None:
+            _require_cuda(t, name, self.torch_dtype(), n_tokens * width)
+
+    def _check_members(self, modules, x, y, add, n_tokens):
+        for i, m in enumerate(modules):
+            if 0 <= m < len(self.modules) and i < len(x) and i < len(y):
+                self._check_rows("x", x[i], n_tokens, self.modules[m][0])
+                self._check_rows("y", y[i], n_tokens, self.modules[m][1])
+                if add is not None and i < len(add):
+                    self._check_rows("add", add[i], n_tokens, self.modules[m][1])
+
+    def _check_gated(self, gate, up, x, y, gate_add, up_add, n_tokens):
+        if 0 <= gate < len(self.modules):
+            d_in, d_out = self.modules[gate]
+            self._check_rows("x", x, n_tokens, d_in)
+            for name, t in (("y", y), ("gate_add", gate_add), ("up_add", up_add)):
+                self._check_rows(name, t, n_tokens, d_out)
+
+    def _check_rotary(self, modules, x, y, positions, n_tokens):
+        import torch
+        _require_cuda(positions, "positions", torch.int32, n_tokens)
+        for i, m in enumerate(modules):
+            if 0 <= m < len(self.modules) and i < len(x) and i < len(y):
+                self._check_rows("x", x[i], n_tokens, self.modules[m][1])
+                self._check_rows("y", y[i], n_tokens, self.modules[m][1])
+
+    def base(self, x, y, module, add=None, n_tokens=None, stream=None):
+        n = _rows(x, n_tokens)
+        self._check_members([module], [x], [y], [add], n)
+        lora_base(self.ctx, x, y, module, add, n, stream)
+
+    def base_group(self, modules, x, y, add=None, n_tokens=None, stream=None):
+        n = _rows(x[0], n_tokens)
+        self._check_members(modules, x, y, add, n)
+        lora_base_group(self.ctx, modules, x, y, add, n, stream)
+
+    def base_gated(self, gate_module, up_module, x, y, gate_add=None, up_add=None,
+                   activation="silu", n_tokens=None, stream=None):
+        n = _rows(x, n_tokens)
+        self._check_gated(gate_module, up_module, x, y, gate_add, up_add, n)
+        lora_base_gated(self.ctx, gate_module, up_module, x, y, gate_add, up_add, activation, n,
+                        stream)
+
+    def rotary_group(self, rotary, modules, x, y, positions, n_tokens=None, stream=None):
+        n = positions.numel() if n_tokens is None else int(n_tokens)
+        self._check_rotary(modules, x, y, positions, n)
+        lora_rotary_group(self.ctx, rotary, modules, x, y, positions, n, stream)
+
+    def _bound(self, fn, args, refs):
+        """A function that makes the library call fn(ctx, *args), whose arguments `refs`
+        keep alive."""
+        def call():
+            _ = refs
+            rc = fn(self.ctx, *args)
+            if rc:
+                _check(rc, self.ctx)
+        return call
+
+    def bind_base(self, modules, x, y, add=None, n_tokens=None, stream=None):
+        """base_group with its arguments marshalled once, as bind_step does: returns a
+        function that makes the library call."""
+        n_tok = _rows(x[0], n_tokens)
+        self._check_members(modules, x, y, add, n_tok)
+        n, mods, xp = _group(modules, x, "x")
+        _, _, yp = _group(modules, y, "y")
+        return self._bound(load_library().lora_base_group,
+                           (n, mods, xp, _add_ptrs(n, add), yp, n_tok, _stream(stream)),
+                           (x, y, add))
+
+    def bind_gated(self, gate_module, up_module, x, y, gate_add=None, up_add=None,
+                   activation="silu", n_tokens=None, stream=None):
+        """base_gated with its arguments marshalled once."""
+        n_tok = _rows(x, n_tokens)
+        self._check_gated(gate_module, up_module, x, y, gate_add, up_add, n_tok)
+        return self._bound(load_library().lora_base_gated,
+                           (int(gate_module), int(up_module), _ptr(x), _ptr(gate_add), _ptr(up_add),
+                            _ptr(y), n_tok, _activation(activation), _stream(stream)),
+                           (x, y, gate_add, up_add))
+
+    def bind_rotary(self, rotary, modules, x, y, positions, n_tokens=None, stream=None):
+        """rotary_group with its arguments marshalled once."""
+        n_tok = positions.numel() if n_tokens is None else int(n_tokens)
+        self._check_rotary(modules, x, y, positions, n_tok)
+        n, mods, xp = _group(modules, x, "x")
+        _, _, yp = _group(modules, y, "y")
+        return self._bound(load_library().lora_rotary_group,
+                           (ctypes.byref(rotary), n, mods, xp, yp, _ptr(positions), n_tok,
+                            _stream(stream)), (rotary, x, y, positions))
 
     def bind_step(self, groups, idx, stream=None, prepare=True, fused=False):
         """One step with its arguments marshalled once: lora_plan_prepare of idx

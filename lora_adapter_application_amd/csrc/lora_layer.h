@@ -1,0 +1,93 @@
+// lora_layer.h -- launch interface between the host side (lora_layer.cpp) and
+// the kernels of a layer's frozen part: the 4-bit base product and its gated
+// form (lora_base.hip), and rotary positions (lora_rotary.hip).  Not installed;
+// not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "lora_internal.h"
+
+namespace lora {
+
+// ---------------------------------------------------------------------------
+// 4-bit base weights
+//
+// A weight block is 16 output columns x 128 inputs, 1 KB: lane l = 16 g + n of
+// the wave that reads it holds column n, inputs 32 j + 8 g .. + 7 in its word
+// j = 0..3, the order in which v_mfma_f32_16x16x32_bf16 takes its right operand.
+// A word holds the even inputs in nibbles 0..3 and the odd ones in nibbles 4..7,
+// so that one mask gives a pair of neighbours in the halves of a register.
+// Blocks are stored column block by column block, their K blocks in order.
+// Beside each block stand the scales of its columns, `spb` per block and column
+// (a group of 32 or 64 inputs has 4 or 2, every longer one 1): in a bf16 ctx one
+// 32-bit word, the scale's upper 24 bits (16 significant bits, exact for scales
+// that came from 16-bit floats) over the byte 16 + zero; in an fp32 ctx two
+// floats, the scale and 16 + zero.  Columns past d_out and groups past d_in have
+// scale 0.
+constexpr int kBaseCols = 16;
+constexpr int kBaseK = 128;
+
+struct BasePack {
+    uint32_t *q = nullptr;       // [col blocks][K blocks][64][4]
+    void *sc = nullptr;          // [col blocks][K blocks][16][spb] words (fp32: pairs of floats)
+    void *bias = nullptr;        // [d_out], ctx dtype
+    int32_t spb = 0;             // 0: no weight loaded
+    int32_t sc_room = 0;         // the spb that sc has room for
+    bool has_bias = false;
+};
+
+struct BasePackArgs {
+    const uint8_t *q;            // rows x d_in / 2
+    const float *scale;          // rows x groups
+    const uint8_t *zero;         // rows x groups, or null (8)
+    uint32_t *q_out;             // the first of the rows' column blocks
+    void *sc_out;
+    int32_t rows;                // rows given; the rest of the last column block is padding
+    int32_t d_in, group, groups, spb;
+};
+hipError_t launch_base_pack(bool bf16, const BasePackArgs &a, hipStream_t st);
+
+struct BaseMember {
+    const uint32_t *q;
+    const void *sc;
+    const void *bias;            // or null
+    const void *x;               // [T][d_in]
+    const void *add;             // [T][d_out] or null
+    void *y;                     // [T][d_out]
+    int32_t d_in, d_out;
+    int32_t kb;                  // K blocks
+};
+
+struct BaseArgs {
+    BaseMember m[kMaxGroup];     // gated: m[0] gate, m[1] up, y in m[0]
+    int32_t col_start[kMaxGroup + 1];   // column blocks of the members before member i
+    int32_t n;
+    int32_t T;
+    int32_t act;                 // gated: LORA_ACT_*
+};
+// All members share spb.
+hipError_t launch_base(bool bf16, bool gated, int spb, const BaseArgs &a, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// rotary positions
+
+struct RotaryMember {
+    const void *x;
+    void *y;
+    int32_t heads;
+    int32_t width;               // heads * head_dim
+};
+
+struct RotaryArgs {
+    lora_rotary rot;
+    RotaryMember m[kMaxGroup];
+    int32_t n;
+    int32_t T;
+    int32_t total_heads;
+    const int32_t *positions;
+};
+hipError_t launch_rotary(bool bf16, bool vec, const RotaryArgs &a, hipStream_t st);
+
+}  // namespace lora
