@@ -357,10 +357,324 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
     }
 }
 
+// ---------------------------------------------------------------------------
+// products of many tokens
+//
+// One workgroup = 16 MT MW tokens x 4 waves of 64 columns (GATED: of 32 of gate
+// and the same 32 of up), MW waves above each other.  x is staged in LDS one K
+// block at a time and shared by the four column waves; each wave unpacks its own
+// weights straight from global memory into the registers its products read.
+//
+// A group's sum starts at -z' sum x instead of 0, so the zero points cost nothing
+// where every column has the same (ZERO false), and one multiplication per sum
+// and group where they differ.  The sums of x themselves are formed once per
+// workgroup, one K block ahead: wave w multiplies token block w of the next K
+// block by ones and leaves the result in LDS.
+//
+// Block k reads stage k % 3, sums stage (k + 1) % 3 and fills stage (k + 2) % 3,
+// which block k - 1 has read; one barrier a block.  16-byte piece p of stage row r
+// sits in slot p ^ (r & 15), so the 16 rows of an operand read fall on distinct
+// banks.
+constexpr int kTileWaveCols = 64;
+
+template <typename XT> struct Staged;      // eight inputs of a token on their way to LDS
+template <> struct Staged<uint16_t> {
+    u32x4 v;
+    __device__ __forceinline__ void load(const uint16_t *src, bool in)
+    {
+        __builtin_memcpy(&v, src, 16);
+        if (!in)
+            v = u32x4{0, 0, 0, 0};
+    }
+};
+template <> struct Staged<float> {
+    float v[8];
+    __device__ __forceinline__ void load(const float *src, bool in)
+    {
+        __builtin_memcpy(v, src, 32);
+        if (!in)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = 0.f;
+    }
+};
+
+template <typename XT, int MT, int MW, int SPB, bool GATED, bool ZERO>
+__global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(BaseArgs a)
+{
+    typedef typename Scale<XT>::word word;
+    constexpr int PIECES = XFrag<XT>::PIECES;
+    constexpr int P = GATED ? 2 : 1;
+    constexpr int NT = 4;                         // column blocks per wave, gate's first
+    constexpr int BM = 16 * MT * MW;
+    constexpr int NK = 4 / SPB;                   // MFMA steps per group of a block
+    __shared__ __attribute__((aligned(16))) uint16_t xs[3][PIECES][BM * kBaseK];
+    __shared__ __attribute__((aligned(16))) float sums[2][SPB][BM];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave & 3, wm = wave >> 2;
+    const int row = lane & 15, g = lane >> 4;
+
+    // work item -> (column tile, token tile): an XCD takes a contiguous run of items,
+    // which go through 8 token tiles of a column tile before the next column tile, so
+    // the items it runs together share x and W in its L2
+    const int per_xcd = gridDim.x >> 3;
+    const int item = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+    if (item >= a.items)
+        return;
+    const int t_tiles = (a.T + BM - 1) / BM;
+    const int c_tiles = a.tile_start[GATED ? 1 : a.n];
+    const int band = item / (8 * c_tiles), in = item - band * 8 * c_tiles;
+    const int high = min(8, t_tiles - band * 8);
+    int c_tile = in / high;
+    const int t0 = (band * 8 + in - c_tile * high) * BM;
+    int mi = 0;
+    if constexpr (!GATED)
+        while (mi + 1 < a.n && c_tile >= a.tile_start[mi + 1])
+            ++mi;
+    c_tile -= a.tile_start[mi];
+    const BaseMember &m = a.m[mi];
+    const int KB = m.kb, d_in = m.d_in, d_out = m.d_out;
+    const int nblocks = (d_out + kBaseCols - 1) / kBaseCols;
+
+    // column blocks of this wave (past the last one: that one again, not stored)
+    const uint32_t *q[NT];
+    const word *sc[NT];
+    int nb[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int b = GATED ? c_tile * 8 + wn * 2 + (n & 1) : c_tile * 16 + wn * 4 + n;
+        nb[n] = b;
+        const int64_t at = (int64_t)min(b, nblocks - 1) * KB;
+        const BaseMember &mp = GATED ? a.m[n >> 1] : m;
+        q[n] = mp.q + (at * 64 + lane) * 4;
+        sc[n] = (const word *)mp.sc + (at * 16 + row) * SPB;
+    }
+
+    // staging: this thread's piece of MT rows
+    const int piece = tid & 15, srow = tid >> 4;
+    const XT *src[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        src[i] = (const XT *)m.x + (int64_t)min(t0 + srow + i * 16 * MW, a.T - 1) * d_in;
+    Staged<XT> st[MT];
+    auto load_x = [&](int kb) __attribute__((always_inline)) {
+        const int k = kb * kBaseK + piece * 8;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            st[i].load(src[i] + min(k, d_in - 8), k < d_in);
+    };
+    auto store_x = [&](int stage) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const int r = srow + i * 16 * MW;
+            const int at = r * kBaseK + ((piece ^ (r & 15)) << 3);
+            if constexpr (PIECES == 1) {
+                *(u32x4 *)&xs[stage][0][at] = st[i].v;
+            } else {
+                bf16x8 p[3];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float f = st[i].v[e];
+                    const __bf16 hi = (__bf16)f;
+                    const float rest = f - (float)hi;      // exact
+                    const __bf16 mid = (__bf16)rest;
+                    p[0][e] = hi;
+                    p[1][e] = mid;
+                    p[2][e] = (__bf16)(rest - (float)mid);
+                }
+#pragma unroll
+                for (int c = 0; c < PIECES; ++c)
+                    *(bf16x8 *)&xs[stage][c][at] = p[c];
+            }
+        }
+    };
+    auto x_frag = [&](int stage, int c, int r0, int j) __attribute__((always_inline)) {
+        const int r = r0 + row;
+        return *(const bf16x8 *)&xs[stage][c][r * kBaseK + (((j * 4 + g) ^ row) << 3)];
+    };
+    const u32x4 ones_bits = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, ones_bits);
+    // -sum x (ZERO) or -24 sum x of this wave's token block, for block kb in `stage`
+    auto sum_x = [&](int stage, int kb) __attribute__((always_inline)) {
+        if (wn >= MT)
+            return;
+        const int r0 = (wm * MT + wn) * 16;
+#pragma unroll
+        for (int sub = 0; sub < SPB; ++sub) {
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = sub * NK; j < (sub + 1) * NK; ++j)
+#pragma unroll
+                for (int c = PIECES - 1; c >= 0; --c)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x_frag(stage, c, r0, j), ones, acc, 0, 0, 0);
+            if (row == 0)
+                *(f32x4 *)&sums[kb & 1][sub][r0 + 4 * g] = acc * (ZERO ? -1.f : -24.f);
+        }
+    };
+
+    f32x4 tot[MT][NT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            tot[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    u32x4 wq[NT];
+    word ws[NT][SPB];
+    auto load_w = [&](int kb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            wq[n] = *(const u32x4 *)(q[n] + (int64_t)kb * 256);
+#pragma unroll
+            for (int b = 0; b < SPB; ++b)
+                ws[n][b] = sc[n][(int64_t)kb * 16 * SPB + b];
+        }
+    };
+
+    load_x(0);
+    load_w(0);
+    store_x(0);
+    if (KB > 1) {
+        load_x(1);
+        store_x(1);
+    }
+    __syncthreads();
+    sum_x(0, 0);
+    if (KB > 2)
+        load_x(2);
+    __syncthreads();
+
+    int cur = 0;                                  // stage of block k
+    for (int k = 0; k < KB; ++k) {
+        const int next = cur == 2 ? 0 : cur + 1, fill = next == 2 ? 0 : next + 1;
+        bf16x8 w[NT][4];
+        float s[NT][SPB], z[NT][SPB];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[n][j] = unpack(wq[n][j]);
+#pragma unroll
+            for (int b = 0; b < SPB; ++b) {
+                s[n][b] = Scale<XT>::scale(ws[n][b]);
+                z[n][b] = ZERO ? Scale<XT>::zero(ws[n][b]) : 0.f;
+            }
+        }
+        load_w(min(k + 1, KB - 1));
+        if (k + 2 < KB)
+            store_x(fill);
+        if (k + 3 < KB)
+            load_x(k + 3);
+        if (k + 1 < KB)
+            sum_x(next, k + 1);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const int r0 = (wm * MT + mt) * 16;
+#pragma unroll
+            for (int sub = 0; sub < SPB; ++sub) {
+                const f32x4 c0 = *(const f32x4 *)&sums[k & 1][sub][r0 + 4 * g];
+                f32x4 acc[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[n] = ZERO ? c0 * z[n][sub] : c0;
+#pragma unroll
+                for (int j = sub * NK; j < (sub + 1) * NK; ++j)
+#pragma unroll
+                    for (int c = PIECES - 1; c >= 0; --c) {
+                        const bf16x8 x = x_frag(cur, c, r0, j);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[n][j], acc[n], 0, 0, 0);
+                    }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        tot[mt][n][r] = fmaf(s[n][sub], acc[n][r], tot[mt][n][r]);
+            }
+        }
+        __syncthreads();
+        cur = next;
+    }
+
+    // lane l holds tokens 4 (l / 16) .. + 3 of column l % 16 of each block
+#pragma unroll
+    for (int n = 0; n < NT / P; ++n) {
+        const int col = nb[n] * kBaseCols + row;
+        if (nb[n] >= nblocks || col >= d_out)
+            continue;
+        float bias[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const BaseMember &mp = GATED ? a.m[p] : m;
+            bias[p] = mp.bias ? to_f32<XT>(((const XT *)mp.bias)[col]) : 0.f;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = t0 + (wm * MT + mt) * 16 + 4 * g + r;
+                if (t >= a.T)
+                    continue;
+                const int64_t at = (int64_t)t * d_out + col;
+                float v[P];
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const BaseMember &mp = GATED ? a.m[p] : m;
+                    float sum = tot[mt][n + p * (NT / P)][r];
+                    if (!(fabsf(sum) < __builtin_inff()))
+                        sum = plain_sum<XT, SPB>((const XT *)m.x + (int64_t)t * d_in,
+                                                 mp.q + (int64_t)nb[n] * KB * 256,
+                                                 (const word *)mp.sc + (int64_t)nb[n] * KB * 16 * SPB,
+                                                 row, d_in);
+                    if (mp.bias)
+                        sum += bias[p];
+                    if (mp.add)
+                        sum += to_f32<XT>(((const XT *)mp.add)[at]);
+                    v[p] = sum;
+                }
+                float out = v[0];
+                if constexpr (GATED)
+                    out = activate(v[0], a.act) * v[P - 1];
+                ((XT *)m.y)[at] = from_f32<XT>(out);
+            }
+    }
+}
+
+template <typename XT, bool GATED, int SPB, int MT, int MW>
+hipError_t launch_tile(const BaseArgs &args, hipStream_t st)
+{
+    BaseArgs a = args;
+    const int cols = GATED ? 8 : 16;              // column blocks of a workgroup
+    bool zero = false;
+    a.tile_start[0] = 0;
+    for (int i = 0; i < a.n; ++i) {
+        a.tile_start[i + 1] = a.tile_start[i] + ((a.m[i].d_out + 15) / 16 + cols - 1) / cols;
+        zero = zero || a.m[i].zero;
+    }
+    a.items = a.tile_start[GATED ? 1 : a.n] * ((a.T + 16 * MT * MW - 1) / (16 * MT * MW));
+    const int grid = (a.items + 7) / 8 * 8;
+    if (zero)
+        base_tile_kernel<XT, MT, MW, SPB, GATED, true><<<grid, 256 * MW, 0, st>>>(a);
+    else
+        base_tile_kernel<XT, MT, MW, SPB, GATED, false><<<grid, 256 * MW, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+constexpr int kFewTokens = 64;
+
 template <typename XT, bool GATED, int SPB>
-hipError_t launch_few(const BaseArgs &a, hipStream_t st)
+hipError_t launch_sized(const BaseArgs &a, hipStream_t st)
 {
     const int cols = a.col_start[GATED ? 1 : a.n];
+    if (a.T > kFewTokens) {
+        if constexpr (sizeof(XT) == 2)
+            return launch_tile<XT, GATED, SPB, 4, 1>(a, st);
+        else
+            return launch_tile<XT, GATED, SPB, 2, 1>(a, st);
+    }
     constexpr int W = 8;
     constexpr int MT = sizeof(XT) == 4 || GATED ? 2 : 4;
     if (a.T <= 16)
@@ -375,9 +689,9 @@ template <typename XT, bool GATED>
 hipError_t launch_spb(int spb, const BaseArgs &a, hipStream_t st)
 {
     switch (spb) {
-    case 1: return launch_few<XT, GATED, 1>(a, st);
-    case 2: return launch_few<XT, GATED, 2>(a, st);
-    default: return launch_few<XT, GATED, 4>(a, st);
+    case 1: return launch_sized<XT, GATED, 1>(a, st);
+    case 2: return launch_sized<XT, GATED, 2>(a, st);
+    default: return launch_sized<XT, GATED, 4>(a, st);
     }
 }
 

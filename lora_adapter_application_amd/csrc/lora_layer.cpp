@@ -85,6 +85,7 @@ BaseMember base_member(const lora_ctx *c, int32_t module, const void *x, const v
     m.d_in = sh.d_in;
     m.d_out = sh.d_out;
     m.kb = ceil_div(sh.d_in, kBaseK);
+    m.zero = p.zero;
     return m;
 }
 
@@ -218,6 +219,7 @@ int lora_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *sc
     ctx->load_gen += 1;
     p.spb = spb;
     p.has_bias = bias != nullptr;
+    p.zero = zero != nullptr;
     return LORA_OK;
 }
 

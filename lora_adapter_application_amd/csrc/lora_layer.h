@@ -36,6 +36,7 @@ struct BasePack {
     int32_t spb = 0;             // 0: no weight loaded
     int32_t sc_room = 0;         // the spb that sc has room for
     bool has_bias = false;
+    bool zero = false;           // loaded with zero points (else all are 8)
 };
 
 struct BasePackArgs {
@@ -58,11 +59,14 @@ struct BaseMember {
     void *y;                     // [T][d_out]
     int32_t d_in, d_out;
     int32_t kb;                  // K blocks
+    int32_t zero;                // some zero point is not 8
 };
 
 struct BaseArgs {
     BaseMember m[kMaxGroup];     // gated: m[0] gate, m[1] up, y in m[0]
     int32_t col_start[kMaxGroup + 1];   // column blocks of the members before member i
+    int32_t tile_start[kMaxGroup + 1];  // many tokens: column tiles of the members before member i
+    int32_t items;                      // and work items (set by the launch)
     int32_t n;
     int32_t T;
     int32_t act;                 // gated: LORA_ACT_*
