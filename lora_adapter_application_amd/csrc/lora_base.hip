@@ -28,6 +28,7 @@ namespace {
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
@@ -73,7 +74,7 @@ __global__ __launch_bounds__(256) void base_pack_q_kernel(BasePackArgs a)
             r |= ((w >> (8 * e)) & 15u) << (4 * e);               // input 2e
             r |= ((w >> (8 * e + 4)) & 15u) << (4 * (e + 4));     // input 2e + 1
         }
-        out[j] = r;
+        out[j] = (r << 3) | (r >> 29);
     }
     *(u32x4 *)(a.q_out + i * 4) = out;
 }
@@ -113,14 +114,37 @@ __global__ __launch_bounds__(256) void base_pack_scale_kernel(BasePackArgs a)
 // ---------------------------------------------------------------------------
 // pieces of the products
 
-__device__ __forceinline__ bf16x8 unpack(uint32_t w)
+// `bytes` bytes from a wave-uniform address as a buffer: a load of it takes its
+// address from scalar registers and one 32-bit offset, and reads 0 past the end.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, uint32_t bytes)
 {
-    const uint32_t mask = 0x00780078u, one = 0x41804180u;
+    const uint64_t at = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)at);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+    return __builtin_amdgcn_make_buffer_rsrc((void *)((uint64_t)hi << 32 | lo), 0,
+                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+
+// The eight weights of a word as bf16 numbers 16 + q.  mask and one are 0x00780078
+// and 0x41804180 in registers (hold_constants): as literals the and and the or would
+// be two instructions.
+struct Constants {
+    uint32_t mask, one;
+};
+__device__ __forceinline__ Constants hold_constants()
+{
+    Constants c = {0x00780078u, 0x41804180u};
+    asm("" : "+s"(c.mask));
+    asm("" : "+v"(c.one));
+    return c;
+}
+__device__ __forceinline__ bf16x8 unpack(uint32_t w, const Constants &c)
+{
     u32x4 r;
-    r[0] = ((w << 3) & mask) | one;
-    r[1] = ((w >> 1) & mask) | one;
-    r[2] = ((w >> 5) & mask) | one;
-    r[3] = ((w >> 9) & mask) | one;
+    r[0] = (w & c.mask) | c.one;
+    r[1] = ((w >> 4) & c.mask) | c.one;
+    r[2] = ((w >> 8) & c.mask) | c.one;
+    r[3] = (__builtin_rotateright32(w, 12) & c.mask) | c.one;
     return __builtin_bit_cast(bf16x8, r);
 }
 
@@ -199,7 +223,7 @@ __device__ __noinline__ float plain_sum(const XT *x, const uint32_t *q, const ty
     for (int k = 0; k < d_in; ++k) {
         const int kb = k >> 7, j = (k >> 5) & 3, g = (k >> 3) & 3, i = k & 7;
         const uint32_t w = q[(int64_t)kb * 256 + (g * 16 + n) * 4 + j];
-        const float v = (float)((w >> (4 * ((i & 1) * 4 + (i >> 1)))) & 15u);
+        const float v = (float)(__builtin_rotateright32(w, 3 + 4 * ((i & 1) * 4 + (i >> 1))) & 15u);
         const typename Scale<XT>::word s = sc[((int64_t)kb * 16 + n) * SPB + ((k & 127) * SPB >> 7)];
         sum += to_f32<XT>(x[k]) * ((v + 16.f - Scale<XT>::zero(s)) * Scale<XT>::scale(s));
     }
@@ -251,6 +275,7 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
             tot[p][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
     const u32x4 ones_bits = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
     const bf16x8 ones = __builtin_bit_cast(bf16x8, ones_bits);
+    const Constants con = hold_constants();
 
     for (int kb0 = wave; kb0 < KB; kb0 += W * U) {
         u32x4 wq[U][P];
@@ -293,7 +318,7 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
                 bf16x8 b[P];
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    b[p] = unpack(wq[u][p][j]);
+                    b[p] = unpack(wq[u][p][j], con);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -380,22 +405,22 @@ constexpr int kTileWaveCols = 64;
 template <typename XT> struct Staged;      // eight inputs of a token on their way to LDS
 template <> struct Staged<uint16_t> {
     u32x4 v;
-    __device__ __forceinline__ void load(const uint16_t *src, bool in)
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t src, uint32_t off)
     {
-        __builtin_memcpy(&v, src, 16);
-        if (!in)
-            v = u32x4{0, 0, 0, 0};
+        v = __builtin_amdgcn_raw_buffer_load_b128(src, off, 0, 0);
     }
 };
 template <> struct Staged<float> {
     float v[8];
-    __device__ __forceinline__ void load(const float *src, bool in)
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t src, uint32_t off)
     {
-        __builtin_memcpy(v, src, 32);
-        if (!in)
+        const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(src, off, 0, 0);
+        const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(src, off, 16, 0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __uint_as_float(lo[i]);
+            v[i + 4] = __uint_as_float(hi[i]);
+        }
     }
 };
 
@@ -408,6 +433,7 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
     constexpr int NT = 4;                         // column blocks per wave, gate's first
     constexpr int BM = 16 * MT * MW;
     constexpr int NK = 4 / SPB;                   // MFMA steps per group of a block
+    constexpr uint32_t kScBytes = 16 * SPB * sizeof(word);   // scales of a weight block
     __shared__ __attribute__((aligned(16))) uint16_t xs[3][PIECES][BM * kBaseK];
     __shared__ __attribute__((aligned(16))) float sums[2][SPB][BM];
 
@@ -427,8 +453,8 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
     const int c_tiles = a.tile_start[GATED ? 1 : a.n];
     const int band = item / (8 * c_tiles), in = item - band * 8 * c_tiles;
     const int high = min(8, t_tiles - band * 8);
-    int c_tile = in / high;
-    const int t0 = (band * 8 + in - c_tile * high) * BM;
+    int c_tile = __builtin_amdgcn_readfirstlane(in / high);
+    const int t0 = __builtin_amdgcn_readfirstlane((band * 8 + in - c_tile * high) * BM);
     int mi = 0;
     if constexpr (!GATED)
         while (mi + 1 < a.n && c_tile >= a.tile_start[mi + 1])
@@ -439,8 +465,7 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
     const int nblocks = (d_out + kBaseCols - 1) / kBaseCols;
 
     // column blocks of this wave (past the last one: that one again, not stored)
-    const uint32_t *q[NT];
-    const word *sc[NT];
+    __amdgpu_buffer_rsrc_t q[NT], sc[NT];
     int nb[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -448,27 +473,34 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
         nb[n] = b;
         const int64_t at = (int64_t)min(b, nblocks - 1) * KB;
         const BaseMember &mp = GATED ? a.m[n >> 1] : m;
-        q[n] = mp.q + (at * 64 + lane) * 4;
-        sc[n] = (const word *)mp.sc + (at * 16 + row) * SPB;
+        q[n] = buffer((const char *)mp.q + at * 1024, (uint32_t)KB * 1024u);
+        sc[n] = buffer((const char *)mp.sc + at * kScBytes, (uint32_t)KB * kScBytes);
     }
+    const uint32_t q_off = lane * 16, sc_off = row * (uint32_t)(SPB * sizeof(word));
 
-    // staging: this thread's piece of MT rows
+    // staging: this thread's piece of MT rows, as offsets from the tile's first row
     const int piece = tid & 15, srow = tid >> 4;
-    const XT *src[MT];
+    const uint32_t rows = (uint32_t)min(BM, a.T - t0);
+    const auto x0 = buffer((const XT *)m.x + (int64_t)t0 * d_in, rows * (uint32_t)d_in * (uint32_t)sizeof(XT));
+    uint32_t src[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-        src[i] = (const XT *)m.x + (int64_t)min(t0 + srow + i * 16 * MW, a.T - 1) * d_in;
-    Staged<XT> st[MT];
-    auto load_x = [&](int kb) __attribute__((always_inline)) {
+        src[i] = (uint32_t)(srow + i * 16 * MW) * (uint32_t)d_in * (uint32_t)sizeof(XT);
+    // half of the rows at a time, which is half of the registers
+    constexpr int HT = MT / 2;
+    Staged<XT> st[HT];
+    auto load_x = [&](int kb, int half) __attribute__((always_inline)) {
         const int k = kb * kBaseK + piece * 8;
+        // inputs past d_in read 0, as rows past the batch do: an offset past the buffer
+        const uint32_t at = k < d_in ? (uint32_t)k * (uint32_t)sizeof(XT) : 0x80000000u;
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-            st[i].load(src[i] + min(k, d_in - 8), k < d_in);
+        for (int i = 0; i < HT; ++i)
+            st[i].load(x0, src[half * HT + i] + at);
     };
-    auto store_x = [&](int stage) __attribute__((always_inline)) {
+    auto store_x = [&](int stage, int half) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int r = srow + i * 16 * MW;
+        for (int i = 0; i < HT; ++i) {
+            const int r = srow + (half * HT + i) * 16 * MW;
             const int at = r * kBaseK + ((piece ^ (r & 15)) << 3);
             if constexpr (PIECES == 1) {
                 *(u32x4 *)&xs[stage][0][at] = st[i].v;
@@ -526,24 +558,40 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
     auto load_w = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            wq[n] = *(const u32x4 *)(q[n] + (int64_t)kb * 256);
+            wq[n] = __builtin_amdgcn_raw_buffer_load_b128(q[n], lane * 16, kb * 1024, 0);
+            constexpr int W32 = SPB * (int)sizeof(word) / 4;      // 32-bit words per column
+            uint32_t v[W32];
 #pragma unroll
-            for (int b = 0; b < SPB; ++b)
-                ws[n][b] = sc[n][(int64_t)kb * 16 * SPB + b];
+            for (int b = 0; b < W32; b += 4) {
+                const int off = row * W32 * 4 + b * 4, at = kb * (int)kScBytes;
+                if constexpr (W32 == 1) {
+                    v[0] = __builtin_amdgcn_raw_buffer_load_b32(sc[n], off, at, 0);
+                } else if constexpr (W32 == 2) {
+                    const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(sc[n], off, at, 0);
+                    v[0] = t[0], v[1] = t[1];
+                } else {
+                    const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(sc[n], off, at, 0);
+                    v[b] = t[0], v[b + 1] = t[1], v[b + 2] = t[2], v[b + 3] = t[3];
+                }
+            }
+            __builtin_memcpy(ws[n], v, sizeof v);
         }
     };
+    const Constants con = hold_constants();
 
-    load_x(0);
     load_w(0);
-    store_x(0);
-    if (KB > 1) {
-        load_x(1);
-        store_x(1);
-    }
+    // blocks past the last one are read as zeros, staged and never multiplied, so that
+    // the loop has no branches
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            load_x(kb, half);
+            store_x(kb, half);
+        }
     __syncthreads();
     sum_x(0, 0);
-    if (KB > 2)
-        load_x(2);
+    load_x(2, 0);
     __syncthreads();
 
     int cur = 0;                                  // stage of block k
@@ -555,7 +603,7 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                w[n][j] = unpack(wq[n][j]);
+                w[n][j] = unpack(wq[n][j], con);
 #pragma unroll
             for (int b = 0; b < SPB; ++b) {
                 s[n][b] = Scale<XT>::scale(ws[n][b]);
@@ -563,37 +611,50 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
             }
         }
         load_w(min(k + 1, KB - 1));
-        if (k + 2 < KB)
-            store_x(fill);
-        if (k + 3 < KB)
-            load_x(k + 3);
-        if (k + 1 < KB)
-            sum_x(next, k + 1);
+        store_x(fill, 0);
+        load_x(k + 2, 1);
+        sum_x(next, k + 1);
+        // one group of one token block after the other, its x read a step ahead
+        constexpr int STEPS = MT * SPB;
+        bf16x8 x[2][NK][PIECES];
+        f32x4 c0[2];
+        auto read_x = [&](int step) __attribute__((always_inline)) {
+            const int r0 = (wm * MT + step / SPB) * 16, sub = step % SPB;
+            c0[step & 1] = *(const f32x4 *)&sums[k & 1][sub][r0 + 4 * g];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            const int r0 = (wm * MT + mt) * 16;
+            for (int j = 0; j < NK; ++j)
 #pragma unroll
-            for (int sub = 0; sub < SPB; ++sub) {
-                const f32x4 c0 = *(const f32x4 *)&sums[k & 1][sub][r0 + 4 * g];
-                f32x4 acc[NT];
+                for (int c = 0; c < PIECES; ++c)
+                    x[step & 1][j][c] = x_frag(cur, c, r0, sub * NK + j);
+        };
+        read_x(0);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    acc[n] = ZERO ? c0 * z[n][sub] : c0;
-#pragma unroll
-                for (int j = sub * NK; j < (sub + 1) * NK; ++j)
-#pragma unroll
-                    for (int c = PIECES - 1; c >= 0; --c) {
-                        const bf16x8 x = x_frag(cur, c, r0, j);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w[n][j], acc[n], 0, 0, 0);
-                    }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        tot[mt][n][r] = fmaf(s[n][sub], acc[n][r], tot[mt][n][r]);
+        for (int step = 0; step < STEPS; ++step) {
+            __builtin_amdgcn_sched_barrier(0xf);      // memory operations stay in their step
+            const int mt = step / SPB, sub = step % SPB;
+            if (step + 1 < STEPS)
+                read_x(step + 1);
+            if (step == STEPS / 2) {
+                store_x(fill, 1);
+                load_x(k + 3, 0);
             }
+            f32x4 acc[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                acc[n] = ZERO ? c0[step & 1] * z[n][sub] : c0[step & 1];
+#pragma unroll
+            for (int j = 0; j < NK; ++j)
+#pragma unroll
+                for (int c = PIECES - 1; c >= 0; --c)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[step & 1][j][c], w[n][sub * NK + j],
+                                                                         acc[n], 0, 0, 0);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    tot[mt][n][r] = fmaf(s[n][sub], acc[n][r], tot[mt][n][r]);
         }
         __syncthreads();
         cur = next;
