@@ -20,6 +20,7 @@
 // what plain arithmetic gives.
 #include <hip/hip_runtime.h>
 
+#include "lora_dma.h"
 #include "lora_layer.h"
 
 namespace lora {
@@ -65,9 +66,15 @@ __global__ __launch_bounds__(256) void base_pack_q_kernel(BasePackArgs a)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int k = kb * kBaseK + j * 32 + (lane >> 4) * 8;
-        if (row >= a.rows || k >= a.d_in)
-            continue;
-        const uint32_t w = *(const uint32_t *)(a.q + (int64_t)row * (a.d_in / 2) + k / 2);
+        uint32_t w = 0;
+        if (row < a.rows && k < a.d_in) {
+            w = *(const uint32_t *)(a.q + (int64_t)row * (a.d_in / 2) + k / 2);
+        } else if (row < a.rows) {
+            // inputs past d_in: the zero point of their group, so that whatever a kernel
+            // multiplies them with cancels
+            const int64_t last = (int64_t)row * a.groups + min(k / a.group, a.groups - 1);
+            w = (a.zero ? a.zero[last] & 15u : 8u) * 0x11111111u;
+        }
         uint32_t r = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -160,48 +167,8 @@ template <> struct Scale<float> {
     static __device__ __forceinline__ float zero(word w) { return w.y; }
 };
 
-// Eight neighbouring inputs of a token as PIECES bf16 operands.
-template <typename XT> struct XFrag;
-template <> struct XFrag<uint16_t> {
-    static constexpr int PIECES = 1;
-    bf16x8 p[1];
-    __device__ __forceinline__ void load(const uint16_t *src, bool in)
-    {
-        u32x4 v;
-        __builtin_memcpy(&v, src, 16);
-        if (!in)
-            v = u32x4{0, 0, 0, 0};
-        p[0] = __builtin_bit_cast(bf16x8, v);
-    }
-};
-template <> struct XFrag<float> {
-    static constexpr int PIECES = 3;
-    bf16x8 p[3];
-    __device__ __forceinline__ void load(const float *src, bool in)
-    {
-        float v[8];
-        __builtin_memcpy(v, src, 32);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float f = in ? v[i] : 0.f;
-            const __bf16 hi = (__bf16)f;
-            const float r = f - (float)hi;      // exact
-            const __bf16 mid = (__bf16)r;
-            p[0][i] = hi;
-            p[1][i] = mid;
-            p[2][i] = (__bf16)(r - (float)mid);
-        }
-    }
-};
-
-template <typename XT>
-__device__ __forceinline__ f32x4 mma(const XFrag<XT> &x, bf16x8 w, f32x4 acc)
-{
-#pragma unroll
-    for (int i = XFrag<XT>::PIECES - 1; i >= 0; --i)      // small pieces first
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.p[i], w, acc, 0, 0, 0);
-    return acc;
-}
+// bf16 numbers that an input is split into.
+template <typename XT> constexpr int XT_PIECES = sizeof(XT) == 2 ? 1 : 3;
 
 __device__ __forceinline__ float activate(float g, int act)
 {
@@ -214,18 +181,23 @@ __device__ __forceinline__ float activate(float g, int act)
 }
 
 // One output from the formula alone, for sums that are not finite.  x: the
-// token's row; q, sc: the column block's first words; n: the column in it.
+// token's row; q, sc: the column block's first words; n: the column in it.  A NaN
+// ends it at once: batches full of them cost little.
 template <typename XT, int SPB>
 __device__ __noinline__ float plain_sum(const XT *x, const uint32_t *q, const typename Scale<XT>::word *sc,
                                         int n, int d_in)
 {
     float sum = 0.f;
-    for (int k = 0; k < d_in; ++k) {
-        const int kb = k >> 7, j = (k >> 5) & 3, g = (k >> 3) & 3, i = k & 7;
-        const uint32_t w = q[(int64_t)kb * 256 + (g * 16 + n) * 4 + j];
-        const float v = (float)(__builtin_rotateright32(w, 3 + 4 * ((i & 1) * 4 + (i >> 1))) & 15u);
-        const typename Scale<XT>::word s = sc[((int64_t)kb * 16 + n) * SPB + ((k & 127) * SPB >> 7)];
-        sum += to_f32<XT>(x[k]) * ((v + 16.f - Scale<XT>::zero(s)) * Scale<XT>::scale(s));
+    for (int k = 0; k < d_in && sum == sum; k += 8) {
+        const int kb = k >> 7, j = (k >> 5) & 3, g = (k >> 3) & 3;
+        const uint32_t w = __builtin_rotateright32(q[(int64_t)kb * 256 + (g * 16 + n) * 4 + j], 3);
+        const typename Scale<XT>::word sw = sc[((int64_t)kb * 16 + n) * SPB + ((k & 127) * SPB >> 7)];
+        const float s = Scale<XT>::scale(sw), z = Scale<XT>::zero(sw) - 16.f;
+        XT v[8];
+        __builtin_memcpy(v, x + k, sizeof v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sum += to_f32<XT>(v[i]) * (((float)((w >> (4 * ((i & 1) * 4 + (i >> 1)))) & 15u) - z) * s);
     }
     return sum;
 }
@@ -233,43 +205,144 @@ __device__ __noinline__ float plain_sum(const XT *x, const uint32_t *q, const ty
 // ---------------------------------------------------------------------------
 // products of few tokens
 //
-// One workgroup = one block of 16 columns (of gate and of up when GATED) and
+// One workgroup = C blocks of 16 columns (of gate and of up when GATED) and
 // 16 MT tokens; its W waves take the K blocks in turn and join their sums in LDS.
-template <typename XT, int MT, int SPB, bool GATED, int W>
+// Each wave keeps D blocks in flight.
+template <typename XT> struct RawX;        // eight inputs of a token as they were loaded
+template <> struct RawX<uint16_t> {
+    u32x4 v;
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t src, uint32_t off)
+    {
+        v = __builtin_amdgcn_raw_buffer_load_b128(src, off, 0, 0);
+    }
+    __device__ __forceinline__ void split(bf16x8 *p) const { p[0] = __builtin_bit_cast(bf16x8, v); }
+};
+template <> struct RawX<float> {
+    u32x4 v[2];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t src, uint32_t off)
+    {
+        v[0] = __builtin_amdgcn_raw_buffer_load_b128(src, off, 0, 0);
+        v[1] = __builtin_amdgcn_raw_buffer_load_b128(src, off + 16, 0, 0);
+    }
+    __device__ __forceinline__ void split(bf16x8 *p) const
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = __uint_as_float(v[i >> 2][i & 3]);
+            const __bf16 hi = (__bf16)f;
+            const float rest = f - (float)hi;      // exact
+            const __bf16 mid = (__bf16)rest;
+            p[0][i] = hi;
+            p[1][i] = mid;
+            p[2][i] = (__bf16)(rest - (float)mid);
+        }
+    }
+};
+
+// The scale words of one column and K block, off + at bytes into the buffer (at is
+// wave-uniform and inside it).
+template <typename XT, int SPB>
+__device__ __forceinline__ void load_scales(typename Scale<XT>::word *out, __amdgpu_buffer_rsrc_t src,
+                                            uint32_t off, uint32_t at)
+{
+    constexpr int W32 = SPB * (int)sizeof(typename Scale<XT>::word) / 4;
+    uint32_t v[W32];
+    if constexpr (W32 == 1) {
+        v[0] = __builtin_amdgcn_raw_buffer_load_b32(src, off, at, 0);
+    } else if constexpr (W32 == 2) {
+        const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(src, off, at, 0);
+        v[0] = t[0], v[1] = t[1];
+    } else {
+#pragma unroll
+        for (int b = 0; b < W32; b += 4) {
+            const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(src, off + b * 4, at, 0);
+            v[b] = t[0], v[b + 1] = t[1], v[b + 2] = t[2], v[b + 3] = t[3];
+        }
+    }
+    __builtin_memcpy(out, v, sizeof v);
+}
+
+// Column tiles of `width` columns of each member; returns how many there are.
+template <bool GATED>
+int set_tiles(BaseArgs &a, int width)
+{
+    a.tile_start[0] = 0;
+    for (int i = 0; i < a.n; ++i)
+        a.tile_start[i + 1] = a.tile_start[i] + (a.m[i].d_out + width - 1) / width;
+    return a.tile_start[GATED ? 1 : a.n];
+}
+bool any_zero(const BaseArgs &a)
+{
+    bool zero = false;
+    for (int i = 0; i < a.n; ++i)
+        zero = zero || a.m[i].zero;
+    return zero;
+}
+
+template <typename XT, int MT, int C, int SPB, bool GATED, int W, int D>
 __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
 {
     typedef typename Scale<XT>::word word;
+    constexpr int PIECES = XT_PIECES<XT>;
     constexpr int P = GATED ? 2 : 1;
-    // K blocks in flight per wave, by the registers their x takes
-    constexpr int U = (sizeof(XT) == 2 ? 4 : 2) / MT > 0 ? (sizeof(XT) == 2 ? 4 : 2) / MT : 1;
-    __shared__ float red[W][P][MT][256];
+    constexpr int B = P * C;                      // weight blocks, each weight's C together
+    constexpr uint32_t kScBytes = 16 * SPB * sizeof(word);
+    __shared__ float red[W][B][MT][256];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = lane & 15, g = lane >> 4;
     int i = 0;
     if constexpr (!GATED)
-        while (i + 1 < a.n && (int)blockIdx.x >= a.col_start[i + 1])
+        while (i + 1 < a.n && (int)blockIdx.x >= a.tile_start[i + 1])
             ++i;
     const BaseMember &m = a.m[i];
-    const int nb = blockIdx.x - a.col_start[i];
+    const int nb = (blockIdx.x - a.tile_start[i]) * C;
     const int t0 = blockIdx.y * 16 * MT;
     const int KB = m.kb, d_in = m.d_in;
 
-    const XT *xrow[MT];
+    // tokens past the batch read 0
+    const uint32_t x_row = (uint32_t)d_in * (uint32_t)sizeof(XT);
+    const auto xb = buffer((const XT *)m.x + (int64_t)t0 * d_in, (uint32_t)min(16 * MT, a.T - t0) * x_row);
+    uint32_t x_off[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
-        xrow[mt] = (const XT *)m.x + (int64_t)min(t0 + mt * 16 + (lane & 15), a.T - 1) * d_in;
-    const uint32_t *q[P];
-    const word *sc[P];
+        x_off[mt] = (uint32_t)(mt * 16 + row) * x_row + g * 8 * (uint32_t)sizeof(XT);
+    const int nblocks = (m.d_out + kBaseCols - 1) / kBaseCols;
+    __amdgpu_buffer_rsrc_t q[B], sc[B];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const BaseMember &mp = GATED ? a.m[p] : m;
-        q[p] = mp.q + ((int64_t)nb * KB * 64 + lane) * 4;
-        sc[p] = (const word *)mp.sc + ((int64_t)nb * KB * 16 + (lane & 15)) * SPB;
+    for (int p = 0; p < B; ++p) {                 // past the last block: that one again, not stored
+        const BaseMember &mp = GATED ? a.m[p / C] : m;
+        const int64_t at = (int64_t)min(nb + p % C, nblocks - 1) * KB;
+        q[p] = buffer((const char *)mp.q + at * 1024, (uint32_t)KB * 1024u);
+        sc[p] = buffer((const char *)mp.sc + at * kScBytes, (uint32_t)KB * kScBytes);
     }
 
-    f32x4 tot[P][MT];
+    u32x4 wq[D][B];
+    word ws[D][B][SPB];
+    RawX<XT> xr[D][MT][4];
+    // Blocks past the last one lie past the ends of the weights' buffers and read zeros;
+    // inputs past d_in are sent past the end of x's.  The whole offset is the lanes'
+    // own: a scalar offset past the end of a buffer is not checked against it.
+    auto load = [&](int d, int kb) __attribute__((always_inline)) {
 #pragma unroll
-    for (int p = 0; p < P; ++p)
+        for (int p = 0; p < B; ++p) {
+            wq[d][p] = __builtin_amdgcn_raw_buffer_load_b128(q[p], (uint32_t)kb * 1024u + lane * 16, 0, 0);
+            load_scales<XT, SPB>(ws[d][p], sc[p], (uint32_t)kb * kScBytes + row * (uint32_t)(SPB * sizeof(word)), 0);
+        }
+        const int left = d_in - kb * kBaseK;
+        const uint32_t at = (uint32_t)kb * (uint32_t)(kBaseK * sizeof(XT));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                xr[d][mt][j].load(xb, j * 32 + g * 8 < left ? x_off[mt] + at + j * 32 * (uint32_t)sizeof(XT)
+                                                            : 0x80000000u);
+    };
+
+    f32x4 tot[B][MT];
+#pragma unroll
+    for (int p = 0; p < B; ++p)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
             tot[p][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -277,33 +350,15 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
     const bf16x8 ones = __builtin_bit_cast(bf16x8, ones_bits);
     const Constants con = hold_constants();
 
-    for (int kb0 = wave; kb0 < KB; kb0 += W * U) {
-        u32x4 wq[U][P];
-        word ws[U][P][SPB];
-        XFrag<XT> xf[U][MT][4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int kb = min(kb0 + u * W, KB - 1);
+    for (int d = 0; d < D; ++d)
+        load(d, wave + d * W);
+    for (int kb0 = wave; kb0 < KB; kb0 += D * W) {
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-                wq[u][p] = *(const u32x4 *)(q[p] + (int64_t)kb * 256);
-#pragma unroll
-                for (int b = 0; b < SPB; ++b)
-                    ws[u][p][b] = sc[p][(int64_t)kb * 16 * SPB + b];
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = kb * kBaseK + j * 32 + (lane >> 4) * 8;
-                    xf[u][mt][j].load(xrow[mt] + min(k, d_in - 8), k < d_in);
-                }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (kb0 + u * W >= KB)
+        for (int d = 0; d < D; ++d) {
+            if (kb0 + d * W >= KB)
                 break;
-            f32x4 acc[P][MT], sum[MT];
+            f32x4 acc[B][MT], sum[MT];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if ((j * SPB) % 4 == 0) {
@@ -311,27 +366,32 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
                     for (int mt = 0; mt < MT; ++mt) {
                         sum[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int p = 0; p < P; ++p)
+                        for (int p = 0; p < B; ++p)
                             acc[p][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
                     }
                 }
-                bf16x8 b[P];
+                bf16x8 b[B];
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    b[p] = unpack(wq[u][p][j], con);
+                for (int p = 0; p < B; ++p)
+                    b[p] = unpack(wq[d][p][j], con);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
+                    bf16x8 x[PIECES];
+                    xr[d][mt][j].split(x);
 #pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        acc[p][mt] = mma<XT>(xf[u][mt][j], b[p], acc[p][mt]);
-                    sum[mt] = mma<XT>(xf[u][mt][j], ones, sum[mt]);
+                    for (int c = PIECES - 1; c >= 0; --c) {      // small pieces first
+#pragma unroll
+                        for (int p = 0; p < B; ++p)
+                            acc[p][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[c], b[p], acc[p][mt], 0, 0, 0);
+                        sum[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[c], ones, sum[mt], 0, 0, 0);
+                    }
                 }
                 if (((j + 1) * SPB) % 4 == 0) {
                     const int sub = j * SPB / 4;
 #pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const float s = Scale<XT>::scale(ws[u][p][sub]);
-                        const float z = Scale<XT>::zero(ws[u][p][sub]);
+                    for (int p = 0; p < B; ++p) {
+                        const float s = Scale<XT>::scale(ws[d][p][sub]);
+                        const float z = Scale<XT>::zero(ws[d][p][sub]);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -340,21 +400,24 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
                     }
                 }
             }
+            if (kb0 + (d + D) * W < KB)
+                load(d, kb0 + (d + D) * W);
         }
     }
 
     // lane l holds tokens 4 (l / 16) .. + 3 of column l % 16
 #pragma unroll
-    for (int p = 0; p < P; ++p)
+    for (int p = 0; p < B; ++p)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                red[wave][p][mt][((lane >> 4) * 4 + r) * 16 + (lane & 15)] = tot[p][mt][r];
+                red[wave][p][mt][(g * 4 + r) * 16 + row] = tot[p][mt][r];
     __syncthreads();
     const int d_out = m.d_out;
-    for (int e = threadIdx.x; e < MT * 256; e += W * 64) {
-        const int t = t0 + (e >> 4), col = nb * kBaseCols + (e & 15);
+    for (int e = threadIdx.x; e < C * MT * 256; e += W * 64) {
+        const int c = e / (MT * 256), in = e % (MT * 256);
+        const int t = t0 + (in >> 4), col = (nb + c) * kBaseCols + (in & 15);
         if (t >= a.T || col >= d_out)
             continue;
         float v[P];
@@ -364,11 +427,11 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < W; ++w)
-                s += red[w][p][e >> 8][e & 255];
+                s += red[w][p * C + c][in >> 8][in & 255];
             if (!(fabsf(s) < __builtin_inff()))
                 s = plain_sum<XT, SPB>((const XT *)m.x + (int64_t)t * d_in,
-                                       mp.q + (int64_t)nb * KB * 256,
-                                       (const word *)mp.sc + (int64_t)nb * KB * 16 * SPB, e & 15, d_in);
+                                       mp.q + (int64_t)(nb + c) * KB * 256,
+                                       (const word *)mp.sc + (int64_t)(nb + c) * KB * 16 * SPB, in & 15, d_in);
             if (mp.bias)
                 s += to_f32<XT>(((const XT *)mp.bias)[col]);
             if (mp.add)
@@ -380,6 +443,15 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
             out = activate(v[0], a.act) * v[P - 1];
         ((XT *)m.y)[(int64_t)t * d_out + col] = from_f32<XT>(out);
     }
+}
+
+template <typename XT, int MT, int C, int SPB, bool GATED, int W, int D>
+hipError_t launch_few(const BaseArgs &args, hipStream_t st)
+{
+    BaseArgs a = args;
+    const int cols = set_tiles<GATED>(a, 16 * C);
+    base_few_kernel<XT, MT, C, SPB, GATED, W, D><<<dim3(cols, (a.T + 16 * MT - 1) / (16 * MT)), W * 64, 0, st>>>(a);
+    return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -400,46 +472,30 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
 // which block k - 1 has read; one barrier a block.  16-byte piece p of stage row r
 // sits in slot p ^ (r & 15), so the 16 rows of an operand read fall on distinct
 // banks.
-constexpr int kTileWaveCols = 64;
-
-template <typename XT> struct Staged;      // eight inputs of a token on their way to LDS
-template <> struct Staged<uint16_t> {
-    u32x4 v;
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t src, uint32_t off)
-    {
-        v = __builtin_amdgcn_raw_buffer_load_b128(src, off, 0, 0);
-    }
-};
-template <> struct Staged<float> {
-    float v[8];
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t src, uint32_t off)
-    {
-        const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(src, off, 0, 0);
-        const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(src, off, 16, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = __uint_as_float(lo[i]);
-            v[i + 4] = __uint_as_float(hi[i]);
-        }
-    }
-};
-
-template <typename XT, int MT, int MW, int SPB, bool GATED, bool ZERO>
-__global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(BaseArgs a)
+// NT column blocks a wave (GATED: half of them gate's, half up's), KW groups of four
+// waves that take the K blocks in turn and join their sums in LDS.
+template <typename XT, int MT, int NT, int KW, int SPB, bool GATED, bool ZERO, bool DX>
+__global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(BaseArgs a)
 {
     typedef typename Scale<XT>::word word;
-    constexpr int PIECES = XFrag<XT>::PIECES;
+    constexpr int PIECES = XT_PIECES<XT>;
     constexpr int P = GATED ? 2 : 1;
-    constexpr int NT = 4;                         // column blocks per wave, gate's first
-    constexpr int BM = 16 * MT * MW;
+    constexpr int NP = NT / P;                    // column blocks per wave and weight
+    constexpr int BM = 16 * MT, BN = 64 * NP;
     constexpr int NK = 4 / SPB;                   // MFMA steps per group of a block
     constexpr uint32_t kScBytes = 16 * SPB * sizeof(word);   // scales of a weight block
-    __shared__ __attribute__((aligned(16))) uint16_t xs[3][PIECES][BM * kBaseK];
-    __shared__ __attribute__((aligned(16))) float sums[2][SPB][BM];
+    constexpr int RN = BN + 4;                    // row of joined sums, padded for the banks
+    constexpr size_t kStageBytes = (size_t)KW * 3 * PIECES * BM * kBaseK * 2;
+    constexpr size_t kJoinBytes = KW == 1 ? 0 : (size_t)KW * P * BM * RN * 4;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes];
+    __shared__ __attribute__((aligned(16))) float sums_all[KW][2][SPB][BM];
 
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wn = wave & 3, wm = wave >> 2;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = wave & 3, kg = wave >> 2;
+    const int tid = threadIdx.x & 255;            // in its group
+    auto &xs = ((uint16_t(*)[3][PIECES][BM * kBaseK])lds)[kg];
+    auto &sums = sums_all[kg];
     const int row = lane & 15, g = lane >> 4;
 
     // work item -> (column tile, token tile): an XCD takes a contiguous run of items,
@@ -469,14 +525,13 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
     int nb[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int b = GATED ? c_tile * 8 + wn * 2 + (n & 1) : c_tile * 16 + wn * 4 + n;
+        const int b = (c_tile * 4 + wn) * NP + n % NP;
         nb[n] = b;
         const int64_t at = (int64_t)min(b, nblocks - 1) * KB;
-        const BaseMember &mp = GATED ? a.m[n >> 1] : m;
+        const BaseMember &mp = GATED ? a.m[n / NP] : m;
         q[n] = buffer((const char *)mp.q + at * 1024, (uint32_t)KB * 1024u);
         sc[n] = buffer((const char *)mp.sc + at * kScBytes, (uint32_t)KB * kScBytes);
     }
-    const uint32_t q_off = lane * 16, sc_off = row * (uint32_t)(SPB * sizeof(word));
 
     // staging: this thread's piece of MT rows, as offsets from the tile's first row
     const int piece = tid & 15, srow = tid >> 4;
@@ -485,10 +540,10 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
     uint32_t src[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-        src[i] = (uint32_t)(srow + i * 16 * MW) * (uint32_t)d_in * (uint32_t)sizeof(XT);
+        src[i] = (uint32_t)(srow + i * 16) * (uint32_t)d_in * (uint32_t)sizeof(XT);
     // half of the rows at a time, which is half of the registers
     constexpr int HT = MT / 2;
-    Staged<XT> st[HT];
+    RawX<XT> st[HT];
     auto load_x = [&](int kb, int half) __attribute__((always_inline)) {
         const int k = kb * kBaseK + piece * 8;
         // inputs past d_in read 0, as rows past the batch do: an offset past the buffer
@@ -500,27 +555,40 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
     auto store_x = [&](int stage, int half) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < HT; ++i) {
-            const int r = srow + (half * HT + i) * 16 * MW;
+            const int r = srow + (half * HT + i) * 16;
             const int at = r * kBaseK + ((piece ^ (r & 15)) << 3);
-            if constexpr (PIECES == 1) {
-                *(u32x4 *)&xs[stage][0][at] = st[i].v;
-            } else {
-                bf16x8 p[3];
+            bf16x8 p[PIECES];
+            st[i].split(p);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float f = st[i].v[e];
-                    const __bf16 hi = (__bf16)f;
-                    const float rest = f - (float)hi;      // exact
-                    const __bf16 mid = (__bf16)rest;
-                    p[0][e] = hi;
-                    p[1][e] = mid;
-                    p[2][e] = (__bf16)(rest - (float)mid);
-                }
-#pragma unroll
-                for (int c = 0; c < PIECES; ++c)
-                    *(bf16x8 *)&xs[stage][c][at] = p[c];
-            }
+            for (int c = 0; c < PIECES; ++c)
+                *(bf16x8 *)&xs[stage][c][at] = p[c];
         }
+    };
+    // or, with direct-to-LDS loads (DX): MT of them a wave and block, 4 rows each; rows
+    // past the batch and inputs past d_in repeat the last (weights past d_in equal their
+    // zero point, so those products cancel)
+    const char *xd = (const char *)m.x + (int64_t)t0 * d_in * 2;
+    const uint32_t xs_at = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) unsigned char *)lds +
+                           (uint32_t)(kg * 3 * PIECES * BM * kBaseK * 2);
+    uint32_t xd_row[MT], xd_k[MT];
+#pragma unroll
+    for (int i = 0; DX && i < MT; ++i) {
+        const int r = 4 * (wn + 4 * i) + (lane >> 4);
+        xd_row[i] = (uint32_t)min(r, a.T - 1 - t0) * (uint32_t)d_in * 2u;
+        xd_k[i] = (uint32_t)(((lane & 15) ^ (r & 15)) * 8);
+    }
+    auto dma_x = [&](int stage, int kb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            dma16_off(xd, xd_row[i] + min((uint32_t)kb * kBaseK + xd_k[i], (uint32_t)d_in - 8u) * 2u,
+                      xs_at + (uint32_t)(stage * BM * kBaseK * 2 + (wn + 4 * i) * 1024));
+    };
+    // every load is in, every read of LDS done, in every wave
+    auto landed = [&]() __attribute__((always_inline)) {
+        if constexpr (DX)
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        else
+            __syncthreads();
     };
     auto x_frag = [&](int stage, int c, int r0, int j) __attribute__((always_inline)) {
         const int r = r0 + row;
@@ -532,7 +600,7 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
     auto sum_x = [&](int stage, int kb) __attribute__((always_inline)) {
         if (wn >= MT)
             return;
-        const int r0 = (wm * MT + wn) * 16;
+        const int r0 = wn * 16;
 #pragma unroll
         for (int sub = 0; sub < SPB; ++sub) {
             f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -559,44 +627,61 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             wq[n] = __builtin_amdgcn_raw_buffer_load_b128(q[n], lane * 16, kb * 1024, 0);
-            constexpr int W32 = SPB * (int)sizeof(word) / 4;      // 32-bit words per column
-            uint32_t v[W32];
-#pragma unroll
-            for (int b = 0; b < W32; b += 4) {
-                const int off = row * W32 * 4 + b * 4, at = kb * (int)kScBytes;
-                if constexpr (W32 == 1) {
-                    v[0] = __builtin_amdgcn_raw_buffer_load_b32(sc[n], off, at, 0);
-                } else if constexpr (W32 == 2) {
-                    const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(sc[n], off, at, 0);
-                    v[0] = t[0], v[1] = t[1];
-                } else {
-                    const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(sc[n], off, at, 0);
-                    v[b] = t[0], v[b + 1] = t[1], v[b + 2] = t[2], v[b + 3] = t[3];
-                }
-            }
-            __builtin_memcpy(ws[n], v, sizeof v);
+            load_scales<XT, SPB>(ws[n], sc[n], row * (uint32_t)(SPB * sizeof(word)), (uint32_t)kb * kScBytes);
         }
     };
     const Constants con = hold_constants();
 
-    load_w(0);
+    // this group's block k is block k KW + kg of the weights; blocks past the last one
+    // repeat it against inputs of 0
+    const int nk = (KB + KW - 1) / KW;
+    auto w_block = [&](int k) __attribute__((always_inline)) { return min(k * KW + kg, KB - 1); };
+
+    load_w(w_block(0));
     // blocks past the last one are read as zeros, staged and never multiplied, so that
     // the loop has no branches
+    if constexpr (DX) {
+        dma_x(0, kg);
+        dma_x(1, KW + kg);
+    } else {
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            load_x(kb, half);
-            store_x(kb, half);
-        }
-    __syncthreads();
+            for (int half = 0; half < 2; ++half) {
+                load_x(kb * KW + kg, half);
+                store_x(kb, half);
+            }
+    }
+    landed();
     sum_x(0, 0);
-    load_x(2, 0);
-    __syncthreads();
+    if constexpr (!DX)
+        load_x(2 * KW + kg, 0);
+    landed();
 
+    constexpr int STEPS = MT * SPB;
+    static_assert(STEPS % 2 == 0, "x alternates between two sets of registers");
+    bf16x8 x[2][NK][PIECES];
+    f32x4 c0[2];
+    auto read_x = [&](int stage, int k, int step) __attribute__((always_inline)) {
+        const int r0 = step / SPB * 16, sub = step % SPB;
+        c0[step & 1] = *(const f32x4 *)&sums[k & 1][sub][r0 + 4 * g];
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+#pragma unroll
+            for (int c = 0; c < PIECES; ++c)
+                x[step & 1][j][c] = x_frag(stage, c, r0, sub * NK + j);
+    };
+    read_x(0, 0, 0);
     int cur = 0;                                  // stage of block k
-    for (int k = 0; k < KB; ++k) {
+    for (int k = 0; k < nk; ++k) {
         const int next = cur == 2 ? 0 : cur + 1, fill = next == 2 ? 0 : next + 1;
+        if constexpr (DX) {
+            // the weights' wait, here where it is over and before further loads start
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                asm volatile("" : "+v"(wq[n]), "+v"(ws[n][0]));
+            dma_x(fill, (k + 2) * KW + kg);
+        }
         bf16x8 w[NT][4];
         float s[NT][SPB], z[NT][SPB];
 #pragma unroll
@@ -610,33 +695,28 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
                 z[n][b] = ZERO ? Scale<XT>::zero(ws[n][b]) : 0.f;
             }
         }
-        load_w(min(k + 1, KB - 1));
-        store_x(fill, 0);
-        load_x(k + 2, 1);
+        load_w(w_block(k + 1));
+        if constexpr (!DX) {
+            store_x(fill, 0);
+            load_x((k + 2) * KW + kg, 1);
+        }
         sum_x(next, k + 1);
-        // one group of one token block after the other, its x read a step ahead
-        constexpr int STEPS = MT * SPB;
-        bf16x8 x[2][NK][PIECES];
-        f32x4 c0[2];
-        auto read_x = [&](int step) __attribute__((always_inline)) {
-            const int r0 = (wm * MT + step / SPB) * 16, sub = step % SPB;
-            c0[step & 1] = *(const f32x4 *)&sums[k & 1][sub][r0 + 4 * g];
-#pragma unroll
-            for (int j = 0; j < NK; ++j)
-#pragma unroll
-                for (int c = 0; c < PIECES; ++c)
-                    x[step & 1][j][c] = x_frag(cur, c, r0, sub * NK + j);
-        };
-        read_x(0);
+        // one group of one token block after the other, its x read a step ahead; before the
+        // last one's products, when this block has been read, the waves meet, and the next
+        // block's first x is read under those products
 #pragma unroll
         for (int step = 0; step < STEPS; ++step) {
             __builtin_amdgcn_sched_barrier(0xf);      // memory operations stay in their step
             const int mt = step / SPB, sub = step % SPB;
-            if (step + 1 < STEPS)
-                read_x(step + 1);
-            if (step == STEPS / 2) {
+            if (!DX && step == STEPS / 2) {
                 store_x(fill, 1);
-                load_x(k + 3, 0);
+                load_x((k + 3) * KW + kg, 0);
+            }
+            if (step + 1 < STEPS) {
+                read_x(cur, k, step + 1);
+            } else {
+                landed();
+                read_x(next, k + 1, 0);
             }
             f32x4 acc[NT];
 #pragma unroll
@@ -656,94 +736,453 @@ __global__ __launch_bounds__(256 * MW, MW == 1 ? 2 : 1) void base_tile_kernel(Ba
                 for (int r = 0; r < 4; ++r)
                     tot[mt][n][r] = fmaf(s[n][sub], acc[n][r], tot[mt][n][r]);
         }
-        __syncthreads();
         cur = next;
     }
 
-    // lane l holds tokens 4 (l / 16) .. + 3 of column l % 16 of each block
-#pragma unroll
-    for (int n = 0; n < NT / P; ++n) {
-        const int col = nb[n] * kBaseCols + row;
-        if (nb[n] >= nblocks || col >= d_out)
-            continue;
-        float bias[P];
+    // an output from its sums
+    auto finish = [&](const float *v, int t, int col) __attribute__((always_inline)) {
+        float f[P];
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const BaseMember &mp = GATED ? a.m[p] : m;
-            bias[p] = mp.bias ? to_f32<XT>(((const XT *)mp.bias)[col]) : 0.f;
+            f[p] = v[p];
+            if (!(fabsf(f[p]) < __builtin_inff())) {
+                const int64_t at = (int64_t)(col >> 4) * KB;
+                f[p] = plain_sum<XT, SPB>((const XT *)m.x + (int64_t)t * d_in, mp.q + at * 256,
+                                          (const word *)mp.sc + at * (16 * SPB), col & 15, d_in);
+            }
+            if (mp.bias)
+                f[p] += to_f32<XT>(((const XT *)mp.bias)[col]);
+            if (mp.add)
+                f[p] += to_f32<XT>(((const XT *)mp.add)[(int64_t)t * d_out + col]);
         }
+        float out = f[0];
+        if constexpr (GATED)
+            out = activate(f[0], a.act) * f[P - 1];
+        return from_f32<XT>(out);
+    };
+    // lane l holds tokens 4 (l / 16) .. + 3 of column l % 16 of each block
+    if constexpr (KW == 1) {
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const int col = nb[n] * kBaseCols + row;
+            if (col >= d_out)
+                continue;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = t0 + mt * 16 + 4 * g + r;
+                    if (t >= a.T)
+                        continue;
+                    float v[P];
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        v[p] = tot[mt][n + p * NP][r];
+                    ((XT *)m.y)[(int64_t)t * d_out + col] = finish(v, t, col);
+                }
+        }
+    } else {
+        landed();                                 // the loop's last reads of the stages are done
+        float *red = (float *)lds;                // [KW][P][BM][RN]
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    red[((kg * P + n / NP) * BM + mt * 16 + 4 * g + r) * RN + (wn * NP + n % NP) * 16 + row] =
+                        tot[mt][n][r];
+        __syncthreads();
+        for (int e = threadIdx.x; e < BM * BN / 4; e += 256 * KW) {
+            const int r = e / (BN / 4), c = e % (BN / 4) * 4;
+            const int t = t0 + r, col = c_tile * BN + c;
+            if (t >= a.T || col >= d_out)
+                continue;
+            f32x4 v[P];
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                v[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < KW; ++w)
+                    v[p] += *(const f32x4 *)&red[((w * P + p) * BM + r) * RN + c];
+            }
+            XT out[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float u[2] = {v[0][i], v[P - 1][i]};
+                out[i] = finish(u, t, col + i);
+            }
+            __builtin_memcpy((XT *)m.y + (int64_t)t * d_out + col, out, sizeof out);
+        }
+    }
+}
+
+// Products of a middling number of tokens (bf16, x on a 16-byte boundary): too few tiles
+// to fill the chip, so a workgroup splits the K blocks over KW groups of four waves,
+// and x, weights and scales are all brought to LDS by direct-to-LDS loads, S - 1 blocks
+// ahead and without registers.  Each wave forms the sums of x of all its rows itself,
+// in the block they belong to: at these sizes it waits for memory, not for products.
+//
+// Block k of a group lies in stage k % S; block k + S - 1 is loaded into the stage of
+// block k - 1 once every wave has read that.  Every wave issues the same number of loads
+// a block (LOADS), so the wait that lets the last S - 2 blocks' loads stand is a constant.
+// Rows past the batch, inputs past d_in and blocks past the last one are addressed inside
+// the buffers and drop out: such rows are not stored, such inputs have weights equal to
+// their zero point, and such blocks get scale 0.
+template <int MT, int NT, int CW, int KW, int S, int SPB, bool GATED, bool ZERO>
+__global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
+{
+    constexpr int P = GATED ? 2 : 1;
+    constexpr int NP = NT / P;
+    constexpr int BM = 16 * MT, BN = 16 * CW * NP;
+    constexpr int NK = 4 / SPB;
+    constexpr int WB = CW * NT;                   // weight blocks of a workgroup
+    constexpr int XL = BM / 4 / CW;               // loads of x a wave and block
+    constexpr int kX = BM * kBaseK * 2, kW = WB * 1024, SL = (WB * SPB + 3) / 4, kS = SL * 256;
+    constexpr int kStage = kX + kW + kS;          // LDS bytes of a group's stage
+    constexpr int RN = BN + 4;
+    constexpr int kJoin = KW * P * BM * RN * 4;
+    constexpr int kLds = S * kStage * KW > kJoin ? S * kStage * KW : kJoin;
+    constexpr int SW = (SL + CW - 1) / CW;        // scale loads (SL of 256 bytes a block) of each wave
+    constexpr int LOADS = XL + NT + SW;
+    static_assert(CW == 4 || !GATED, "a load of scales is of one weight");
+    static_assert((S - 2) * LOADS < 64, "vmcnt counts to 63");
+    __shared__ __attribute__((aligned(16))) unsigned char lds[kLds];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kg = wave / CW, wn = wave % CW;
+    const int row = lane & 15, g = lane >> 4;
+
+    const int per_xcd = gridDim.x >> 3;
+    const int item = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+    if (item >= a.items)
+        return;
+    const int t_tiles = (a.T + BM - 1) / BM;
+    const int c_tiles = a.tile_start[GATED ? 1 : a.n];
+    const int band = item / (8 * c_tiles), in = item - band * 8 * c_tiles;
+    const int high = min(8, t_tiles - band * 8);
+    int c_tile = __builtin_amdgcn_readfirstlane(in / high);
+    const int t0 = __builtin_amdgcn_readfirstlane((band * 8 + in - c_tile * high) * BM);
+    int mi = 0;
+    if constexpr (!GATED)
+        while (mi + 1 < a.n && c_tile >= a.tile_start[mi + 1])
+            ++mi;
+    c_tile -= a.tile_start[mi];
+    const BaseMember &m = a.m[mi];
+    const int KB = m.kb, d_in = m.d_in, d_out = m.d_out;
+    const int nblocks = (d_out + kBaseCols - 1) / kBaseCols;
+    const int nk = (KB + KW - 1) / KW;
+
+    unsigned char *const my = lds + kg * S * kStage;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) unsigned char *)my;
+
+    // this wave's loads of a block: XL of x (4 rows of 256 bytes each), NT weight blocks,
+    // and its share of the scales (where there are fewer, several waves load the same)
+    const char *x0 = (const char *)m.x + (int64_t)t0 * d_in * 2;
+    uint32_t x_row[XL], x_k[XL];
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+        const int r = 4 * (wn + CW * i) + (lane >> 4);
+        x_row[i] = (uint32_t)min(r, a.T - 1 - t0) * (uint32_t)d_in * 2u;
+        x_k[i] = (uint32_t)(((lane & 15) ^ (r & 15)) * 8);
+    }
+    // weight block b of the workgroup: weight b / (CW NP), column block b % (CW NP)
+    auto block_at = [&](int b) __attribute__((always_inline)) {
+        return (int64_t)min(c_tile * CW * NP + b % (CW * NP), nblocks - 1) * KB;
+    };
+    const char *wsrc[NT], *ssrc[SW];
+    uint32_t s_off[SW], s_at[SW];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int b = wn + CW * i;
+        wsrc[i] = (const char *)(GATED ? a.m[b / (CW * NP)] : m).q + block_at(b) * 1024;
+    }
+#pragma unroll
+    for (int i = 0; i < SW; ++i) {
+        const int l = min(wn + CW * i, SL - 1);
+        const int word = min(l * 64 + lane, WB * 16 * SPB - 1);   // word of the workgroup's scales
+        const int b = word / (16 * SPB);
+        const int b0 = l * 64 / (16 * SPB);       // the load's first block: all are of one weight
+        ssrc[i] = (const char *)(GATED ? a.m[b0 / (CW * NP)] : m).sc + block_at(b0) * (16 * SPB * 4);
+        s_off[i] = (uint32_t)((block_at(b) - block_at(b0)) * (16 * SPB) + word % (16 * SPB)) * 4u;
+        s_at[i] = (uint32_t)(kX + kW + l * 256);
+    }
+    auto load = [&](int stage, int k) __attribute__((always_inline)) {
+        const int kb = min(k * KW + kg, KB - 1);
+        const uint32_t at = lds0 + (uint32_t)(stage * kStage);
+#pragma unroll
+        for (int i = 0; i < XL; ++i)
+            dma16_off(x0, x_row[i] + min((uint32_t)kb * kBaseK + x_k[i], (uint32_t)d_in - 8u) * 2u,
+                      at + (uint32_t)((wn + CW * i) * 1024));
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            dma16_off(wsrc[i] + (int64_t)kb * 1024, lane * 16, at + (uint32_t)(kX + (wn + CW * i) * 1024));
+#pragma unroll
+        for (int i = 0; i < SW; ++i)
+            dma4_off(ssrc[i] + (int64_t)kb * (16 * SPB * 4), s_off[i], at + s_at[i]);
+    };
+    auto landed = [&]() __attribute__((always_inline)) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * LOADS) : "memory");
+    };
+    const u32x4 ones_bits = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, ones_bits);
+    const Constants con = hold_constants();
+
+    f32x4 tot[MT][NT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            tot[mt][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k)
+        load(k, k);
+    landed();
+
+    // Before the products of a block's last step, when the wave has read all it needs of
+    // the block, it meets the others, and reads the weights and first x of the next block
+    // under those products.
+    constexpr int STEPS = MT * SPB;
+    static_assert(STEPS % 2 == 0, "x alternates between two sets of registers");
+    u32x4 raw[NT];
+    uint32_t sw[NT][SPB];
+    bf16x8 x[2][NK];
+    auto read_w = [&](const unsigned char *st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int b = n / NP * (CW * NP) + wn * NP + n % NP;
+            raw[n] = *(const u32x4 *)(st + kX + b * 1024 + lane * 16);
+#pragma unroll
+            for (int i = 0; i < SPB; ++i)
+                sw[n][i] = ((const uint32_t *)(st + kX + kW))[(b * 16 + row) * SPB + i];
+        }
+    };
+    auto read_x = [&](const unsigned char *st, int step) __attribute__((always_inline)) {
+        const int r0 = step / SPB * 16, sub = step % SPB;
+#pragma unroll
+        for (int j = 0; j < NK; ++j)
+            x[step & 1][j] = *(const bf16x8 *)(st + (r0 + row) * 256 + ((((sub * NK + j) * 4 + g) ^ row) << 4));
+    };
+    read_w(my);
+    read_x(my, 0);
+    int cur = 0;
+    for (int k = 0; k < nk; ++k) {
+        load(cur == 0 ? S - 1 : cur - 1, k + S - 1);
+        const unsigned char *st = my + cur * kStage;
+        cur = cur == S - 1 ? 0 : cur + 1;
+        bf16x8 w[NT][4];
+        float s[NT][SPB], z[NT][SPB];
+        const bool dead = k * KW + kg >= KB;      // a block past the last one
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[n][j] = unpack(raw[n][j], con);
+#pragma unroll
+            for (int i = 0; i < SPB; ++i) {
+                s[n][i] = dead ? 0.f : Scale<uint16_t>::scale(sw[n][i]);
+                z[n][i] = ZERO ? Scale<uint16_t>::zero(sw[n][i]) : 24.f;
+            }
+        }
+#pragma unroll
+        for (int step = 0; step < STEPS; ++step) {
+            // memory operations stay in their step (with short steps everything does)
+            __builtin_amdgcn_sched_barrier(SPB == 1 ? 0xf : 0);
+            const int mt = step / SPB, sub = step % SPB;
+            if (step + 1 < STEPS) {
+                read_x(st, step + 1);
+            } else {
+                landed();
+                read_w(my + cur * kStage);
+                read_x(my + cur * kStage, 0);
+            }
+            f32x4 acc[NT], sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < NK; ++j) {
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[step & 1][j], ones, sum, 0, 0, 0);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[step & 1][j], w[n][sub * NK + j], acc[n],
+                                                                     0, 0, 0);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    tot[mt][n][r] = fmaf(s[n][sub], fmaf(-z[n][sub], sum[r], acc[n][r]), tot[mt][n][r]);
+        }
+    }
+    // the loads of blocks past the last one are in before the stages hold sums
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+    // an output from its sums
+    auto finish = [&](const float *v, int t, int col) __attribute__((always_inline)) {
+        float f[P];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const BaseMember &mp = GATED ? a.m[p] : m;
+            f[p] = v[p];
+            if (!(fabsf(f[p]) < __builtin_inff())) {
+                const int64_t at = (int64_t)(col >> 4) * KB;
+                f[p] = plain_sum<uint16_t, SPB>((const uint16_t *)m.x + (int64_t)t * d_in, mp.q + at * 256,
+                                          (const uint32_t *)mp.sc + at * (16 * SPB), col & 15, d_in);
+            }
+            if (mp.bias)
+                f[p] += to_f32<uint16_t>(((const uint16_t *)mp.bias)[col]);
+            if (mp.add)
+                f[p] += to_f32<uint16_t>(((const uint16_t *)mp.add)[(int64_t)t * d_out + col]);
+        }
+        float out = f[0];
+        if constexpr (GATED)
+            out = activate(f[0], a.act) * f[P - 1];
+        return from_f32<uint16_t>(out);
+    };
+    // lane l holds tokens 4 (l / 16) .. + 3 of column l % 16 of each block
+    float *red = (float *)lds;                // [KW][P][BM][RN]
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = t0 + (wm * MT + mt) * 16 + 4 * g + r;
-                if (t >= a.T)
-                    continue;
-                const int64_t at = (int64_t)t * d_out + col;
-                float v[P];
+            for (int r = 0; r < 4; ++r)
+                red[((kg * P + n / NP) * BM + mt * 16 + 4 * g + r) * RN + (wn * NP + n % NP) * 16 + row] =
+                    tot[mt][n][r];
+    __syncthreads();
+    for (int e = threadIdx.x; e < BM * BN / 4; e += 64 * CW * KW) {
+        const int r = e / (BN / 4), c = e % (BN / 4) * 4;
+        const int t = t0 + r, col = c_tile * BN + c;
+        if (t >= a.T || col >= d_out)
+            continue;
+        f32x4 v[P];
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    const BaseMember &mp = GATED ? a.m[p] : m;
-                    float sum = tot[mt][n + p * (NT / P)][r];
-                    if (!(fabsf(sum) < __builtin_inff()))
-                        sum = plain_sum<XT, SPB>((const XT *)m.x + (int64_t)t * d_in,
-                                                 mp.q + (int64_t)nb[n] * KB * 256,
-                                                 (const word *)mp.sc + (int64_t)nb[n] * KB * 16 * SPB,
-                                                 row, d_in);
-                    if (mp.bias)
-                        sum += bias[p];
-                    if (mp.add)
-                        sum += to_f32<XT>(((const XT *)mp.add)[at]);
-                    v[p] = sum;
-                }
-                float out = v[0];
-                if constexpr (GATED)
-                    out = activate(v[0], a.act) * v[P - 1];
-                ((XT *)m.y)[at] = from_f32<XT>(out);
-            }
+        for (int p = 0; p < P; ++p) {
+            v[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < KW; ++w)
+                v[p] += *(const f32x4 *)&red[((w * P + p) * BM + r) * RN + c];
+        }
+        uint16_t out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float u[2] = {v[0][i], v[P - 1][i]};
+            out[i] = finish(u, t, col + i);
+        }
+        __builtin_memcpy((uint16_t *)m.y + (int64_t)t * d_out + col, out, sizeof out);
     }
 }
 
-template <typename XT, bool GATED, int SPB, int MT, int MW>
+template <bool GATED, int SPB, int MT, int NT, int CW, int KW, int S>
+hipError_t launch_split(const BaseArgs &args, hipStream_t st)
+{
+    BaseArgs a = args;
+    constexpr int BM = 16 * MT, BN = 16 * CW * (GATED ? NT / 2 : NT);
+    const bool zero = any_zero(a);
+    a.items = set_tiles<GATED>(a, BN) * ((a.T + BM - 1) / BM);
+    const int grid = (a.items + 7) / 8 * 8;
+    if (zero)
+        base_split_kernel<MT, NT, CW, KW, S, SPB, GATED, true><<<grid, 64 * CW * KW, 0, st>>>(a);
+    else
+        base_split_kernel<MT, NT, CW, KW, S, SPB, GATED, false><<<grid, 64 * CW * KW, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+template <typename XT, bool GATED, int SPB, int MT, int NT, int KW, bool DX>
 hipError_t launch_tile(const BaseArgs &args, hipStream_t st)
 {
     BaseArgs a = args;
-    const int cols = GATED ? 8 : 16;              // column blocks of a workgroup
-    bool zero = false;
-    a.tile_start[0] = 0;
-    for (int i = 0; i < a.n; ++i) {
-        a.tile_start[i + 1] = a.tile_start[i] + ((a.m[i].d_out + 15) / 16 + cols - 1) / cols;
-        zero = zero || a.m[i].zero;
-    }
-    a.items = a.tile_start[GATED ? 1 : a.n] * ((a.T + 16 * MT * MW - 1) / (16 * MT * MW));
+    constexpr int BM = 16 * MT, BN = 64 * (GATED ? NT / 2 : NT);
+    const bool zero = any_zero(a);
+    a.items = set_tiles<GATED>(a, BN) * ((a.T + BM - 1) / BM);
     const int grid = (a.items + 7) / 8 * 8;
     if (zero)
-        base_tile_kernel<XT, MT, MW, SPB, GATED, true><<<grid, 256 * MW, 0, st>>>(a);
+        base_tile_kernel<XT, MT, NT, KW, SPB, GATED, true, DX><<<grid, 256 * KW, 0, st>>>(a);
     else
-        base_tile_kernel<XT, MT, MW, SPB, GATED, false><<<grid, 256 * MW, 0, st>>>(a);
+        base_tile_kernel<XT, MT, NT, KW, SPB, GATED, false, DX><<<grid, 256 * KW, 0, st>>>(a);
     return hipGetLastError();
 }
 
-constexpr int kFewTokens = 64;
+// ---------------------------------------------------------------------------
+// which kernel
 
+constexpr int kCus = 256;
+
+// Whether tiles of BM tokens and BN columns are at most one per CU.
+template <bool GATED>
+bool one_per_cu(const BaseArgs &args, int BM, int BN)
+{
+    BaseArgs a = args;
+    return (int64_t)set_tiles<GATED>(a, BN) * ((a.T + BM - 1) / BM) <= kCus;
+}
+
+// Up to 16 tokens the weights' bytes decide and one MFMA row block holds the batch.
+// A workgroup of one column block reads all of x for 16 columns; where there are two
+// blocks a CU or more, workgroups of C = 4 blocks read a quarter of that (microseconds,
+// bf16, 5120 -> 10240: 1 token 8.3 against 8.5, 4 tokens 10.2 / 8.6, 16 tokens
+// 17.1 / 9.4; gated 4096 -> 11008, whose two weights share x already: 8 tokens
+// 12.2 / 12.2, 16 tokens 15.8 / 13.0; fp32, which also splits x into bf16 pieces less
+// often: 1 token of 5120 -> 10240 21.0 / 14.4).  With fewer blocks they would leave CUs
+// idle (4096 -> 4096, 16 tokens: 6.5 / 7.8).  Groups of 32 keep four scales a block: two
+// column blocks of gate and of up are what the registers hold.
+//
+// Above that, the smallest tile of which every CU gets at most one, since such a batch
+// waits for its slowest workgroup (4096 -> 4096: 64 tokens 9.1 us on 32 x 32, 11.1 on
+// 32 x 64, 15.9 on 32 x 128 tiles; 256 tokens 30.3, 23.5, 18.9; 5120 -> 10240, 256
+// tokens: 55 on 64 x 128, 45 on 64 x 256); with more, the tile kernel, two workgroups
+// a CU (8192 tokens of 4096 -> 4096: 303 us against 330 on the 64 x 256 split).
+// x off a 16-byte boundary cannot be loaded to LDS directly and takes slower ways.
 template <typename XT, bool GATED, int SPB>
 hipError_t launch_sized(const BaseArgs &a, hipStream_t st)
 {
-    const int cols = a.col_start[GATED ? 1 : a.n];
-    if (a.T > kFewTokens) {
-        if constexpr (sizeof(XT) == 2)
-            return launch_tile<XT, GATED, SPB, 4, 1>(a, st);
-        else
-            return launch_tile<XT, GATED, SPB, 2, 1>(a, st);
+    constexpr bool WIDE = sizeof(XT) == 4;
+    int blocks = 0;
+    bool aligned = true;
+    for (int i = 0; i < (GATED ? 1 : a.n); ++i) {
+        blocks += (a.m[i].d_out + kBaseCols - 1) / kBaseCols;
+        aligned = aligned && ((uintptr_t)a.m[i].x & 15) == 0;
     }
-    constexpr int W = 8;
-    constexpr int MT = sizeof(XT) == 4 || GATED ? 2 : 4;
-    if (a.T <= 16)
-        base_few_kernel<XT, 1, SPB, GATED, W><<<dim3(cols, 1), W * 64, 0, st>>>(a);
-    else
-        base_few_kernel<XT, MT, SPB, GATED, W>
-            <<<dim3(cols, (a.T + 16 * MT - 1) / (16 * MT)), W * 64, 0, st>>>(a);
-    return hipGetLastError();
+    if (a.T <= 16) {
+        if (blocks >= 2 * kCus && (WIDE || a.T > (GATED ? 8 : 2)))
+            return launch_few<XT, 1, GATED && SPB == 4 ? 2 : 4, SPB, GATED, 8, 1>(a, st);
+        return launch_few<XT, 1, 1, SPB, GATED, 8, 2>(a, st);
+    }
+    if constexpr (WIDE) {
+        // (24 tokens: 4096 -> 4096 16.8 us against 34, 5120 -> 10240 51 against 41)
+        if (a.T <= 32 && blocks <= kCus)
+            return launch_few<XT, 2, 1, SPB, GATED, 8, 1>(a, st);
+        if (one_per_cu<GATED>(a, 32, GATED ? 64 : 128))
+            return launch_tile<XT, GATED, SPB, 2, 2, 2, false>(a, st);
+        return launch_tile<XT, GATED, SPB, 2, 4, 1, false>(a, st);
+    } else {
+        if (!aligned)
+            return a.T <= 64 ? launch_few<XT, 2, 1, SPB, GATED, 8, 2>(a, st)
+                             : launch_tile<XT, GATED, SPB, 4, 4, 1, false>(a, st);
+        if constexpr (GATED) {
+            if (one_per_cu<true>(a, 32, 64))
+                return launch_split<true, SPB, 2, 2, 4, 4, 2>(a, st);
+            if (one_per_cu<true>(a, 64, 64))
+                return launch_split<true, SPB, 4, 2, 4, 2, 3>(a, st);
+            if (one_per_cu<true>(a, 64, 128))
+                return launch_split<true, SPB, 4, 4, 4, 2, 2>(a, st);
+        } else {
+            if (one_per_cu<false>(a, 32, 32))
+                return launch_split<false, SPB, 2, 1, 2, 4, 3>(a, st);
+            if (one_per_cu<false>(a, 32, 64))
+                return launch_split<false, SPB, 2, 1, 4, 4, SPB == 1 ? 3 : 2>(a, st);
+            if (one_per_cu<false>(a, 32, 128))
+                return launch_split<false, SPB, 2, 2, 4, 2, 4>(a, st);
+            if (one_per_cu<false>(a, 64, 128))
+                return launch_split<false, SPB, 4, 2, 4, 2, 3>(a, st);
+            if (one_per_cu<false>(a, 64, 256))
+                return launch_split<false, SPB, 4, 4, 4, 2, 2>(a, st);
+        }
+        return launch_tile<XT, GATED, SPB, 4, 4, 1, true>(a, st);
+    }
 }
 
 template <typename XT, bool GATED>

@@ -140,6 +140,9 @@ int lora_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *sc
             return fail(ctx, LORA_ERR_INVALID_ARGUMENT,
                         "base load while a stream this ctx launched on is under graph capture");
     const lora_module_shape sh = ctx->shapes[module];
+    if (sh.d_in > kBaseMaxIn)
+        return fail(ctx, LORA_ERR_INVALID_ARGUMENT, "d_in %d of module %d exceeds %d", sh.d_in, module,
+                    kBaseMaxIn);
     const bool bf16 = ctx->dtype == LORA_BF16;
     const int64_t kb = ceil_div(sh.d_in, kBaseK), nb = ceil_div(sh.d_out, kBaseCols);
     const int group = group_size ? group_size : (int)pad(sh.d_in, kBaseK);

@@ -28,6 +28,9 @@ namespace lora {
 // scale 0.
 constexpr int kBaseCols = 16;
 constexpr int kBaseK = 128;
+// Largest d_in of a base weight: a workgroup's rows of x (64 of 4 bytes an input) and
+// a column block's weights are addressed by 31-bit offsets.
+constexpr int kBaseMaxIn = 1 << 22;
 
 struct BasePack {
     uint32_t *q = nullptr;       // [col blocks][K blocks][64][4]

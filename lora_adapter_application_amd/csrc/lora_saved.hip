@@ -31,6 +31,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "lora_dma.h"
 #include "lora_internal.h"
 
 namespace lora {
@@ -280,20 +281,6 @@ __global__ __launch_bounds__(256, 2) void saved_bf16_kernel(SavedArgs a)
         __syncthreads();                     // the first run's last LDS reads are done
         saved_run<4>(a, m, chunk, t1.slot, t1.len, t1.len, tok1, tok1, xs);
     }
-}
-
-// One global_load_lds_dwordx4 with a wave-uniform 64-bit base and a 32-bit
-// byte offset per lane, written as asm so that the compiler does not track it:
-// its own tracking cannot tell the stages apart and would wait for every load
-// in flight before each LDS read.  The waits for these loads are explicit
-// (s_waitcnt vmcnt in the kernel); lane l writes the 16 bytes at LDS offset
-// 16 l of the instruction's 1 KB, whose wave-uniform address is lds.  m0 is
-// not named as clobbered: the compiler reserves it and sets it before each of
-// its own uses.
-__device__ __forceinline__ void dma16_off(const void *base, uint32_t off, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
-                 : "memory");
 }
 
 // ----------------------------------------------------------------------------
