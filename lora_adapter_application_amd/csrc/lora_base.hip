@@ -202,6 +202,48 @@ __device__ __noinline__ float plain_sum(const XT *x, const uint32_t *q, const ty
     return sum;
 }
 
+// Four neighbouring outputs of a token from their sums v[weight]: the sums that are not
+// finite again, bias, add, the activation, and one rounding.
+template <typename XT, int SPB, bool GATED>
+__device__ __forceinline__ void finish(const BaseArgs &a, int mi, const f32x4 *v, int t, int col)
+{
+    typedef typename Scale<XT>::word word;
+    constexpr int P = GATED ? 2 : 1;
+    const BaseMember &m = a.m[mi];
+    const int64_t at = (int64_t)t * m.d_out + col;
+    f32x4 f[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const BaseMember &mp = a.m[GATED ? p : mi];
+        f[p] = v[p];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (!(fabsf(f[p][i]) < __builtin_inff())) {
+                const int64_t block = (int64_t)(col >> 4) * m.kb;
+                f[p][i] = plain_sum<XT, SPB>((const XT *)m.x + (int64_t)t * m.d_in, mp.q + block * 256,
+                                             (const word *)mp.sc + block * (16 * SPB), (col & 15) + i, m.d_in);
+            }
+        XT e[4];
+        if (mp.bias) {
+            __builtin_memcpy(e, (const XT *)mp.bias + col, sizeof e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f[p][i] += to_f32<XT>(e[i]);
+        }
+        if (mp.add) {
+            __builtin_memcpy(e, (const XT *)mp.add + at, sizeof e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f[p][i] += to_f32<XT>(e[i]);
+        }
+    }
+    XT out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        out[i] = from_f32<XT>(GATED ? activate(f[0][i], a.act) * f[P - 1][i] : f[0][i]);
+    __builtin_memcpy((XT *)m.y + at, out, sizeof out);
+}
+
 // ---------------------------------------------------------------------------
 // products of few tokens
 //
@@ -287,7 +329,7 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
     constexpr int P = GATED ? 2 : 1;
     constexpr int B = P * C;                      // weight blocks, each weight's C together
     constexpr uint32_t kScBytes = 16 * SPB * sizeof(word);
-    __shared__ float red[W][B][MT][256];
+    __shared__ __attribute__((aligned(16))) float red[W][B][MT][256];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -414,34 +456,20 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
             for (int r = 0; r < 4; ++r)
                 red[wave][p][mt][(g * 4 + r) * 16 + row] = tot[p][mt][r];
     __syncthreads();
-    const int d_out = m.d_out;
-    for (int e = threadIdx.x; e < C * MT * 256; e += W * 64) {
-        const int c = e / (MT * 256), in = e % (MT * 256);
+    for (int e = threadIdx.x; e < C * MT * 64; e += W * 64) {
+        const int c = e / (MT * 64), in = e % (MT * 64) * 4;
         const int t = t0 + (in >> 4), col = (nb + c) * kBaseCols + (in & 15);
-        if (t >= a.T || col >= d_out)
+        if (t >= a.T || col >= m.d_out)
             continue;
-        float v[P];
+        f32x4 v[P];
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const BaseMember &mp = GATED ? a.m[p] : m;
-            float s = 0.f;
+            v[p] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < W; ++w)
-                s += red[w][p * C + c][in >> 8][in & 255];
-            if (!(fabsf(s) < __builtin_inff()))
-                s = plain_sum<XT, SPB>((const XT *)m.x + (int64_t)t * d_in,
-                                       mp.q + (int64_t)(nb + c) * KB * 256,
-                                       (const word *)mp.sc + (int64_t)(nb + c) * KB * 16 * SPB, in & 15, d_in);
-            if (mp.bias)
-                s += to_f32<XT>(((const XT *)mp.bias)[col]);
-            if (mp.add)
-                s += to_f32<XT>(((const XT *)mp.add)[(int64_t)t * d_out + col]);
-            v[p] = s;
+                v[p] += *(const f32x4 *)&red[w][p * C + c][in >> 8][in & 255];
         }
-        float out = v[0];
-        if constexpr (GATED)
-            out = activate(v[0], a.act) * v[P - 1];
-        ((XT *)m.y)[(int64_t)t * d_out + col] = from_f32<XT>(out);
+        finish<XT, SPB, GATED>(a, i, v, t, col);
     }
 }
 
@@ -486,7 +514,7 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
     constexpr uint32_t kScBytes = 16 * SPB * sizeof(word);   // scales of a weight block
     constexpr int RN = BN + 4;                    // row of joined sums, padded for the banks
     constexpr size_t kStageBytes = (size_t)KW * 3 * PIECES * BM * kBaseK * 2;
-    constexpr size_t kJoinBytes = KW == 1 ? 0 : (size_t)KW * P * BM * RN * 4;
+    constexpr size_t kJoinBytes = (size_t)KW * P * (BM / 2) * RN * 4;
     __shared__ __attribute__((aligned(16))) unsigned char lds[kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes];
     __shared__ __attribute__((aligned(16))) float sums_all[KW][2][SPB][BM];
 
@@ -739,64 +767,25 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
         cur = next;
     }
 
-    // an output from its sums
-    auto finish = [&](const float *v, int t, int col) __attribute__((always_inline)) {
-        float f[P];
+    // Through LDS, so that y is written (and add read) in rows: in two halves of the
+    // tokens, which fit the stages.  Lane l holds tokens 4 (l / 16) .. + 3 of column
+    // l % 16 of each block.
+    float *red = (float *)lds;                    // [KW][P][BM / 2][RN]
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const BaseMember &mp = GATED ? a.m[p] : m;
-            f[p] = v[p];
-            if (!(fabsf(f[p]) < __builtin_inff())) {
-                const int64_t at = (int64_t)(col >> 4) * KB;
-                f[p] = plain_sum<XT, SPB>((const XT *)m.x + (int64_t)t * d_in, mp.q + at * 256,
-                                          (const word *)mp.sc + at * (16 * SPB), col & 15, d_in);
-            }
-            if (mp.bias)
-                f[p] += to_f32<XT>(((const XT *)mp.bias)[col]);
-            if (mp.add)
-                f[p] += to_f32<XT>(((const XT *)mp.add)[(int64_t)t * d_out + col]);
-        }
-        float out = f[0];
-        if constexpr (GATED)
-            out = activate(f[0], a.act) * f[P - 1];
-        return from_f32<XT>(out);
-    };
-    // lane l holds tokens 4 (l / 16) .. + 3 of column l % 16 of each block
-    if constexpr (KW == 1) {
-#pragma unroll
-        for (int n = 0; n < NP; ++n) {
-            const int col = nb[n] * kBaseCols + row;
-            if (col >= d_out)
-                continue;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = t0 + mt * 16 + 4 * g + r;
-                    if (t >= a.T)
-                        continue;
-                    float v[P];
-#pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        v[p] = tot[mt][n + p * NP][r];
-                    ((XT *)m.y)[(int64_t)t * d_out + col] = finish(v, t, col);
-                }
-        }
-    } else {
-        landed();                                 // the loop's last reads of the stages are done
-        float *red = (float *)lds;                // [KW][P][BM][RN]
+    for (int half = 0; half < 2; ++half) {
+        landed();                                 // the last reads of the stages, or of the first half
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < MT / 2; ++mt)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    red[((kg * P + n / NP) * BM + mt * 16 + 4 * g + r) * RN + (wn * NP + n % NP) * 16 + row] =
-                        tot[mt][n][r];
+                    red[((kg * P + n / NP) * (BM / 2) + mt * 16 + 4 * g + r) * RN + (wn * NP + n % NP) * 16 + row] =
+                        tot[half * (MT / 2) + mt][n][r];
         __syncthreads();
-        for (int e = threadIdx.x; e < BM * BN / 4; e += 256 * KW) {
+        for (int e = threadIdx.x; e < BM / 2 * BN / 4; e += 256 * KW) {
             const int r = e / (BN / 4), c = e % (BN / 4) * 4;
-            const int t = t0 + r, col = c_tile * BN + c;
+            const int t = t0 + half * (BM / 2) + r, col = c_tile * BN + c;
             if (t >= a.T || col >= d_out)
                 continue;
             f32x4 v[P];
@@ -805,15 +794,9 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
                 v[p] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int w = 0; w < KW; ++w)
-                    v[p] += *(const f32x4 *)&red[((w * P + p) * BM + r) * RN + c];
+                    v[p] += *(const f32x4 *)&red[((w * P + p) * (BM / 2) + r) * RN + c];
             }
-            XT out[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u[2] = {v[0][i], v[P - 1][i]};
-                out[i] = finish(u, t, col + i);
-            }
-            __builtin_memcpy((XT *)m.y + (int64_t)t * d_out + col, out, sizeof out);
+            finish<XT, SPB, GATED>(a, mi, v, t, col);
         }
     }
 }
@@ -1021,28 +1004,6 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
     // the loads of blocks past the last one are in before the stages hold sums
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
-    // an output from its sums
-    auto finish = [&](const float *v, int t, int col) __attribute__((always_inline)) {
-        float f[P];
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const BaseMember &mp = GATED ? a.m[p] : m;
-            f[p] = v[p];
-            if (!(fabsf(f[p]) < __builtin_inff())) {
-                const int64_t at = (int64_t)(col >> 4) * KB;
-                f[p] = plain_sum<uint16_t, SPB>((const uint16_t *)m.x + (int64_t)t * d_in, mp.q + at * 256,
-                                          (const uint32_t *)mp.sc + at * (16 * SPB), col & 15, d_in);
-            }
-            if (mp.bias)
-                f[p] += to_f32<uint16_t>(((const uint16_t *)mp.bias)[col]);
-            if (mp.add)
-                f[p] += to_f32<uint16_t>(((const uint16_t *)mp.add)[(int64_t)t * d_out + col]);
-        }
-        float out = f[0];
-        if constexpr (GATED)
-            out = activate(f[0], a.act) * f[P - 1];
-        return from_f32<uint16_t>(out);
-    };
     // lane l holds tokens 4 (l / 16) .. + 3 of column l % 16 of each block
     float *red = (float *)lds;                // [KW][P][BM][RN]
 #pragma unroll
@@ -1067,13 +1028,7 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
             for (int w = 0; w < KW; ++w)
                 v[p] += *(const f32x4 *)&red[((w * P + p) * BM + r) * RN + c];
         }
-        uint16_t out[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float u[2] = {v[0][i], v[P - 1][i]};
-            out[i] = finish(u, t, col + i);
-        }
-        __builtin_memcpy((uint16_t *)m.y + (int64_t)t * d_out + col, out, sizeof out);
+        finish<uint16_t, SPB, GATED>(a, mi, v, t, col);
     }
 }
 
@@ -1152,8 +1107,9 @@ hipError_t launch_sized(const BaseArgs &a, hipStream_t st)
         return launch_few<XT, 1, 1, SPB, GATED, 8, 2>(a, st);
     }
     if constexpr (WIDE) {
-        // (24 tokens: 4096 -> 4096 16.8 us against 34, 5120 -> 10240 51 against 41)
-        if (a.T <= 32 && blocks <= kCus)
+        // (24 tokens: 4096 -> 4096 16.8 us against 34, 5120 -> 10240 51 against 41; 128 tokens
+        // of 1000 -> 1296 11.6 against 14.4, 256 tokens 16.6 against 14.7)
+        if ((int64_t)blocks * ((a.T + 31) / 32) <= 2 * kCus)
             return launch_few<XT, 2, 1, SPB, GATED, 8, 1>(a, st);
         if (one_per_cu<GATED>(a, 32, GATED ? 64 : 128))
             return launch_tile<XT, GATED, SPB, 2, 2, 2, false>(a, st);
