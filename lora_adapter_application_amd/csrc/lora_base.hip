@@ -517,6 +517,7 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
     constexpr size_t kJoinBytes = (size_t)KW * P * (BM / 2) * RN * 4;
     __shared__ __attribute__((aligned(16))) unsigned char lds[kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes];
     __shared__ __attribute__((aligned(16))) float sums_all[KW][2][SPB][BM];
+    __shared__ __attribute__((aligned(16))) float unread[256 + 2 * SPB * BM];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -606,10 +607,17 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
         xd_k[i] = (uint32_t)(((lane & 15) ^ (r & 15)) * 8);
     }
     auto dma_x = [&](int stage, int kb) __attribute__((always_inline)) {
+        const uint32_t at = xs_at + (uint32_t)(stage * BM * kBaseK * 2 + wn * 1024);
+        if ((kb + 1) * kBaseK <= d_in) {          // a whole block: its place in the rows is scalar
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-            dma16_off(xd, xd_row[i] + min((uint32_t)kb * kBaseK + xd_k[i], (uint32_t)d_in - 8u) * 2u,
-                      xs_at + (uint32_t)(stage * BM * kBaseK * 2 + (wn + 4 * i) * 1024));
+            for (int i = 0; i < MT; ++i)
+                dma16_off(xd + (int64_t)kb * (kBaseK * 2), xd_row[i] + xd_k[i] * 2u, at + (uint32_t)(i * 4096));
+        } else {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                dma16_off(xd, xd_row[i] + min((uint32_t)kb * kBaseK + xd_k[i], (uint32_t)d_in - 8u) * 2u,
+                          at + (uint32_t)(i * 4096));
+        }
     };
     // every load is in, every read of LDS done, in every wave
     auto landed = [&]() __attribute__((always_inline)) {
@@ -624,11 +632,16 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
     };
     const u32x4 ones_bits = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
     const bf16x8 ones = __builtin_bit_cast(bf16x8, ones_bits);
-    // -sum x (ZERO) or -24 sum x of this wave's token block, for block kb in `stage`
+    // -sum x (ZERO) or -24 sum x of this wave's token block, for block kb in `stage`.
+    // Every column of the product is the sum: the lanes of column 0 store it, the others
+    // store to a place that nobody reads, which costs less than a branch.
+    float *const sum_at = row == 0 ? &sums[0][0][wn * 16 + 4 * g] : &unread[lane * 4];
+    auto store_sum = [&](f32x4 acc, int kb, int sub) __attribute__((always_inline)) {
+        *(f32x4 *)(sum_at + ((kb & 1) * SPB + sub) * BM) = acc * (ZERO ? -1.f : -24.f);
+    };
     auto sum_x = [&](int stage, int kb) __attribute__((always_inline)) {
         if (wn >= MT)
             return;
-        const int r0 = wn * 16;
 #pragma unroll
         for (int sub = 0; sub < SPB; ++sub) {
             f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -636,11 +649,13 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
             for (int j = sub * NK; j < (sub + 1) * NK; ++j)
 #pragma unroll
                 for (int c = PIECES - 1; c >= 0; --c)
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x_frag(stage, c, r0, j), ones, acc, 0, 0, 0);
-            if (row == 0)
-                *(f32x4 *)&sums[kb & 1][sub][r0 + 4 * g] = acc * (ZERO ? -1.f : -24.f);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x_frag(stage, c, wn * 16, j), ones, acc, 0, 0, 0);
+            store_sum(acc, kb, sub);
         }
     };
+    // With one group a block and a token block a wave, the next block's sum is formed in
+    // pieces between the steps of this one.
+    constexpr bool SPREAD = SPB == 1 && PIECES == 1 && MT == 4;
 
     f32x4 tot[MT][NT];
 #pragma unroll
@@ -728,7 +743,10 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
             store_x(fill, 0);
             load_x((k + 2) * KW + kg, 1);
         }
-        sum_x(next, k + 1);
+        bf16x8 xn[2];
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (!SPREAD)
+            sum_x(next, k + 1);
         // one group of one token block after the other, its x read a step ahead; before the
         // last one's products, when this block has been read, the waves meet, and the next
         // block's first x is read under those products
@@ -740,6 +758,16 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
                 store_x(fill, 1);
                 load_x((k + 3) * KW + kg, 0);
             }
+            if (SPREAD && step > 0 && step < 3) {
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xn[0], ones, sum, 0, 0, 0);
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xn[1], ones, sum, 0, 0, 0);
+            }
+            if (SPREAD && step < 2) {
+                xn[0] = x_frag(next, 0, wn * 16, 2 * step);
+                xn[1] = x_frag(next, 0, wn * 16, 2 * step + 1);
+            }
+            if (SPREAD && step == 3)
+                store_sum(sum, k + 1, 0);
             if (step + 1 < STEPS) {
                 read_x(cur, k, step + 1);
             } else {
