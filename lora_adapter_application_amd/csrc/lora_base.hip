@@ -202,12 +202,11 @@ __device__ __noinline__ float plain_sum(const XT *x, const uint32_t *q, const ty
     return sum;
 }
 
-// Four neighbouring outputs of a token from their sums v[weight]: the sums that are not
-// finite again, bias, add, the activation, and one rounding.
+// Four neighbouring outputs of a token from their sums v[weight]: bias, add, the
+// activation, and one rounding.
 template <typename XT, int SPB, bool GATED>
 __device__ __forceinline__ void finish(const BaseArgs &a, int mi, const f32x4 *v, int t, int col)
 {
-    typedef typename Scale<XT>::word word;
     constexpr int P = GATED ? 2 : 1;
     const BaseMember &m = a.m[mi];
     const int64_t at = (int64_t)t * m.d_out + col;
@@ -216,13 +215,6 @@ __device__ __forceinline__ void finish(const BaseArgs &a, int mi, const f32x4 *v
     for (int p = 0; p < P; ++p) {
         const BaseMember &mp = a.m[GATED ? p : mi];
         f[p] = v[p];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (!(fabsf(f[p][i]) < __builtin_inff())) {
-                const int64_t block = (int64_t)(col >> 4) * m.kb;
-                f[p][i] = plain_sum<XT, SPB>((const XT *)m.x + (int64_t)t * m.d_in, mp.q + block * 256,
-                                             (const word *)mp.sc + block * (16 * SPB), (col & 15) + i, m.d_in);
-            }
         XT e[4];
         if (mp.bias) {
             __builtin_memcpy(e, (const XT *)mp.bias + col, sizeof e);
@@ -242,6 +234,41 @@ __device__ __forceinline__ void finish(const BaseArgs &a, int mi, const f32x4 *v
     for (int i = 0; i < 4; ++i)
         out[i] = from_f32<XT>(GATED ? activate(f[0][i], a.act) * f[P - 1][i] : f[0][i]);
     __builtin_memcpy((XT *)m.y + at, out, sizeof out);
+}
+
+// finish() where every sum is finite; else false, and nothing is stored.
+template <typename XT, int SPB, bool GATED>
+__device__ __forceinline__ bool finish_finite(const BaseArgs &a, int mi, const f32x4 *v, int t, int col)
+{
+    float big = 0.f;
+#pragma unroll
+    for (int p = 0; p < (GATED ? 2 : 1); ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            big += fabsf(v[p][i]);                // infinite or NaN as any of them is
+    if (!(big < __builtin_inff()))
+        return false;
+    finish<XT, SPB, GATED>(a, mi, v, t, col);
+    return true;
+}
+
+// finish() with the four sums formed again from the formula.
+template <typename XT, int SPB, bool GATED>
+__device__ __forceinline__ void finish_again(const BaseArgs &a, int mi, int t, int col)
+{
+    typedef typename Scale<XT>::word word;
+    const BaseMember &m = a.m[mi];
+    const int64_t block = (int64_t)(col >> 4) * m.kb;
+    f32x4 v[2];
+#pragma unroll
+    for (int p = 0; p < (GATED ? 2 : 1); ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const BaseMember &mp = a.m[GATED ? p : mi];
+            v[p][i] = plain_sum<XT, SPB>((const XT *)m.x + (int64_t)t * m.d_in, mp.q + block * 256,
+                                         (const word *)mp.sc + block * (16 * SPB), (col & 15) + i, m.d_in);
+        }
+    finish<XT, SPB, GATED>(a, mi, v, t, col);
 }
 
 // ---------------------------------------------------------------------------
@@ -469,7 +496,8 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
             for (int w = 0; w < W; ++w)
                 v[p] += *(const f32x4 *)&red[w][p * C + c][in >> 8][in & 255];
         }
-        finish<XT, SPB, GATED>(a, i, v, t, col);
+        if (!finish_finite<XT, SPB, GATED>(a, i, v, t, col))
+            finish_again<XT, SPB, GATED>(a, i, t, col);
     }
 }
 
@@ -653,10 +681,6 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
             store_sum(acc, kb, sub);
         }
     };
-    // With one group a block and a token block a wave, the next block's sum is formed in
-    // pieces between the steps of this one.
-    constexpr bool SPREAD = SPB == 1 && PIECES == 1 && MT == 4;
-
     f32x4 tot[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -743,37 +767,31 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
             store_x(fill, 0);
             load_x((k + 2) * KW + kg, 1);
         }
-        bf16x8 xn[2];
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (!SPREAD)
-            sum_x(next, k + 1);
+        sum_x(next, k + 1);
         // one group of one token block after the other, its x read a step ahead; before the
         // last one's products, when this block has been read, the waves meet, and the next
         // block's first x is read under those products
 #pragma unroll
         for (int step = 0; step < STEPS; ++step) {
-            __builtin_amdgcn_sched_barrier(0xf);      // memory operations stay in their step
+            // nothing moves between the steps, nor the reads behind the products: left alone,
+            // the reads sink to where they are waited for (8192 tokens of 4096 -> 4096: 296
+            // against 289 us; groups of 32, 2048 tokens of 5120 -> 10240: 399 against 349)
+            // (fp32, whose steps hold three times the x, keeps to the order of its reads only)
+            constexpr int FREE = PIECES == 1 ? 0 : 0xf;
+            __builtin_amdgcn_sched_barrier(FREE);
             const int mt = step / SPB, sub = step % SPB;
             if (!DX && step == STEPS / 2) {
                 store_x(fill, 1);
                 load_x((k + 3) * KW + kg, 0);
             }
-            if (SPREAD && step > 0 && step < 3) {
-                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xn[0], ones, sum, 0, 0, 0);
-                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xn[1], ones, sum, 0, 0, 0);
-            }
-            if (SPREAD && step < 2) {
-                xn[0] = x_frag(next, 0, wn * 16, 2 * step);
-                xn[1] = x_frag(next, 0, wn * 16, 2 * step + 1);
-            }
-            if (SPREAD && step == 3)
-                store_sum(sum, k + 1, 0);
             if (step + 1 < STEPS) {
                 read_x(cur, k, step + 1);
             } else {
                 landed();
                 read_x(next, k + 1, 0);
             }
+            if constexpr (PIECES == 1)
+                __builtin_amdgcn_sched_barrier(0);
             f32x4 acc[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -799,6 +817,9 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
     // tokens, which fit the stages.  Lane l holds tokens 4 (l / 16) .. + 3 of column
     // l % 16 of each block.
     float *red = (float *)lds;                    // [KW][P][BM / 2][RN]
+    constexpr int PASSES = (BM / 2 * BN / 4 + 256 * KW - 1) / (256 * KW);
+    static_assert(2 * PASSES <= 32, "a bit for each of a thread's fours");
+    uint32_t again = 0;                           // fours with a sum that is not finite
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         landed();                                 // the last reads of the stages, or of the first half
@@ -811,10 +832,12 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
                     red[((kg * P + n / NP) * (BM / 2) + mt * 16 + 4 * g + r) * RN + (wn * NP + n % NP) * 16 + row] =
                         tot[half * (MT / 2) + mt][n][r];
         __syncthreads();
-        for (int e = threadIdx.x; e < BM / 2 * BN / 4; e += 256 * KW) {
+#pragma unroll
+        for (int pass = 0; pass < PASSES; ++pass) {
+            const int e = threadIdx.x + pass * (256 * KW);
             const int r = e / (BN / 4), c = e % (BN / 4) * 4;
             const int t = t0 + half * (BM / 2) + r, col = c_tile * BN + c;
-            if (t >= a.T || col >= d_out)
+            if (e >= BM / 2 * BN / 4 || t >= a.T || col >= d_out)
                 continue;
             f32x4 v[P];
 #pragma unroll
@@ -824,8 +847,17 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
                 for (int w = 0; w < KW; ++w)
                     v[p] += *(const f32x4 *)&red[((w * P + p) * (BM / 2) + r) * RN + c];
             }
-            finish<XT, SPB, GATED>(a, mi, v, t, col);
+            if (!finish_finite<XT, SPB, GATED>(a, mi, v, t, col))
+                again |= 1u << (half * PASSES + pass);
         }
+    }
+    // behind the sums' last use, so that the call costs the rest no registers
+    while (again) {
+        const int bit = __builtin_ctz(again);
+        again &= again - 1;
+        const int e = threadIdx.x + bit % PASSES * (256 * KW);
+        finish_again<XT, SPB, GATED>(a, mi, t0 + bit / PASSES * (BM / 2) + e / (BN / 4),
+                                     c_tile * BN + e % (BN / 4) * 4);
     }
 }
 
@@ -1056,7 +1088,8 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
             for (int w = 0; w < KW; ++w)
                 v[p] += *(const f32x4 *)&red[((w * P + p) * BM + r) * RN + c];
         }
-        finish<uint16_t, SPB, GATED>(a, mi, v, t, col);
+        if (!finish_finite<uint16_t, SPB, GATED>(a, mi, v, t, col))
+            finish_again<uint16_t, SPB, GATED>(a, mi, t, col);
     }
 }
 
