@@ -400,17 +400,19 @@ int lora_apply_group_noalloc(lora_ctx *ctx, int32_t n, const int32_t *modules,
  * until lora_sync_loads returns (or a later call on a stream that waited for the
  * load has completed).  A bf16 ctx holds scales with 16 significant bits: exact
  * for scales that came from fp16 or bf16, else off by at most 2^-16 of their
- * value.  Asynchronous on the ctx's side stream, with the ordering and the
- * capture rule of lora_slot_load; a load over a weight in use waits for the
- * base products already enqueued.  Storage (d_out x d_in / 2 bytes and 4 or 8
+ * value.  Asynchronous on the ctx's side stream, with the capture rule of
+ * lora_slot_load: later base products wait for it, and a load over a weight in use
+ * waits for the base products already enqueued.  Slot loads and base products do
+ * not wait for each other.  Storage (d_out x d_in / 2 bytes and 4 or 8
  * bytes per scale, the sizes rounded up to 16 and 128) is allocated at the
  * module's first load, and again by a load whose scales need more; all of it is
  * kept until lora_slots_destroy.  A graph captured before a reload sees the new
  * weights if group_size and the presence of a bias are as before; any other
  * reload needs a new capture.  A load does not touch slots, adapters or saved
  * modules.
- * Errors: LORA_ERR_BAD_MODULE; q or scale NULL or a bad group_size ->
- * LORA_ERR_INVALID_ARGUMENT; LORA_ERR_HOST_NOT_PINNED; LORA_ERR_OUT_OF_MEMORY.
+ * Errors: LORA_ERR_BAD_MODULE; q or scale NULL, a bad group_size or a d_in above
+ * 2^22 -> LORA_ERR_INVALID_ARGUMENT; LORA_ERR_HOST_NOT_PINNED;
+ * LORA_ERR_OUT_OF_MEMORY.
  */
 int lora_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scale,
                    const uint8_t *zero, int32_t group_size, const void *bias);

@@ -185,6 +185,15 @@ def _stream(stream) -> Optional[int]:
     return int(stream.cuda_stream) or None
 
 
+def _stream_of(stream, t) -> Optional[int]:
+    """As _stream, but without one given the current stream of t's device, which need not
+    be the current device."""
+    if stream is None and t is not None and not isinstance(t, int) and t.is_cuda:
+        import torch
+        return int(torch._C._cuda_getCurrentRawStream(t.device.index)) or None
+    return _stream(stream)
+
+
 def _require_cuda(t, name, dtype=None, numel=None):
     if isinstance(t, int):
         return
@@ -386,8 +395,9 @@ def lora_base_load(ctx, module: int, q, scale, zero=None, group_size: int = 128,
                    bias=None) -> None:
     """A module's 4-bit base weight: q uint8 [d_out][d_in / 2], scale float32 and zero
     uint8 (or None: 8) [d_out][groups], bias [d_out] of the ctx dtype or None; pinned
-    host or device tensors.  Device tensors may still be in the making on the current
-    stream of their device: this call waits for it on the host."""
+    host or device tensors that stay alive and unmodified until lora_sync_loads.  Device
+    tensors may still be in the making on the current stream of their device: this call
+    waits for it on the host."""
     import torch
     for name, t, dtype in (("q", q, torch.uint8), ("scale", scale, torch.float32),
                            ("zero", zero, torch.uint8), ("bias", bias, None)):
@@ -426,7 +436,7 @@ def lora_base(ctx, x, y, module: int, add=None, n_tokens: Optional[int] = None,
         if t is not None:
             _require_cuda(t, name)
     _check(load_library().lora_base(ctx, _ptr(x), _ptr(add), _ptr(y), _rows(x, n_tokens),
-                                    int(module), _stream(stream)), ctx)
+                                    int(module), _stream_of(stream, x)), ctx)
 
 
 def lora_base_group(ctx, modules: Sequence[int], x: Sequence, y: Sequence,
@@ -436,7 +446,7 @@ def lora_base_group(ctx, modules: Sequence[int], x: Sequence, y: Sequence,
     n, mods, xp = _group(modules, x, "x")
     _, _, yp = _group(modules, y, "y")
     _check(load_library().lora_base_group(ctx, n, mods, xp, _add_ptrs(n, add), yp,
-                                          _rows(x[0], n_tokens), _stream(stream)), ctx)
+                                          _rows(x[0], n_tokens), _stream_of(stream, x[0])), ctx)
 
 
 def _activation(activation) -> int:
@@ -456,7 +466,7 @@ def lora_base_gated(ctx, gate_module: int, up_module: int, x, y, gate_add=None, 
     _check(load_library().lora_base_gated(ctx, int(gate_module), int(up_module), _ptr(x),
                                           _ptr(gate_add), _ptr(up_add), _ptr(y),
                                           _rows(x, n_tokens), _activation(activation),
-                                          _stream(stream)), ctx)
+                                          _stream_of(stream, x)), ctx)
 
 
 def lora_rotary_init(head_dim: int, rotary_dim: Optional[int] = None, layout="half",
@@ -492,7 +502,8 @@ def lora_rotary_group(ctx, rotary: Rotary, modules: Sequence[int], x: Sequence, 
     n, mods, xp = _group(modules, x, "x")
     _, _, yp = _group(modules, y, "y")
     _check(load_library().lora_rotary_group(ctx, ctypes.byref(rotary), n, mods, xp, yp,
-                                            _ptr(positions), int(n_tokens), _stream(stream)), ctx)
+                                            _ptr(positions), int(n_tokens),
+                                            _stream_of(stream, positions)), ctx)
 
 
 def lora_get_device_flags(ctx) -> int:
@@ -531,6 +542,8 @@ class Slots:
         self.modules = [(int(a), int(b)) for a, b in modules]
         self.dtype = dtype
         self.max_loras, self.max_rank, self.max_tokens = max_loras, max_rank, max_tokens
+        self.device = int(device)
+        self._loading = []       # sources of base loads that may still be read
         self.ctx = lora_slots_create(max_loras, max_rank, self.modules,
                                      LORA_BF16 if dtype == "bf16" else LORA_FP32, max_tokens,
                                      device)
@@ -549,6 +562,7 @@ class Slots:
 
     def sync_loads(self):
         lora_sync_loads(self.ctx)
+        self._loading.clear()
 
     def prepare(self, idx, n_tokens=None, stream=None, used_slots=None):
         if used_slots is None:
@@ -581,6 +595,7 @@ class Slots:
         lora_apply_group_noalloc(self.ctx, modules, x, y, idx, n_tokens, stream)
 
     def load_base(self, module, q, scale, zero=None, group_size=128, bias=None):
+        """lora_base_load; the tensors are kept alive until sync_loads."""
         d_in, d_out = self.modules[module]
         groups = -(-d_in // (group_size or d_in)) if group_size >= 0 else 1
         for name, t, shape in (("q", q, (d_out, d_in // 2)), ("scale", scale, (d_out, groups)),
@@ -589,6 +604,7 @@ class Slots:
                 raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
         if bias is not None and not isinstance(bias, int) and bias.dtype != self.torch_dtype():
             raise ValueError(f"bias has dtype {bias.dtype}, expected {self.torch_dtype()}")
+        self._loading.append((q, scale, zero, bias))
         lora_base_load(self.ctx, module, q, scale, zero, group_size, bias)
 
     def torch_dtype(self):
@@ -598,6 +614,8 @@ class Slots:
     def _check_rows(self, name, t, n_tokens, width):
         if t is not None:
             _require_cuda(t, name, self.torch_dtype(), n_tokens * width)
+            if not isinstance(t, int) and t.device.index != self.device:
+                raise ValueError(f"{name} is on {t.device}, the slot pool on device {self.device}")
 
     def _check_members(self, modules, x, y, add, n_tokens):
         for i, m in enumerate(modules):
@@ -655,15 +673,15 @@ class Slots:
         return call
 
     def bind_base(self, modules, x, y, add=None, n_tokens=None, stream=None):
-        """base_group with its arguments marshalled once, as bind_step does: returns a
-        function that makes the library call."""
+        """base_group with its arguments marshalled and its stream taken once, as bind_step
+        does: returns a function that makes the library call."""
         n_tok = _rows(x[0], n_tokens)
         self._check_members(modules, x, y, add, n_tok)
         n, mods, xp = _group(modules, x, "x")
         _, _, yp = _group(modules, y, "y")
         return self._bound(load_library().lora_base_group,
-                           (n, mods, xp, _add_ptrs(n, add), yp, n_tok, _stream(stream)),
-                           (x, y, add))
+                           (n, mods, xp, _add_ptrs(n, add), yp, n_tok,
+                            _stream_of(stream, x[0])), (x, y, add))
 
     def bind_gated(self, gate_module, up_module, x, y, gate_add=None, up_add=None,
                    activation="silu", n_tokens=None, stream=None):
@@ -672,7 +690,7 @@ class Slots:
         self._check_gated(gate_module, up_module, x, y, gate_add, up_add, n_tok)
         return self._bound(load_library().lora_base_gated,
                            (int(gate_module), int(up_module), _ptr(x), _ptr(gate_add), _ptr(up_add),
-                            _ptr(y), n_tok, _activation(activation), _stream(stream)),
+                            _ptr(y), n_tok, _activation(activation), _stream_of(stream, x)),
                            (x, y, gate_add, up_add))
 
     def bind_rotary(self, rotary, modules, x, y, positions, n_tokens=None, stream=None):
@@ -683,7 +701,7 @@ class Slots:
         _, _, yp = _group(modules, y, "y")
         return self._bound(load_library().lora_rotary_group,
                            (ctypes.byref(rotary), n, mods, xp, yp, _ptr(positions), n_tok,
-                            _stream(stream)), (rotary, x, y, positions))
+                            _stream_of(stream, positions)), (rotary, x, y, positions))
 
     def bind_step(self, groups, idx, stream=None, prepare=True, fused=False):
         """One step with its arguments marshalled once: lora_plan_prepare of idx

@@ -111,7 +111,11 @@ __global__ __launch_bounds__(256) void base_pack_scale_kernel(BasePackArgs a)
     if constexpr (BF16) {
         // 16 significant bits, to nearest; the freed byte holds 16 + z
         const uint32_t bits = __float_as_uint(s);
-        const uint32_t kept = s != s ? 0x7fc00000u : (bits + 0x80u) & 0xffffff00u;
+        uint32_t kept = (bits + 0x80u) & 0xffffff00u;
+        if (s != s)
+            kept = 0x7fc00000u;
+        else if ((kept & 0x7fffffffu) == 0x7f800000u)
+            kept = bits & 0xffffff00u;             // the largest numbers stay finite
         ((uint32_t *)a.sc_out)[i] = kept | (16u + z);
     } else {
         ((float2 *)a.sc_out)[i] = make_float2(s, 16.f + (float)z);

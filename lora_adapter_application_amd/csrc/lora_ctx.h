@@ -21,6 +21,7 @@ struct StreamState {
     bool since_fence;       // launched on since the side stream last waited for it
     hipEvent_t tail;        // recorded at load time to fence the stream's tail
     bool base_since_load;   // launched a base product since the last base load
+    uint64_t base_waited;   // base-load generation this stream has waited for
 };
 
 struct DeviceGuard {
@@ -120,6 +121,8 @@ struct lora_ctx {
     int64_t prof_untimed = 0;
     std::string last_error;
     std::vector<lora::BasePack> base;        // per module its 4-bit base weight (lora_base_load)
+    hipEvent_t base_done = nullptr;          // the last base load; slot loads have load_done
+    uint64_t base_gen = 0, base_synced = 0;  // base loads, and those the host has seen complete
     std::vector<void *> allocations;
     uint32_t flags_host = 0;                 // lora_get_device_flags' copy of the sticky word
 };

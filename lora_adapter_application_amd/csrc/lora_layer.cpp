@@ -3,16 +3,18 @@
 // (lora_base_*), and rotary positions (lora_rotary_*).
 //
 // Base weights belong to the ctx's modules.  They have the ctx's ordering
-// without host synchronisation: a load runs on the side stream and records the
-// ctx's load event, which every later launch's stream waits for once; before it
-// overwrites weights the side stream waits for the tail of each stream that has
-// launched a base product since the last base load.  Slot loads do not wait for
-// base products, which read no slot.
+// without host synchronisation, apart from that of the slots: a load runs on the
+// side stream and records an event of its own, which the stream of every later
+// base product waits for once; before it overwrites weights the side stream waits
+// for the tail of each stream that has launched a base product since the last base
+// load.  Slot loads and base products do not wait for each other: the adapters that
+// a step misses can be uploaded under its base products.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <new>
 
 #include "../../include/lora_mi355x.h"
 #include "lora_ctx.h"
@@ -30,20 +32,20 @@ bool overlap(const void *p, size_t pb, const void *q, size_t qb)
     return (uintptr_t)p < (uintptr_t)q + qb && (uintptr_t)q < (uintptr_t)p + pb;
 }
 
-// Make stream s wait for the loads issued so far.  Under capture the load event,
-// recorded outside the capture, cannot be waited for: loads must be complete.
-int wait_loads(lora_ctx *c, hipStream_t s, bool reads_base)
+// Make stream s wait for the base loads issued so far.  Under capture the load
+// event, recorded outside the capture, cannot be waited for: loads must be complete.
+int before_layer_launch(lora_ctx *c, hipStream_t s, bool reads_base)
 {
     StreamState *st = stream_state(c, s);
     if (!st)
         return fail(c, LORA_ERR_HIP, "hipEventCreateWithFlags failed");
-    if (reads_base && st->waited_gen < c->load_gen && c->synced_gen < c->load_gen) {
+    if (reads_base && st->base_waited < c->base_gen && c->base_synced < c->base_gen) {
         if (stream_capturing(s))
             return fail(c, LORA_ERR_INVALID_ARGUMENT,
-                        "loads pending on a stream under graph capture: call lora_sync_loads "
+                        "base loads pending on a stream under graph capture: call lora_sync_loads "
                         "before the capture");
-        HIP_TRY(c, hipStreamWaitEvent(s, c->load_done, 0));
-        st->waited_gen = c->load_gen;
+        HIP_TRY(c, hipStreamWaitEvent(s, c->base_done, 0));
+        st->base_waited = c->base_gen;
     }
     if (reads_base)
         st->base_since_load = true;
@@ -92,6 +94,7 @@ BaseMember base_member(const lora_ctx *c, int32_t module, const void *x, const v
 // Device memory the ctx keeps until it is destroyed.
 int base_alloc(lora_ctx *c, void **p, size_t bytes, int32_t module)
 {
+    c->allocations.reserve(c->allocations.size() + 1);
     const hipError_t e = hipMalloc(p, bytes);
     if (e != hipSuccess) {
         (void)hipGetLastError();
@@ -104,11 +107,20 @@ int base_alloc(lora_ctx *c, void **p, size_t bytes, int32_t module)
     return LORA_OK;
 }
 
-}  // namespace
+// The host containers may throw: nothing leaves a C entry but a status.
+template <typename F>
+int guarded(F &&f) noexcept
+{
+    try {
+        return f();
+    } catch (const std::bad_alloc &) {
+        return LORA_ERR_OUT_OF_MEMORY;
+    } catch (...) {
+        return LORA_ERR_HIP;
+    }
+}
 
-extern "C" {
-
-int lora_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scale,
+int do_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scale,
                    const uint8_t *zero, int32_t group_size, const void *bias)
 {
     if (check_ctx(ctx))
@@ -149,6 +161,8 @@ int lora_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *sc
     const int groups = ceil_div(sh.d_in, group);
     const int spb = group >= kBaseK ? 1 : kBaseK / group;
     const size_t word = bf16 ? 4 : 8;
+    if (!ctx->base_done)
+        HIP_TRY(ctx, hipEventCreateWithFlags(&ctx->base_done, hipEventDisableTiming));
     if (ctx->base.empty())
         ctx->base.resize(ctx->n_modules);
     BasePack &p = ctx->base[module];
@@ -218,15 +232,15 @@ int lora_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *sc
     if (bias)
         HIP_TRY(ctx, hipMemcpyAsync(p.bias, bias, (size_t)sh.d_out * ctx->elem, hipMemcpyDefault,
                                     ctx->side));
-    HIP_TRY(ctx, hipEventRecord(ctx->load_done, ctx->side));
-    ctx->load_gen += 1;
+    HIP_TRY(ctx, hipEventRecord(ctx->base_done, ctx->side));
+    ctx->base_gen += 1;
     p.spb = spb;
     p.has_bias = bias != nullptr;
     p.zero = zero != nullptr;
     return LORA_OK;
 }
 
-int lora_base_group(lora_ctx *ctx, int32_t n, const int32_t *modules, const void *const *x,
+int do_base_group(lora_ctx *ctx, int32_t n, const int32_t *modules, const void *const *x,
                     const void *const *add, void *const *y, int32_t n_tokens, void *stream)
 {
     if (check_ctx(ctx))
@@ -257,7 +271,7 @@ int lora_base_group(lora_ctx *ctx, int32_t n, const int32_t *modules, const void
         }
     DeviceGuard guard(ctx->device);
     hipStream_t s = (hipStream_t)stream;
-    if ((rc = wait_loads(ctx, s, true)))
+    if ((rc = before_layer_launch(ctx, s, true)))
         return rc;
     for (int spb = 1; spb <= 4; spb *= 2) {
         BaseArgs a;
@@ -266,9 +280,7 @@ int lora_base_group(lora_ctx *ctx, int32_t n, const int32_t *modules, const void
         for (int i = 0; i < n; ++i) {
             if (ctx->base[modules[i]].spb != spb)
                 continue;
-            a.m[a.n] = base_member(ctx, modules[i], x[i], add ? add[i] : nullptr, y[i]);
-            a.col_start[a.n + 1] = a.col_start[a.n] + ceil_div(a.m[a.n].d_out, kBaseCols);
-            ++a.n;
+            a.m[a.n++] = base_member(ctx, modules[i], x[i], add ? add[i] : nullptr, y[i]);
         }
         if (a.n)
             HIP_TRY(ctx, launch_base(ctx->dtype == LORA_BF16, false, spb, a, s));
@@ -276,13 +288,13 @@ int lora_base_group(lora_ctx *ctx, int32_t n, const int32_t *modules, const void
     return LORA_OK;
 }
 
-int lora_base(lora_ctx *ctx, const void *x, const void *add, void *y, int32_t n_tokens,
+int do_base(lora_ctx *ctx, const void *x, const void *add, void *y, int32_t n_tokens,
               int32_t module, void *stream)
 {
-    return lora_base_group(ctx, 1, &module, &x, &add, &y, n_tokens, stream);
+    return do_base_group(ctx, 1, &module, &x, &add, &y, n_tokens, stream);
 }
 
-int lora_base_gated(lora_ctx *ctx, int32_t gate_module, int32_t up_module, const void *x,
+int do_base_gated(lora_ctx *ctx, int32_t gate_module, int32_t up_module, const void *x,
                     const void *gate_add, const void *up_add, void *y, int32_t n_tokens,
                     int32_t activation, void *stream)
 {
@@ -315,7 +327,7 @@ int lora_base_gated(lora_ctx *ctx, int32_t gate_module, int32_t up_module, const
             return fail(ctx, LORA_ERR_INVALID_ARGUMENT, "y overlaps an add buffer that it is not");
     DeviceGuard guard(ctx->device);
     hipStream_t s = (hipStream_t)stream;
-    if ((rc = wait_loads(ctx, s, true)))
+    if ((rc = before_layer_launch(ctx, s, true)))
         return rc;
     BaseArgs a;
     std::memset(&a, 0, sizeof a);
@@ -324,12 +336,11 @@ int lora_base_gated(lora_ctx *ctx, int32_t gate_module, int32_t up_module, const
     a.act = activation;
     a.m[0] = base_member(ctx, gate_module, x, gate_add, y);
     a.m[1] = base_member(ctx, up_module, x, up_add, y);
-    a.col_start[1] = a.col_start[2] = ceil_div(sg.d_out, kBaseCols);
     HIP_TRY(ctx, launch_base(ctx->dtype == LORA_BF16, true, ctx->base[gate_module].spb, a, s));
     return LORA_OK;
 }
 
-int lora_rotary_init(lora_rotary *out, const lora_rotary_params *p)
+int do_rotary_init(lora_rotary *out, const lora_rotary_params *p)
 {
     fail(nullptr, 0, "%s", "");
     auto bad = [](const char *what) { return fail(nullptr, LORA_ERR_INVALID_ARGUMENT, "%s", what); };
@@ -395,7 +406,7 @@ int lora_rotary_init(lora_rotary *out, const lora_rotary_params *p)
     return LORA_OK;
 }
 
-int lora_rotary_group(lora_ctx *ctx, const lora_rotary *rotary, int32_t n, const int32_t *modules,
+int do_rotary_group(lora_ctx *ctx, const lora_rotary *rotary, int32_t n, const int32_t *modules,
                       const void *const *x, void *const *y, const int32_t *positions,
                       int32_t n_tokens, void *stream)
 {
@@ -448,10 +459,51 @@ int lora_rotary_group(lora_ctx *ctx, const lora_rotary *rotary, int32_t n, const
     }
     DeviceGuard guard(ctx->device);
     hipStream_t s = (hipStream_t)stream;
-    if ((rc = wait_loads(ctx, s, false)))
+    if ((rc = before_layer_launch(ctx, s, false)))
         return rc;
     HIP_TRY(ctx, launch_rotary(ctx->dtype == LORA_BF16, vec, a, s));
     return LORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int lora_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scale,
+                   const uint8_t *zero, int32_t group_size, const void *bias)
+{
+    return guarded([&] { return do_base_load(ctx, module, q, scale, zero, group_size, bias); });
+}
+
+int lora_base_group(lora_ctx *ctx, int32_t n, const int32_t *modules, const void *const *x,
+                    const void *const *add, void *const *y, int32_t n_tokens, void *stream)
+{
+    return guarded([&] { return do_base_group(ctx, n, modules, x, add, y, n_tokens, stream); });
+}
+
+int lora_base(lora_ctx *ctx, const void *x, const void *add, void *y, int32_t n_tokens,
+              int32_t module, void *stream)
+{
+    return guarded([&] { return do_base(ctx, x, add, y, n_tokens, module, stream); });
+}
+
+int lora_base_gated(lora_ctx *ctx, int32_t gate_module, int32_t up_module, const void *x,
+                    const void *gate_add, const void *up_add, void *y, int32_t n_tokens,
+                    int32_t activation, void *stream)
+{
+    return guarded([&] { return do_base_gated(ctx, gate_module, up_module, x, gate_add, up_add, y, n_tokens, activation, stream); });
+}
+
+int lora_rotary_init(lora_rotary *out, const lora_rotary_params *p)
+{
+    return guarded([&] { return do_rotary_init(out, p); });
+}
+
+int lora_rotary_group(lora_ctx *ctx, const lora_rotary *rotary, int32_t n, const int32_t *modules,
+                      const void *const *x, void *const *y, const int32_t *positions,
+                      int32_t n_tokens, void *stream)
+{
+    return guarded([&] { return do_rotary_group(ctx, rotary, n, modules, x, y, positions, n_tokens, stream); });
 }
 
 }  // extern "C"

@@ -67,9 +67,8 @@ struct BaseMember {
 
 struct BaseArgs {
     BaseMember m[kMaxGroup];     // gated: m[0] gate, m[1] up, y in m[0]
-    int32_t col_start[kMaxGroup + 1];   // column blocks of the members before member i
-    int32_t tile_start[kMaxGroup + 1];  // many tokens: column tiles of the members before member i
-    int32_t items;                      // and work items (set by the launch)
+    int32_t tile_start[kMaxGroup + 1];  // column tiles of the members before member i, and
+    int32_t items;                      // work items (both set by the launch)
     int32_t n;
     int32_t T;
     int32_t act;                 // gated: LORA_ACT_*

@@ -72,7 +72,7 @@ StreamState *stream_state(lora_ctx *c, hipStream_t s)
     for (auto &st : c->streams)
         if (st.stream == s)
             return &st;
-    StreamState st{s, 0, false, false, nullptr, false};
+    StreamState st{s, 0, false, false, nullptr, false, 0};
     if (hipEventCreateWithFlags(&st.tail, hipEventDisableTiming) != hipSuccess)
         return nullptr;
     c->streams.push_back(st);
@@ -219,6 +219,9 @@ void free_all(lora_ctx *c)
         }
     if (c->load_done)
         (void)hipEventDestroy(c->load_done);
+    if (c->base_done)
+        (void)hipEventDestroy(c->base_done);
+    c->base_done = nullptr;
     if (c->side)
         (void)hipStreamDestroy(c->side);
     c->load_done = nullptr;
@@ -1065,6 +1068,7 @@ int lora_sync_loads(lora_ctx *ctx)
     DeviceGuard guard(ctx->device);
     HIP_TRY(ctx, hipStreamSynchronize(ctx->side));
     ctx->synced_gen = ctx->load_gen;
+    ctx->base_synced = ctx->base_gen;
     return LORA_OK;
 }
 

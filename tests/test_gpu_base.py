@@ -87,6 +87,107 @@ def test_integers_are_exact(dtype, tokens, d_in, outs, group, zero, bias, add):
             intact()
 
 
+# One case for each way the library multiplies (by tokens, columns and alignment), each
+# with one, two and four groups a block of 128 inputs, with and without zero points.
+WAYS = [
+    # dtype, tokens, d_out: what takes it
+    ("bf16", 3, 8200),       # few tokens, four column blocks a workgroup
+    ("bf16", 16, 8200),
+    ("bf16", 129, 2056),     # split, 32 x 64
+    ("bf16", 257, 2056),     # split, 32 x 128
+    ("bf16", 513, 2056),     # split, 64 x 128
+    ("bf16", 1025, 2056),    # split, 64 x 256
+    ("bf16", 2049, 2056),    # tiles
+    ("fp32", 5, 8200),       # few tokens, four column blocks a workgroup
+    ("fp32", 17, 8200),      # tiles, K halved
+    ("fp32", 129, 8200),     # tiles
+]
+
+
+@pytest.mark.parametrize("group,zero", [(0, True), (128, False), (64, True), (64, False),
+                                        (32, True), (32, False)])
+@pytest.mark.parametrize("dtype,tokens,d_out", WAYS)
+def test_every_way_is_exact_on_integers(dtype, tokens, d_out, group, zero):
+    d_in = 520 if group else 1000
+    log("case", dtype, tokens, d_out, group, zero)
+    w, x, b, a = make(dtype, tokens, d_in, [d_out], group, zero, True, True, tokens + group, True)
+    with binding.Slots(1, 1, [(d_in, d_out)], dtype, tokens) as S:
+        load_all(S, w, group, b)
+        y, intact = guarded(tokens, d_out, TORCH[dtype])
+        S.base(x[0].cuda(), y, 0, a[0].cuda())
+        # the 64-bit sums on the device, where they are quick
+        v = torch.stack((w[0][0] & 15, w[0][0] >> 4), 2).view(d_out, d_in).double()
+        of = torch.arange(d_in) // (group or d_in)
+        z = 8.0 if w[0][2] is None else w[0][2].double()[:, of]
+        full = ((v - z) * w[0][1].double()[:, of]).cuda()
+        want = x[0].cuda().double() @ full.t().contiguous() + b[0].cuda().double() + a[0].cuda().double()
+        assert torch.equal(y, want.float().to(TORCH[dtype]))
+        intact()
+
+
+@pytest.mark.parametrize("tokens", [20, 64, 65, 200])
+def test_unaligned_rows_are_exact_on_integers(tokens):
+    for group, zero, d_in in ((128, True, 520), (64, False, 392), (32, True, 264)):
+        w, x, _, _ = make("bf16", tokens, d_in, [264], group, zero, False, False, tokens, True)
+        with binding.Slots(1, 1, [(d_in, 264)], "bf16", tokens) as S:
+            load_all(S, w, group, [None])
+            xs, _ = guarded(tokens, d_in, torch.bfloat16, 1)
+            xs.copy_(x[0])
+            y, intact = guarded(tokens, 264, torch.bfloat16, 5)
+            S.base(xs, y, 0)
+            want, _ = base_sum(x[0], w[0], d_in, group)
+            assert torch.equal(y.cpu(), want.float().bfloat16()), (group, zero)
+            intact()
+
+
+@pytest.mark.parametrize("tokens,n", [(40, 2056), (600, 2056), (2100, 2056)])
+def test_nonfinite_rows_in_large_batches(tokens, n):
+    """A NaN row, an infinity at the end of a row, and a batch of NaN: quick, and the rows
+    beside them keep their bits."""
+    d_in = 520
+    w, x, _, a = make("bf16", tokens, d_in, [n], 128, True, False, True, 7, True)
+    with binding.Slots(1, 1, [(d_in, n)], "bf16", tokens) as S:
+        load_all(S, w, 128, [None])
+        clean = torch.empty(tokens, n, dtype=torch.bfloat16, device="cuda")
+        S.base(x[0].cuda(), clean, 0, a[0].cuda())
+        bad = x[0].clone()
+        bad[3, 0] = float("nan")
+        bad[tokens - 1, d_in - 1] = float("inf")
+        y = a[0].cuda()
+        S.base(bad.cuda(), y, 0, y)
+        keep = torch.ones(tokens, dtype=torch.bool)
+        keep[3] = keep[tokens - 1] = False
+        assert torch.equal(y[keep.cuda()], clean[keep.cuda()])
+        assert bool(y[3].isnan().all())
+        d = (w[0][0][:, -1] >> 4).double() - w[0][2][:, -1].double()    # the last input's weights
+        last = y[tokens - 1].cpu()
+        assert torch.equal(last.isnan(), d == 0)
+        assert bool((last[d > 0] == float("inf")).all()) and bool((last[d < 0] == float("-inf")).all())
+        bad[:] = float("nan")
+        S.base(bad.cuda(), y, 0)
+        assert bool(y.isnan().all())
+
+
+def test_scales_of_a_bf16_pool():
+    """16 significant bits of a float32 scale, to nearest; the largest stays finite, and an
+    infinite or NaN scale acts as one."""
+    s = torch.tensor([1 + 2.0 ** -15, 1 + 2.0 ** -16 + 2.0 ** -20, torch.finfo(torch.float32).max,
+                      float("inf"), float("nan"), -0.75, 0.0, 2.0 ** -100]).view(8, 1)
+    q = torch.full((8, 8), 0x99, dtype=torch.uint8)            # 9 - 8 = 1
+    x = torch.zeros(1, 16).bfloat16()
+    x[0, 0] = 1.0
+    with binding.Slots(1, 1, [(16, 8)], "bf16", 1) as S:
+        S.load_base(0, q.cuda(), s.cuda(), None, 0)
+        add = torch.full((1, 8), -1.0).bfloat16().cuda()       # 1 + 2^-15 - 1 needs the kept bits
+        y = torch.empty(1, 8, dtype=torch.bfloat16, device="cuda")
+        S.base(x.cuda(), y, 0, add)
+        y = y.cpu()[0]
+    assert y[0] == 2.0 ** -15 and y[1] == 2.0 ** -15
+    assert y[2].double() >= 3.3e38 or y[2] == float("inf")     # bf16 of the largest float32
+    assert y[3] == float("inf") or y[3].isnan()                # inf * 0 of the other inputs
+    assert y[4].isnan() and y[5] == -1.75 and y[6] == -1.0 and y[7] == -1.0
+
+
 CLOSE = [
     ("bf16", 1, 4096, [4096], 128, True, False, False),
     ("bf16", 5, 11008, [264], 128, True, True, True),

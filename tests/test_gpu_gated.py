@@ -91,6 +91,31 @@ def test_gated(dtype, tokens, d_in, d_out, group, zero, bias, gadd, uadd, act):
         check_within(y, want, bound, "one module twice")
 
 
+# One case for each way the library multiplies.
+WAYS = [("bf16", 9, 8200), ("bf16", 129, 4104), ("bf16", 257, 4104), ("bf16", 1025, 4104),
+        ("fp32", 9, 8200), ("fp32", 17, 8200), ("fp32", 65, 8200)]
+
+
+@pytest.mark.parametrize("group,zero", [(0, True), (128, False), (64, True), (64, False),
+                                        (32, True), (32, False)])
+@pytest.mark.parametrize("dtype,tokens,d_out", WAYS)
+def test_every_way(dtype, tokens, d_out, group, zero):
+    d_in = 264
+    log("case", dtype, tokens, d_out, group, zero)
+    gen = torch.Generator().manual_seed(tokens + group)
+    w = [random_weight(gen, d_out, d_in, group, zero) for _ in range(2)]
+    x = torch.randn(tokens, d_in, generator=gen).to(TORCH[dtype])
+    a = [torch.randn(tokens, d_out, generator=gen).to(TORCH[dtype]) for _ in range(2)]
+    with binding.Slots(1, 1, [(d_in, d_out)] * 2, dtype, tokens) as S:
+        for i, (q, s, z) in enumerate(w):
+            S.load_base(i, q.cuda(), s.cuda(), None if z is None else z.cuda(), group)
+        y, intact = guarded(tokens, d_out, TORCH[dtype])
+        S.base_gated(0, 1, x.cuda(), y, a[0].cuda(), a[1].cuda())
+        want, bound = expected(x, w[0], w[1], [None] * 2, a, d_in, group, "silu")
+        check_within(y, want, bound, "gated")
+        intact()
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("tokens", [1, 80])
 def test_activations_far_from_zero(act, tokens):
