@@ -424,8 +424,9 @@ int lora_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *sc
  * y must not overlap x, and add must be y or apart from it.  Rows from n_tokens
  * on are left as they are; n_tokens == 0 is a no-op.  Products of x with q - zero
  * are summed in fp32 over each group, and the groups' sums are scaled and summed
- * in fp32; bf16 results are rounded once.  Infinities and NaNs in x give what
- * the formula gives.
+ * in fp32, in an order that goes by the launch's tokens and columns and by x's
+ * alignment alone (16 bytes is the fast one), so equal calls give equal bits; bf16
+ * results are rounded once.  Infinities and NaNs in x give what the formula gives.
  * Errors: a module without a base weight, n_tokens < 0, NULL x or y, overlapping
  * buffers -> LORA_ERR_INVALID_ARGUMENT; LORA_ERR_BAD_MODULE;
  * n_tokens > max_tokens -> LORA_ERR_TOO_MANY_TOKENS.
@@ -438,7 +439,7 @@ int lora_base(lora_ctx *ctx, const void *x, const void *add, void *y, int32_t n_
  * and v of a layer: modules with the same scale storage (group sizes 32; 64;
  * every other) share a launch.  add may be NULL, as may its entries.  A module
  * may appear more than once.  No y may overlap another member's x, add or y.
- * Results equal n single-module calls.
+ * Results are those of n single-module calls up to the order of their fp32 sums.
  */
 int lora_base_group(lora_ctx *ctx, int32_t n, const int32_t *modules, const void *const *x,
                     const void *const *add, void *const *y, int32_t n_tokens, void *stream);

@@ -280,7 +280,10 @@ __device__ __forceinline__ void finish_again(const BaseArgs &a, int mi, int t, i
 //
 // One workgroup = C blocks of 16 columns (of gate and of up when GATED) and
 // 16 MT tokens; its W waves take the K blocks in turn and join their sums in LDS.
-// Each wave keeps D blocks in flight.
+// Each wave keeps D blocks in flight.  Bytes bound it: one token through q, k and v of
+// 4096 -> 4096 (27 MB) takes 7.1 us, gate and up of 4096 -> 11008 (49 MB) 10.9 us, 3.8
+// and 4.5 TB/s with the launch and the first load's latency in it.  With more tokens
+// the bytes of x count, which every workgroup reads whole: see launch_sized.
 template <typename XT> struct RawX;        // eight inputs of a token as they were loaded
 template <> struct RawX<uint16_t> {
     u32x4 v;
@@ -517,10 +520,13 @@ hipError_t launch_few(const BaseArgs &args, hipStream_t st)
 // ---------------------------------------------------------------------------
 // products of many tokens
 //
-// One workgroup = 16 MT MW tokens x 4 waves of 64 columns (GATED: of 32 of gate
-// and the same 32 of up), MW waves above each other.  x is staged in LDS one K
-// block at a time and shared by the four column waves; each wave unpacks its own
-// weights straight from global memory into the registers its products read.
+// One workgroup = 16 MT tokens x 4 waves of 16 NT columns (GATED: half of them
+// gate's, half the same columns of up), in KW groups of four waves that take the K
+// blocks in turn and join their sums in LDS.  x is staged in LDS one K block at a
+// time and shared by the four column waves, by direct-to-LDS loads where x lies on a
+// 16-byte boundary (DX), else through registers; each wave unpacks its own weights
+// from global memory into the registers its products read, so a weight is unpacked
+// once per 16 MT tokens.
 //
 // A group's sum starts at -z' sum x instead of 0, so the zero points cost nothing
 // where every column has the same (ZERO false), and one multiplication per sum
@@ -529,11 +535,20 @@ hipError_t launch_few(const BaseArgs &args, hipStream_t st)
 // block by ones and leaves the result in LDS.
 //
 // Block k reads stage k % 3, sums stage (k + 1) % 3 and fills stage (k + 2) % 3,
-// which block k - 1 has read; one barrier a block.  16-byte piece p of stage row r
-// sits in slot p ^ (r & 15), so the 16 rows of an operand read fall on distinct
-// banks.
-// NT column blocks a wave (GATED: half of them gate's, half up's), KW groups of four
-// waves that take the K blocks in turn and join their sums in LDS.
+// which block k - 1 has read; one barrier a block, before its last products.  16-byte
+// piece p of stage row r sits in slot p ^ (r & 15), so the 16 rows of an operand read
+// fall on distinct banks.
+//
+// bf16 takes 64 x 256 tiles (MT = NT = 4), whose 64 fp32 sums, 64 registers of
+// unpacked weights and two steps of x fill the 256 registers of two waves a SIMD: two
+// workgroups a CU, each under the other's waits.  Measured on 8192 tokens: 4096 -> 4096
+// with a residual 301 us (913 TFLOP/s), gated 4096 -> 11008 1495 us (988 TFLOP/s; a
+// library's bf16 product of 8192^3 reaches 1375 on the same card).  The matrix cores
+// are busy half of the time and the vector unit, which unpacks, scales and also issues
+// the matrix instructions, 0.7 of it; taking out the reads of x from LDS gains 23%,
+// unpacking 10%, scaling 6%, the loads of x or w 8% each, so no single one bounds it.
+// One workgroup of eight waves on 128 x 256 with weights in LDS too was slower (1642
+// against 1562 us then).
 template <typename XT, int MT, int NT, int KW, int SPB, bool GATED, bool ZERO, bool DX>
 __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(BaseArgs a)
 {
@@ -865,11 +880,17 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
     }
 }
 
-// Products of a middling number of tokens (bf16, x on a 16-byte boundary): too few tiles
-// to fill the chip, so a workgroup splits the K blocks over KW groups of four waves,
+// ---------------------------------------------------------------------------
+// products of a middling number of tokens
+//
+// bf16, x on a 16-byte boundary, too few tiles to fill the chip: a workgroup of
+// 16 MT tokens x CW waves of 16 NT columns splits the K blocks over KW groups of waves,
 // and x, weights and scales are all brought to LDS by direct-to-LDS loads, S - 1 blocks
 // ahead and without registers.  Each wave forms the sums of x of all its rows itself,
-// in the block they belong to: at these sizes it waits for memory, not for products.
+// in the block they belong to.  24 tokens of 11008 -> 4096 take 15.7 us (few-token
+// kernel 19.4), 64 tokens of gated 4096 -> 11008 24.5 (54).  Per K block of a group the
+// LDS reads, the unpacking and a chain of products follow each other: that latency,
+// times the blocks of a group, is the time.
 //
 // Block k of a group lies in stage k % S; block k + S - 1 is loaded into the stage of
 // block k - 1 once every wave has read that.  Every wave issues the same number of loads
@@ -1154,7 +1175,7 @@ bool one_per_cu(const BaseArgs &args, int BM, int BN)
 // waits for its slowest workgroup (4096 -> 4096: 64 tokens 9.1 us on 32 x 32, 11.1 on
 // 32 x 64, 15.9 on 32 x 128 tiles; 256 tokens 30.3, 23.5, 18.9; 5120 -> 10240, 256
 // tokens: 55 on 64 x 128, 45 on 64 x 256); with more, the tile kernel, two workgroups
-// a CU (8192 tokens of 4096 -> 4096: 303 us against 330 on the 64 x 256 split).
+// a CU (8192 tokens of 4096 -> 4096: 303 us against 330 on the 64 x 256 split then).
 // x off a 16-byte boundary cannot be loaded to LDS directly and takes slower ways.
 template <typename XT, bool GATED, int SPB>
 hipError_t launch_sized(const BaseArgs &a, hipStream_t st)
@@ -1169,7 +1190,8 @@ hipError_t launch_sized(const BaseArgs &a, hipStream_t st)
     if (a.T <= 16) {
         if (blocks >= 2 * kCus && (WIDE || a.T > (GATED ? 8 : 2)))
             return launch_few<XT, 1, GATED && SPB == 4 ? 2 : 4, SPB, GATED, 8, 1>(a, st);
-        return launch_few<XT, 1, 1, SPB, GATED, 8, 2>(a, st);
+        // (gate and up in flight together: one token of 4096 -> 11008 10.9 us, 11.4 with two each)
+        return launch_few<XT, 1, 1, SPB, GATED, 8, GATED && !WIDE ? 1 : 2>(a, st);
     }
     if constexpr (WIDE) {
         // (24 tokens: 4096 -> 4096 16.8 us against 34, 5120 -> 10240 51 against 41; 128 tokens
