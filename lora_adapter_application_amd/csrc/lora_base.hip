@@ -888,9 +888,12 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
 // and x, weights and scales are all brought to LDS by direct-to-LDS loads, S - 1 blocks
 // ahead and without registers.  Each wave forms the sums of x of all its rows itself,
 // in the block they belong to.  24 tokens of 11008 -> 4096 take 15.7 us (few-token
-// kernel 19.4), 64 tokens of gated 4096 -> 11008 24.5 (54).  Per K block of a group the
+// kernel 19.4), 64 tokens of gated 4096 -> 11008 23.3 (54).  Per K block of a group the
 // LDS reads, the unpacking and a chain of products follow each other: that latency,
-// times the blocks of a group, is the time.
+// times the blocks of a group, is the time.  So LDS goes to groups before stages: with 2
+// stages of more groups in place of 3 or 4 of 2 groups, 100 tokens of 11008 -> 11008 take
+// 48.2 us (51.8), 64 tokens of it 33.8 (35.4), and 64 tokens of 4096 -> 11008 in groups of
+// 32 19.4 (22.7).  The small tiles, with 4 groups already, keep 3 or 4 stages.
 //
 // Block k of a group lies in stage k % S; block k + S - 1 is loaded into the stage of
 // block k - 1 once every wave has read that.  Every wave issues the same number of loads
@@ -1172,9 +1175,9 @@ bool one_per_cu(const BaseArgs &args, int BM, int BN)
 // column blocks of gate and of up are what the registers hold.
 //
 // Above that, the smallest tile of which every CU gets at most one, since such a batch
-// waits for its slowest workgroup (4096 -> 4096: 64 tokens 9.1 us on 32 x 32, 11.1 on
-// 32 x 64, 15.9 on 32 x 128 tiles; 256 tokens 30.3, 23.5, 18.9; 5120 -> 10240, 256
-// tokens: 55 on 64 x 128, 45 on 64 x 256); with more, the tile kernel, two workgroups
+// waits for its slowest workgroup (4096 -> 4096: 64 tokens 8.6 us on 32 x 32, 10.5 on
+// 32 x 64, 14.6 on 32 x 128 tiles; 256 tokens 27.7, 22.5, 18.1; 5120 -> 10240, 256
+// tokens: 54 on 64 x 128, 43 on 64 x 256); with more, the tile kernel, two workgroups
 // a CU (8192 tokens of 4096 -> 4096: 303 us against 330 on the 64 x 256 split then).
 // x off a 16-byte boundary cannot be loaded to LDS directly and takes slower ways.
 template <typename XT, bool GATED, int SPB>
@@ -1209,7 +1212,7 @@ hipError_t launch_sized(const BaseArgs &a, hipStream_t st)
             if (one_per_cu<true>(a, 32, 64))
                 return launch_split<true, SPB, 2, 2, 4, 4, 2>(a, st);
             if (one_per_cu<true>(a, 64, 64))
-                return launch_split<true, SPB, 4, 2, 4, 2, 3>(a, st);
+                return launch_split<true, SPB, 4, 2, 4, 3, 2>(a, st);
             if (one_per_cu<true>(a, 64, 128))
                 return launch_split<true, SPB, 4, 4, 4, 2, 2>(a, st);
         } else {
@@ -1218,9 +1221,9 @@ hipError_t launch_sized(const BaseArgs &a, hipStream_t st)
             if (one_per_cu<false>(a, 32, 64))
                 return launch_split<false, SPB, 2, 1, 4, 4, SPB == 1 ? 3 : 2>(a, st);
             if (one_per_cu<false>(a, 32, 128))
-                return launch_split<false, SPB, 2, 2, 4, 2, 4>(a, st);
+                return launch_split<false, SPB, 2, 2, 4, 4, 2>(a, st);
             if (one_per_cu<false>(a, 64, 128))
-                return launch_split<false, SPB, 4, 2, 4, 2, 3>(a, st);
+                return launch_split<false, SPB, 4, 2, 4, 3, 2>(a, st);
             if (one_per_cu<false>(a, 64, 256))
                 return launch_split<false, SPB, 4, 4, 4, 2, 2>(a, st);
         }
