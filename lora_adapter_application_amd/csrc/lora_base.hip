@@ -893,7 +893,10 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
 // times the blocks of a group, is the time.  So LDS goes to groups before stages: with 2
 // stages of more groups in place of 3 or 4 of 2 groups, 100 tokens of 11008 -> 11008 take
 // 48.2 us (51.8), 64 tokens of it 33.8 (35.4), and 64 tokens of 4096 -> 11008 in groups of
-// 32 19.4 (22.7).  The small tiles, with 4 groups already, keep 3 or 4 stages.
+// 32 19.4 (22.7).  The small tiles, with 4 groups already, keep 3 or 4 stages; the
+// largest, 64 x 384 on 8 waves of 48 columns, fill LDS with one group of 3 (4 waves of 96
+// columns, one a SIMD: 512 tokens of 5120 -> 10240 86.5 us against 68.5).  A wave takes NT
+// weight blocks in a row of gate's and then up's, so it may have blocks of one only.
 //
 // Block k of a group lies in stage k % S; block k + S - 1 is loaded into the stage of
 // block k - 1 once every wave has read that.  Every wave issues the same number of loads
@@ -905,10 +908,10 @@ template <int MT, int NT, int CW, int KW, int S, int SPB, bool GATED, bool ZERO>
 __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
 {
     constexpr int P = GATED ? 2 : 1;
-    constexpr int NP = NT / P;
-    constexpr int BM = 16 * MT, BN = 16 * CW * NP;
+    constexpr int WB = CW * NT;                   // weight blocks of a workgroup, gate's before up's
+    constexpr int CB = WB / P;                    // column blocks: wave w multiplies weight blocks NT w ..
+    constexpr int BM = 16 * MT, BN = 16 * CB;
     constexpr int NK = 4 / SPB;
-    constexpr int WB = CW * NT;                   // weight blocks of a workgroup
     constexpr int XL = BM / 4 / CW;               // loads of x a wave and block
     constexpr int kX = BM * kBaseK * 2, kW = WB * 1024, SL = (WB * SPB + 3) / 4, kS = SL * 256;
     constexpr int kStage = kX + kW + kS;          // LDS bytes of a group's stage
@@ -917,7 +920,8 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
     constexpr int kLds = S * kStage * KW > kJoin ? S * kStage * KW : kJoin;
     constexpr int SW = (SL + CW - 1) / CW;        // scale loads (SL of 256 bytes a block) of each wave
     constexpr int LOADS = XL + NT + SW;
-    static_assert(CW == 4 || !GATED, "a load of scales is of one weight");
+    static_assert(WB % P == 0 && BM / 4 % CW == 0, "");
+    static_assert(!GATED || CB * SPB % 4 == 0, "a load of scales is of one weight");
     static_assert((S - 2) * LOADS < 64, "vmcnt counts to 63");
     __shared__ __attribute__((aligned(16))) unsigned char lds[kLds];
 
@@ -959,16 +963,16 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
         x_row[i] = (uint32_t)min(r, a.T - 1 - t0) * (uint32_t)d_in * 2u;
         x_k[i] = (uint32_t)(((lane & 15) ^ (r & 15)) * 8);
     }
-    // weight block b of the workgroup: weight b / (CW NP), column block b % (CW NP)
+    // weight block b of the workgroup: weight b / CB, column block b % CB
     auto block_at = [&](int b) __attribute__((always_inline)) {
-        return (int64_t)min(c_tile * CW * NP + b % (CW * NP), nblocks - 1) * KB;
+        return (int64_t)min(c_tile * CB + b % CB, nblocks - 1) * KB;
     };
     const char *wsrc[NT], *ssrc[SW];
     uint32_t s_off[SW], s_at[SW];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int b = wn + CW * i;
-        wsrc[i] = (const char *)(GATED ? a.m[b / (CW * NP)] : m).q + block_at(b) * 1024;
+        wsrc[i] = (const char *)(GATED ? a.m[b / CB] : m).q + block_at(b) * 1024;
     }
 #pragma unroll
     for (int i = 0; i < SW; ++i) {
@@ -976,7 +980,7 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
         const int word = min(l * 64 + lane, WB * 16 * SPB - 1);   // word of the workgroup's scales
         const int b = word / (16 * SPB);
         const int b0 = l * 64 / (16 * SPB);       // the load's first block: all are of one weight
-        ssrc[i] = (const char *)(GATED ? a.m[b0 / (CW * NP)] : m).sc + block_at(b0) * (16 * SPB * 4);
+        ssrc[i] = (const char *)(GATED ? a.m[b0 / CB] : m).sc + block_at(b0) * (16 * SPB * 4);
         s_off[i] = (uint32_t)((block_at(b) - block_at(b0)) * (16 * SPB) + word % (16 * SPB)) * 4u;
         s_at[i] = (uint32_t)(kX + kW + l * 256);
     }
@@ -1024,7 +1028,7 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
     auto read_w = [&](const unsigned char *st) __attribute__((always_inline)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int b = n / NP * (CW * NP) + wn * NP + n % NP;
+            const int b = wn * NT + n;
             raw[n] = *(const u32x4 *)(st + kX + b * 1024 + lane * 16);
 #pragma unroll
             for (int i = 0; i < SPB; ++i)
@@ -1095,13 +1099,14 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
     // lane l holds tokens 4 (l / 16) .. + 3 of column l % 16 of each block
     float *red = (float *)lds;                // [KW][P][BM][RN]
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+        const int b = wn * NT + n;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                red[((kg * P + n / NP) * BM + mt * 16 + 4 * g + r) * RN + (wn * NP + n % NP) * 16 + row] =
-                    tot[mt][n][r];
+                red[((kg * P + b / CB) * BM + mt * 16 + 4 * g + r) * RN + b % CB * 16 + row] = tot[mt][n][r];
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < BM * BN / 4; e += 64 * CW * KW) {
         const int r = e / (BN / 4), c = e % (BN / 4) * 4;
@@ -1125,7 +1130,7 @@ template <bool GATED, int SPB, int MT, int NT, int CW, int KW, int S>
 hipError_t launch_split(const BaseArgs &args, hipStream_t st)
 {
     BaseArgs a = args;
-    constexpr int BM = 16 * MT, BN = 16 * CW * (GATED ? NT / 2 : NT);
+    constexpr int BM = 16 * MT, BN = 16 * CW * NT / (GATED ? 2 : 1);
     const bool zero = any_zero(a);
     a.items = set_tiles<GATED>(a, BN) * ((a.T + BM - 1) / BM);
     const int grid = (a.items + 7) / 8 * 8;
@@ -1177,8 +1182,9 @@ bool one_per_cu(const BaseArgs &args, int BM, int BN)
 // Above that, the smallest tile of which every CU gets at most one, since such a batch
 // waits for its slowest workgroup (4096 -> 4096: 64 tokens 8.6 us on 32 x 32, 10.5 on
 // 32 x 64, 14.6 on 32 x 128 tiles; 256 tokens 27.7, 22.5, 18.1; 5120 -> 10240, 256
-// tokens: 54 on 64 x 128, 43 on 64 x 256); with more, the tile kernel, two workgroups
-// a CU (8192 tokens of 4096 -> 4096: 303 us against 330 on the 64 x 256 split then).
+// tokens: 54 on 64 x 128, 43 on 64 x 256; 512 tokens 78 on 64 x 256, some CUs with two,
+// and 68.5 on 64 x 384); with more, the tile kernel, two workgroups a CU (8192 tokens of
+// 4096 -> 4096: 292 us against 345 on the 64 x 384 split).
 // x off a 16-byte boundary cannot be loaded to LDS directly and takes slower ways.
 template <typename XT, bool GATED, int SPB>
 hipError_t launch_sized(const BaseArgs &a, hipStream_t st)
@@ -1215,6 +1221,8 @@ hipError_t launch_sized(const BaseArgs &a, hipStream_t st)
                 return launch_split<true, SPB, 4, 2, 4, 3, 2>(a, st);
             if (one_per_cu<true>(a, 64, 128))
                 return launch_split<true, SPB, 4, 4, 4, 2, 2>(a, st);
+            if (one_per_cu<true>(a, 64, 192))
+                return launch_split<true, SPB, 4, 3, 8, 1, 3>(a, st);
         } else {
             if (one_per_cu<false>(a, 32, 32))
                 return launch_split<false, SPB, 2, 1, 2, 4, 3>(a, st);
@@ -1226,6 +1234,8 @@ hipError_t launch_sized(const BaseArgs &a, hipStream_t st)
                 return launch_split<false, SPB, 4, 2, 4, 3, 2>(a, st);
             if (one_per_cu<false>(a, 64, 256))
                 return launch_split<false, SPB, 4, 4, 4, 2, 2>(a, st);
+            if (one_per_cu<false>(a, 64, 384))
+                return launch_split<false, SPB, 4, 3, 8, 1, 3>(a, st);
         }
         return launch_tile<XT, GATED, SPB, 4, 4, 1, true>(a, st);
     }

@@ -97,7 +97,8 @@ WAYS = [
     ("bf16", 257, 2056),     # split, 32 x 128
     ("bf16", 513, 2056),     # split, 64 x 128
     ("bf16", 1025, 2056),    # split, 64 x 256
-    ("bf16", 2049, 2056),    # tiles
+    ("bf16", 2049, 2056),    # split, 64 x 384
+    ("bf16", 2689, 2056),    # tiles
     ("fp32", 5, 8200),       # few tokens, four column blocks a workgroup
     ("fp32", 17, 8200),      # tiles, K halved
     ("fp32", 129, 8200),     # tiles
@@ -140,7 +141,7 @@ def test_unaligned_rows_are_exact_on_integers(tokens):
             intact()
 
 
-@pytest.mark.parametrize("tokens,n", [(40, 2056), (600, 2056), (2100, 2056)])
+@pytest.mark.parametrize("tokens,n", [(40, 2056), (600, 2056), (2100, 2056), (2700, 2056)])
 def test_nonfinite_rows_in_large_batches(tokens, n):
     """A NaN row, an infinity at the end of a row, and a batch of NaN: quick, and the rows
     beside them keep their bits."""

@@ -92,7 +92,8 @@ def test_gated(dtype, tokens, d_in, d_out, group, zero, bias, gadd, uadd, act):
 
 
 # One case for each way the library multiplies.
-WAYS = [("bf16", 9, 8200), ("bf16", 129, 4104), ("bf16", 257, 4104), ("bf16", 1025, 4104),
+WAYS = [("bf16", 9, 8200), ("bf16", 129, 4104), ("bf16", 257, 4104), ("bf16", 449, 4104),
+        ("bf16", 1025, 4104),
         ("fp32", 9, 8200), ("fp32", 17, 8200), ("fp32", 65, 8200)]
 
 
