@@ -897,6 +897,11 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
 // largest, 64 x 384 on 8 waves of 48 columns, fill LDS with one group of 3 (4 waves of 96
 // columns, one a SIMD: 512 tokens of 5120 -> 10240 86.5 us against 68.5).  A wave takes NT
 // weight blocks in a row of gate's and then up's, so it may have blocks of one only.
+// Without zero points the products start at -24 sum x, which halves the vector work per
+// sum but waits for that sum first: 512 tokens of 5120 -> 10240 in groups of 64 84 -> 74
+// us, gated 256 tokens 63 -> 60, 64 tokens of 4096 -> 11008 in groups of 32 19.1 -> 17.3;
+// the smallest grids, which wait most, lose a little (64 tokens of 4096 -> 4096 8.8 -> 8.9,
+// of gated 4096 -> 11008 23.0 -> 24.4).
 //
 // Block k of a group lies in stage k % S; block k + S - 1 is loaded into the stage of
 // block k - 1 once every wave has read that.  Every wave issues the same number of loads
@@ -1001,7 +1006,9 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
     auto landed = [&]() __attribute__((always_inline)) {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * LOADS) : "memory");
     };
-    const u32x4 ones_bits = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+    // ones, or -24 where that is every zero point: then the products start at -24 sum x
+    constexpr uint32_t kOne = ZERO ? 0x3f803f80u : 0xc1c0c1c0u;
+    const u32x4 ones_bits = {kOne, kOne, kOne, kOne};
     const bf16x8 ones = __builtin_bit_cast(bf16x8, ones_bits);
     const Constants con = hold_constants();
 
@@ -1059,7 +1066,7 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
 #pragma unroll
             for (int i = 0; i < SPB; ++i) {
                 s[n][i] = dead ? 0.f : Scale<uint16_t>::scale(sw[n][i]);
-                z[n][i] = ZERO ? Scale<uint16_t>::zero(sw[n][i]) : 24.f;
+                z[n][i] = ZERO ? Scale<uint16_t>::zero(sw[n][i]) : 0.f;
             }
         }
 #pragma unroll
@@ -1075,12 +1082,17 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
                 read_x(my + cur * kStage, 0);
             }
             f32x4 acc[NT], sum = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (!ZERO)
+#pragma unroll
+                for (int j = 0; j < NK; ++j)
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[step & 1][j], ones, sum, 0, 0, 0);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+                acc[n] = ZERO ? f32x4{0.f, 0.f, 0.f, 0.f} : sum;
 #pragma unroll
             for (int j = 0; j < NK; ++j) {
-                sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[step & 1][j], ones, sum, 0, 0, 0);
+                if constexpr (ZERO)
+                    sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[step & 1][j], ones, sum, 0, 0, 0);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[step & 1][j], w[n][sub * NK + j], acc[n],
@@ -1090,7 +1102,8 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    tot[mt][n][r] = fmaf(s[n][sub], fmaf(-z[n][sub], sum[r], acc[n][r]), tot[mt][n][r]);
+                    tot[mt][n][r] = fmaf(s[n][sub], ZERO ? fmaf(-z[n][sub], sum[r], acc[n][r]) : acc[n][r],
+                                         tot[mt][n][r]);
         }
     }
     // the loads of blocks past the last one are in before the stages hold sums
