@@ -407,8 +407,8 @@ int lora_apply_group_noalloc(lora_ctx *ctx, int32_t n, const int32_t *modules,
  * bytes per scale, the sizes rounded up to 16 and 128) is allocated at the
  * module's first load, and again by a load whose scales need more; all of it is
  * kept until lora_slots_destroy.  A graph captured before a reload sees the new
- * weights if group_size and the presence of a bias are as before; any other
- * reload needs a new capture.  A load does not touch slots, adapters or saved
+ * weights, and their zero points or that they have none, if group_size and the
+ * presence of a bias are as before; any other reload needs a new capture.  A load does not touch slots, adapters or saved
  * modules.
  * Errors: LORA_ERR_BAD_MODULE; q or scale NULL, a bad group_size or a d_in above
  * 2^22 -> LORA_ERR_INVALID_ARGUMENT; LORA_ERR_HOST_NOT_PINNED;

@@ -20,6 +20,8 @@
 // what plain arithmetic gives.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "lora_dma.h"
 #include "lora_layer.h"
 
@@ -58,6 +60,8 @@ __global__ __launch_bounds__(256) void base_pack_q_kernel(BasePackArgs a)
     const int64_t n_items = (int64_t)((a.rows + kBaseCols - 1) / kBaseCols) * KB * 64;
     if (i >= n_items)
         return;
+    if (i == 0)
+        *a.has_zero = a.zero != nullptr;
     const int lane = (int)(i & 63);
     const int64_t block = i >> 6;
     const int kb = (int)(block % KB);
@@ -338,6 +342,15 @@ __device__ __forceinline__ void load_scales(typename Scale<XT>::word *out, __amd
     __builtin_memcpy(out, v, sizeof v);
 }
 
+// Whether the weights of member mi (gated: either weight) were loaded with zero points, from
+// the word that the load wrote (kZerosAsk).
+template <bool GATED>
+__device__ __forceinline__ bool has_zero(const BaseArgs &a, int mi)
+{
+    const uint32_t z = GATED ? *a.m[0].has_zero | *a.m[1].has_zero : *a.m[mi].has_zero;
+    return __builtin_amdgcn_readfirstlane(z) != 0;
+}
+
 // Column tiles of `width` columns of each member; returns how many there are.
 template <bool GATED>
 int set_tiles(BaseArgs &a, int width)
@@ -346,13 +359,6 @@ int set_tiles(BaseArgs &a, int width)
     for (int i = 0; i < a.n; ++i)
         a.tile_start[i + 1] = a.tile_start[i] + (a.m[i].d_out + width - 1) / width;
     return a.tile_start[GATED ? 1 : a.n];
-}
-bool any_zero(const BaseArgs &a)
-{
-    bool zero = false;
-    for (int i = 0; i < a.n; ++i)
-        zero = zero || a.m[i].zero;
-    return zero;
 }
 
 template <typename XT, int MT, int C, int SPB, bool GATED, int W, int D>
@@ -517,6 +523,30 @@ hipError_t launch_few(const BaseArgs &args, hipStream_t st)
     return hipGetLastError();
 }
 
+// Work item -> (member, its column tile, the first token of its token tile): an XCD takes a
+// contiguous run of items, which go through 8 token tiles of a column tile before the next
+// column tile, so the items it runs together share x and W in its L2.  False: no item.
+template <bool GATED, int BM>
+__device__ __forceinline__ bool item_of(const BaseArgs &a, int &mi, int &c_tile, int &t0)
+{
+    const int per_xcd = gridDim.x >> 3;
+    const int item = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+    if (item >= a.items)
+        return false;
+    const int t_tiles = (a.T + BM - 1) / BM;
+    const int c_tiles = a.tile_start[GATED ? 1 : a.n];
+    const int band = item / (8 * c_tiles), in = item - band * 8 * c_tiles;
+    const int high = min(8, t_tiles - band * 8);
+    c_tile = __builtin_amdgcn_readfirstlane(in / high);
+    t0 = __builtin_amdgcn_readfirstlane((band * 8 + in - c_tile * high) * BM);
+    mi = 0;
+    if constexpr (!GATED)
+        while (mi + 1 < a.n && c_tile >= a.tile_start[mi + 1])
+            ++mi;
+    c_tile -= a.tile_start[mi];
+    return true;
+}
+
 // ---------------------------------------------------------------------------
 // products of many tokens
 //
@@ -549,8 +579,20 @@ hipError_t launch_few(const BaseArgs &args, hipStream_t st)
 // unpacking 10%, scaling 6%, the loads of x or w 8% each, so no single one bounds it.
 // One workgroup of eight waves on 128 x 256 with weights in LDS too was slower (1642
 // against 1562 us then).
+template <typename XT, int MT, int NT, int KW, int SPB, bool GATED> struct TileLds {
+    static constexpr int P = GATED ? 2 : 1;
+    static constexpr int BM = 16 * MT, BN = 64 * (NT / P);
+    static constexpr int RN = BN + 4;             // row of joined sums, padded for the banks
+    static constexpr size_t kStageBytes = (size_t)KW * 3 * XT_PIECES<XT> * BM * kBaseK * 2;
+    static constexpr size_t kJoinBytes = (size_t)KW * P * (BM / 2) * RN * 4;
+    __attribute__((aligned(16))) unsigned char stages[kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes];
+    __attribute__((aligned(16))) float sums[KW][2][SPB][BM];
+    __attribute__((aligned(16))) float unread[256 + 2 * SPB * BM];
+};
+
 template <typename XT, int MT, int NT, int KW, int SPB, bool GATED, bool ZERO, bool DX>
-__global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(BaseArgs a)
+__device__ __forceinline__ void base_tile(const BaseArgs &a, TileLds<XT, MT, NT, KW, SPB, GATED> &shared,
+                                          int mi, int c_tile, int t0)
 {
     typedef typename Scale<XT>::word word;
     constexpr int PIECES = XT_PIECES<XT>;
@@ -559,39 +601,18 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
     constexpr int BM = 16 * MT, BN = 64 * NP;
     constexpr int NK = 4 / SPB;                   // MFMA steps per group of a block
     constexpr uint32_t kScBytes = 16 * SPB * sizeof(word);   // scales of a weight block
-    constexpr int RN = BN + 4;                    // row of joined sums, padded for the banks
-    constexpr size_t kStageBytes = (size_t)KW * 3 * PIECES * BM * kBaseK * 2;
-    constexpr size_t kJoinBytes = (size_t)KW * P * (BM / 2) * RN * 4;
-    __shared__ __attribute__((aligned(16))) unsigned char lds[kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes];
-    __shared__ __attribute__((aligned(16))) float sums_all[KW][2][SPB][BM];
-    __shared__ __attribute__((aligned(16))) float unread[256 + 2 * SPB * BM];
+    constexpr int RN = std::remove_reference_t<decltype(shared)>::RN;
+    unsigned char *const lds = shared.stages;
+    auto &unread = shared.unread;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave & 3, kg = wave >> 2;
     const int tid = threadIdx.x & 255;            // in its group
     auto &xs = ((uint16_t(*)[3][PIECES][BM * kBaseK])lds)[kg];
-    auto &sums = sums_all[kg];
+    auto &sums = shared.sums[kg];
     const int row = lane & 15, g = lane >> 4;
 
-    // work item -> (column tile, token tile): an XCD takes a contiguous run of items,
-    // which go through 8 token tiles of a column tile before the next column tile, so
-    // the items it runs together share x and W in its L2
-    const int per_xcd = gridDim.x >> 3;
-    const int item = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-    if (item >= a.items)
-        return;
-    const int t_tiles = (a.T + BM - 1) / BM;
-    const int c_tiles = a.tile_start[GATED ? 1 : a.n];
-    const int band = item / (8 * c_tiles), in = item - band * 8 * c_tiles;
-    const int high = min(8, t_tiles - band * 8);
-    int c_tile = __builtin_amdgcn_readfirstlane(in / high);
-    const int t0 = __builtin_amdgcn_readfirstlane((band * 8 + in - c_tile * high) * BM);
-    int mi = 0;
-    if constexpr (!GATED)
-        while (mi + 1 < a.n && c_tile >= a.tile_start[mi + 1])
-            ++mi;
-    c_tile -= a.tile_start[mi];
     const BaseMember &m = a.m[mi];
     const int KB = m.kb, d_in = m.d_in, d_out = m.d_out;
     const int nblocks = (d_out + kBaseCols - 1) / kBaseCols;
@@ -880,6 +901,19 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
     }
 }
 
+template <typename XT, int MT, int NT, int KW, int SPB, bool GATED, bool DX, Zeros Z>
+__global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(BaseArgs a)
+{
+    __shared__ TileLds<XT, MT, NT, KW, SPB, GATED> shared;
+    int mi, c_tile, t0;
+    if (!item_of<GATED, 16 * MT>(a, mi, c_tile, t0))
+        return;
+    if (Z == kZerosSome || (Z == kZerosAsk && has_zero<GATED>(a, mi)))
+        base_tile<XT, MT, NT, KW, SPB, GATED, true, DX>(a, shared, mi, c_tile, t0);
+    else
+        base_tile<XT, MT, NT, KW, SPB, GATED, false, DX>(a, shared, mi, c_tile, t0);
+}
+
 // ---------------------------------------------------------------------------
 // products of a middling number of tokens
 //
@@ -909,8 +943,17 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
 // Rows past the batch, inputs past d_in and blocks past the last one are addressed inside
 // the buffers and drop out: such rows are not stored, such inputs have weights equal to
 // their zero point, and such blocks get scale 0.
+template <int MT, int NT, int CW, int KW, int S, int SPB, bool GATED> struct SplitLds {
+    static constexpr int P = GATED ? 2 : 1, WB = CW * NT, BM = 16 * MT;
+    static constexpr int kStage = BM * kBaseK * 2 + WB * 1024 + (WB * SPB + 3) / 4 * 256;   // of a group
+    static constexpr int RN = 16 * (WB / P) + 4;
+    static constexpr int kJoin = KW * P * BM * RN * 4;
+    __attribute__((aligned(16))) unsigned char bytes[S * kStage * KW > kJoin ? S * kStage * KW : kJoin];
+};
+
 template <int MT, int NT, int CW, int KW, int S, int SPB, bool GATED, bool ZERO>
-__global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
+__device__ __forceinline__ void base_split(const BaseArgs &a, SplitLds<MT, NT, CW, KW, S, SPB, GATED> &shared,
+                                           int mi, int c_tile, int t0)
 {
     constexpr int P = GATED ? 2 : 1;
     constexpr int WB = CW * NT;                   // weight blocks of a workgroup, gate's before up's
@@ -920,36 +963,21 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
     constexpr int XL = BM / 4 / CW;               // loads of x a wave and block
     constexpr int kX = BM * kBaseK * 2, kW = WB * 1024, SL = (WB * SPB + 3) / 4, kS = SL * 256;
     constexpr int kStage = kX + kW + kS;          // LDS bytes of a group's stage
-    constexpr int RN = BN + 4;
-    constexpr int kJoin = KW * P * BM * RN * 4;
-    constexpr int kLds = S * kStage * KW > kJoin ? S * kStage * KW : kJoin;
+    typedef std::remove_reference_t<decltype(shared)> Lds;
+    static_assert(kStage == Lds::kStage, "");
+    constexpr int RN = Lds::RN;
     constexpr int SW = (SL + CW - 1) / CW;        // scale loads (SL of 256 bytes a block) of each wave
     constexpr int LOADS = XL + NT + SW;
     static_assert(WB % P == 0 && BM / 4 % CW == 0, "");
     static_assert(!GATED || CB * SPB % 4 == 0, "a load of scales is of one weight");
     static_assert((S - 2) * LOADS < 64, "vmcnt counts to 63");
-    __shared__ __attribute__((aligned(16))) unsigned char lds[kLds];
+    unsigned char *const lds = shared.bytes;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kg = wave / CW, wn = wave % CW;
     const int row = lane & 15, g = lane >> 4;
 
-    const int per_xcd = gridDim.x >> 3;
-    const int item = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
-    if (item >= a.items)
-        return;
-    const int t_tiles = (a.T + BM - 1) / BM;
-    const int c_tiles = a.tile_start[GATED ? 1 : a.n];
-    const int band = item / (8 * c_tiles), in = item - band * 8 * c_tiles;
-    const int high = min(8, t_tiles - band * 8);
-    int c_tile = __builtin_amdgcn_readfirstlane(in / high);
-    const int t0 = __builtin_amdgcn_readfirstlane((band * 8 + in - c_tile * high) * BM);
-    int mi = 0;
-    if constexpr (!GATED)
-        while (mi + 1 < a.n && c_tile >= a.tile_start[mi + 1])
-            ++mi;
-    c_tile -= a.tile_start[mi];
     const BaseMember &m = a.m[mi];
     const int KB = m.kb, d_in = m.d_in, d_out = m.d_out;
     const int nblocks = (d_out + kBaseCols - 1) / kBaseCols;
@@ -1139,18 +1167,38 @@ __global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
     }
 }
 
+template <int MT, int NT, int CW, int KW, int S, int SPB, bool GATED, Zeros Z>
+__global__ __launch_bounds__(64 * CW * KW) void base_split_kernel(BaseArgs a)
+{
+    __shared__ SplitLds<MT, NT, CW, KW, S, SPB, GATED> shared;
+    int mi, c_tile, t0;
+    if (!item_of<GATED, 16 * MT>(a, mi, c_tile, t0))
+        return;
+    if (Z == kZerosSome || (Z == kZerosAsk && has_zero<GATED>(a, mi)))
+        base_split<MT, NT, CW, KW, S, SPB, GATED, true>(a, shared, mi, c_tile, t0);
+    else
+        base_split<MT, NT, CW, KW, S, SPB, GATED, false>(a, shared, mi, c_tile, t0);
+}
+
+template <typename F> void with_zeros(Zeros zeros, F &&launch)
+{
+    switch (zeros) {
+    case kZerosNone: launch(std::integral_constant<Zeros, kZerosNone>{}); break;
+    case kZerosSome: launch(std::integral_constant<Zeros, kZerosSome>{}); break;
+    default: launch(std::integral_constant<Zeros, kZerosAsk>{});
+    }
+}
+
 template <bool GATED, int SPB, int MT, int NT, int CW, int KW, int S>
 hipError_t launch_split(const BaseArgs &args, hipStream_t st)
 {
     BaseArgs a = args;
     constexpr int BM = 16 * MT, BN = 16 * CW * NT / (GATED ? 2 : 1);
-    const bool zero = any_zero(a);
     a.items = set_tiles<GATED>(a, BN) * ((a.T + BM - 1) / BM);
     const int grid = (a.items + 7) / 8 * 8;
-    if (zero)
-        base_split_kernel<MT, NT, CW, KW, S, SPB, GATED, true><<<grid, 64 * CW * KW, 0, st>>>(a);
-    else
-        base_split_kernel<MT, NT, CW, KW, S, SPB, GATED, false><<<grid, 64 * CW * KW, 0, st>>>(a);
+    with_zeros(a.zeros, [&](auto z) {
+        base_split_kernel<MT, NT, CW, KW, S, SPB, GATED, z.value><<<grid, 64 * CW * KW, 0, st>>>(a);
+    });
     return hipGetLastError();
 }
 
@@ -1159,13 +1207,11 @@ hipError_t launch_tile(const BaseArgs &args, hipStream_t st)
 {
     BaseArgs a = args;
     constexpr int BM = 16 * MT, BN = 64 * (GATED ? NT / 2 : NT);
-    const bool zero = any_zero(a);
     a.items = set_tiles<GATED>(a, BN) * ((a.T + BM - 1) / BM);
     const int grid = (a.items + 7) / 8 * 8;
-    if (zero)
-        base_tile_kernel<XT, MT, NT, KW, SPB, GATED, true, DX><<<grid, 256 * KW, 0, st>>>(a);
-    else
-        base_tile_kernel<XT, MT, NT, KW, SPB, GATED, false, DX><<<grid, 256 * KW, 0, st>>>(a);
+    with_zeros(a.zeros, [&](auto z) {
+        base_tile_kernel<XT, MT, NT, KW, SPB, GATED, DX, z.value><<<grid, 256 * KW, 0, st>>>(a);
+    });
     return hipGetLastError();
 }
 

@@ -87,8 +87,18 @@ BaseMember base_member(const lora_ctx *c, int32_t module, const void *x, const v
     m.d_in = sh.d_in;
     m.d_out = sh.d_out;
     m.kb = ceil_div(sh.d_in, kBaseK);
-    m.zero = p.zero;
+    m.has_zero = p.has_zero;
     return m;
+}
+
+// What a launch on s may take for granted of the zero points of n modules: a captured one
+// only what no later load can change.
+Zeros zeros_of(const lora_ctx *c, int32_t n, const int32_t *modules, int spb, hipStream_t s)
+{
+    for (int i = 0; i < n; ++i)
+        if (c->base[modules[i]].spb == spb && c->base[modules[i]].zero)
+            return kZerosSome;
+    return s && stream_capturing(s) ? kZerosAsk : kZerosNone;
 }
 
 // Device memory the ctx keeps until it is destroyed.
@@ -169,9 +179,10 @@ int do_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scal
     // storage first: a failed allocation leaves the module as it was
     void *nq = p.q, *nsc = p.sc, *nbias = p.bias;
     int rc;
-    if (!nq && (rc = base_alloc(ctx, &nq, (size_t)(nb * kb) * 1024, module)))
+    if (!nq && (rc = base_alloc(ctx, &nq, (size_t)(nb * kb) * 1024 + 16, module)))
         return rc;
     p.q = (uint32_t *)nq;
+    p.has_zero = p.q + nb * kb * 256;
     if (spb > p.sc_room) {
         if ((rc = base_alloc(ctx, &nsc, (size_t)(nb * kb) * kBaseCols * spb * word, module)))
             return rc;
@@ -221,6 +232,7 @@ int do_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scal
         a.scale = (const float *)at[1];
         a.zero = (const uint8_t *)at[2];
         a.q_out = p.q + (r0 / kBaseCols) * kb * 256;
+        a.has_zero = p.has_zero;
         a.sc_out = (char *)p.sc + (size_t)(r0 / kBaseCols) * kb * kBaseCols * spb * word;
         a.rows = (int32_t)n;
         a.d_in = sh.d_in;
@@ -282,8 +294,10 @@ int do_base_group(lora_ctx *ctx, int32_t n, const int32_t *modules, const void *
                 continue;
             a.m[a.n++] = base_member(ctx, modules[i], x[i], add ? add[i] : nullptr, y[i]);
         }
-        if (a.n)
-            HIP_TRY(ctx, launch_base(ctx->dtype == LORA_BF16, false, spb, a, s));
+        if (!a.n)
+            continue;
+        a.zeros = zeros_of(ctx, n, modules, spb, s);
+        HIP_TRY(ctx, launch_base(ctx->dtype == LORA_BF16, false, spb, a, s));
     }
     return LORA_OK;
 }
@@ -336,6 +350,8 @@ int do_base_gated(lora_ctx *ctx, int32_t gate_module, int32_t up_module, const v
     a.act = activation;
     a.m[0] = base_member(ctx, gate_module, x, gate_add, y);
     a.m[1] = base_member(ctx, up_module, x, up_add, y);
+    const int32_t both[2] = {gate_module, up_module};
+    a.zeros = zeros_of(ctx, 2, both, ctx->base[gate_module].spb, s);
     HIP_TRY(ctx, launch_base(ctx->dtype == LORA_BF16, true, ctx->base[gate_module].spb, a, s));
     return LORA_OK;
 }
