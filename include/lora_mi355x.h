@@ -405,11 +405,12 @@ int lora_apply_group_noalloc(lora_ctx *ctx, int32_t n, const int32_t *modules,
  * waits for the base products already enqueued.  Slot loads and base products do
  * not wait for each other.  Storage (d_out x d_in / 2 bytes and 4 or 8
  * bytes per scale, the sizes rounded up to 16 and 128) is allocated at the
- * module's first load, and again by a load whose scales need more; all of it is
- * kept until lora_slots_destroy.  A graph captured before a reload sees the new
- * weights, and their zero points or that they have none, if group_size and the
- * presence of a bias are as before; any other reload needs a new capture.  A load does not touch slots, adapters or saved
- * modules.
+ * module's first load, and that of the scales again by the first load with another
+ * kind of scale storage (group sizes 32; 64; every other); all of it is kept until
+ * lora_slots_destroy.  A replayed graph sees the weights loaded last, and their
+ * zero points or that they have none, if their kind of scale storage and the
+ * presence of a bias are those at the capture; else it needs a new capture.  A
+ * load does not touch slots, adapters or saved modules.
  * Errors: LORA_ERR_BAD_MODULE; q or scale NULL, a bad group_size or a d_in above
  * 2^22 -> LORA_ERR_INVALID_ARGUMENT; LORA_ERR_HOST_NOT_PINNED;
  * LORA_ERR_OUT_OF_MEMORY.

@@ -79,7 +79,7 @@ BaseMember base_member(const lora_ctx *c, int32_t module, const void *x, const v
     const lora_module_shape sh = c->shapes[module];
     BaseMember m{};
     m.q = p.q;
-    m.sc = p.sc;
+    m.sc = p.sc();
     m.bias = p.has_bias ? p.bias : nullptr;
     m.x = x;
     m.add = add;
@@ -177,18 +177,16 @@ int do_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scal
         ctx->base.resize(ctx->n_modules);
     BasePack &p = ctx->base[module];
     // storage first: a failed allocation leaves the module as it was
-    void *nq = p.q, *nsc = p.sc, *nbias = p.bias;
+    void *nq = p.q, *nsc = p.sc(spb), *nbias = p.bias;
     int rc;
     if (!nq && (rc = base_alloc(ctx, &nq, (size_t)(nb * kb) * 1024 + 16, module)))
         return rc;
     p.q = (uint32_t *)nq;
     p.has_zero = p.q + nb * kb * 256;
-    if (spb > p.sc_room) {
+    if (!nsc) {
         if ((rc = base_alloc(ctx, &nsc, (size_t)(nb * kb) * kBaseCols * spb * word, module)))
             return rc;
-        p.sc = nsc;
-        p.sc_room = spb;
-        p.spb = 0;               // its scales are the new ones from here on
+        p.sc(spb) = nsc;
     }
     if (bias && !nbias) {
         if ((rc = base_alloc(ctx, &nbias, (size_t)sh.d_out * ctx->elem, module)))
@@ -233,7 +231,7 @@ int do_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scal
         a.zero = (const uint8_t *)at[2];
         a.q_out = p.q + (r0 / kBaseCols) * kb * 256;
         a.has_zero = p.has_zero;
-        a.sc_out = (char *)p.sc + (size_t)(r0 / kBaseCols) * kb * kBaseCols * spb * word;
+        a.sc_out = (char *)nsc + (size_t)(r0 / kBaseCols) * kb * kBaseCols * spb * word;
         a.rows = (int32_t)n;
         a.d_in = sh.d_in;
         a.group = group;

@@ -34,11 +34,14 @@ constexpr int kBaseMaxIn = 1 << 22;
 
 struct BasePack {
     uint32_t *q = nullptr;       // [col blocks][K blocks][64][4]
-    void *sc = nullptr;          // [col blocks][K blocks][16][spb] words (fp32: pairs of floats)
+    void *scales[3] = {};        // for 1, 2 and 4 scales a block: [col blocks][K blocks][16][spb] words
+                                 // (fp32: pairs of floats); each stays where it is, so that a graph
+                                 // captured on it finds the scales of every later load of its kind
     void *bias = nullptr;        // [d_out], ctx dtype
     int32_t spb = 0;             // 0: no weight loaded
-    int32_t sc_room = 0;         // the spb that sc has room for
     bool has_bias = false;
+    void *&sc(int of) { return scales[of >> 1]; }
+    void *sc() const { return scales[spb >> 1]; }
     bool zero = false;           // loaded with zero points (else all are 8), and the same
     uint32_t *has_zero = nullptr;   // in a device word behind q, for captured launches
 };

@@ -150,3 +150,36 @@ def test_group_of_modules_with_and_without_zero_points():
                 want = base_sum(x, w[i], d_in, 64)[0].float().bfloat16()
                 assert torch.equal(eager[i].cpu(), want), ("eager", pattern, i)
                 assert torch.equal(y[i].cpu(), want), ("replay", pattern, i)
+
+
+@pytest.mark.parametrize("tokens", [3, 40, 700])
+def test_replay_after_a_reload_in_another_group_size_and_back(tokens):
+    """Weights in groups of 128, captured; then others in groups of 32, with more scales and
+    a bias; then again groups of 128 without a bias, as at the capture: the replay sees them."""
+    d_in, n = 392, 264
+    gen = torch.Generator().manual_seed(tokens)
+    x = torch.randint(-3, 4, (tokens, d_in), generator=gen).bfloat16()
+    xd = x.cuda()
+    bias = torch.randint(-3, 4, (n,), generator=gen).bfloat16()
+    with binding.Slots(1, 1, [(d_in, n)], "bf16", tokens) as S:
+        y = torch.zeros(tokens, n, dtype=torch.bfloat16, device="cuda")
+        graph = None
+        for group in (128, 32, 256, 64, 128):
+            w = integer_weight(gen, n, d_in, group, True)
+            b = bias if group == 32 else None
+            S.load_base(0, *(t.cuda() for t in w), group, None if b is None else b.cuda())
+            S.sync_loads()
+            if graph is None:
+                graph = capture(lambda: S.base(xd, y, 0))
+            want = base_sum(x, w, d_in, group)[0] + (0 if b is None else b.double())
+            want = want.float().bfloat16()
+            eager = torch.empty_like(y)
+            S.base(xd, eager, 0)
+            assert torch.equal(eager.cpu(), want), group
+            if group < 128:
+                continue
+            y.zero_()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y.cpu(), want), group
