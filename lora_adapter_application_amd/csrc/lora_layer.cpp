@@ -176,7 +176,8 @@ int do_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scal
     if (ctx->base.empty())
         ctx->base.resize(ctx->n_modules);
     BasePack &p = ctx->base[module];
-    // storage first: a failed allocation leaves the module as it was
+    // Storage first, each kind kept for the module's next load: a failed allocation leaves the
+    // weight as it was.
     void *nq = p.q, *nsc = p.sc(spb), *nbias = p.bias;
     int rc;
     if (!nq && (rc = base_alloc(ctx, &nq, (size_t)(nb * kb) * 1024 + 16, module)))
@@ -212,6 +213,9 @@ int do_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scal
         if (rows < std::min<int64_t>(kBaseCols, sh.d_out))
             return fail(ctx, LORA_ERR_OUT_OF_MEMORY, "the stage holds no 16 rows of module %d", module);
     }
+    // from the first copy to the event the module has no weight: a load that fails between
+    // leaves none, not part of one and part of another
+    p.spb = 0;
     for (int64_t r0 = 0; r0 < sh.d_out; r0 += rows) {
         const int64_t n = std::min<int64_t>(rows, sh.d_out - r0);
         char *stage = (char *)ctx->stage;
