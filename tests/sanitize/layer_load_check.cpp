@@ -1,8 +1,8 @@
 // layer_load_check.cpp -- drives lora_base_load under AddressSanitizer and
 // UndefinedBehaviorSanitizer without a GPU: the runtime's device calls are replaced
 // by ones on host memory, each of which can be made to fail in its turn.  A load that
-// fails must leave its module with the weight it had (nothing was enqueued) or with
-// none (something was), never with a mixture.  Built and run by
+// fails must leave its module with the weight it had (before the first copy or pack is
+// tried) or with none (from there on), never with a mixture.  Built and run by
 // tests/test_layer_sanitizers_load.py.
 #include <cstdint>
 #include <cstdio>
@@ -15,7 +15,7 @@
 
 static int failures = 0;
 static int countdown = 0;      // the call that fails, counted from 1; 0: none
-static int enqueued = 0;       // copies and packs of the present load
+static int tried = 0;          // copies and packs of the present load
 static bool fails() { return countdown > 0 && --countdown == 0; }
 
 extern "C" {
@@ -34,9 +34,9 @@ hipError_t hipFree(void *p) { std::free(p); return hipSuccess; }
 hipError_t hipMemsetAsync(void *p, int v, size_t n, hipStream_t) { std::memset(p, v, n); return hipSuccess; }
 hipError_t hipMemcpyAsync(void *d, const void *s, size_t n, hipMemcpyKind, hipStream_t)
 {
+    ++tried;
     if (fails())
         return hipErrorUnknown;
-    ++enqueued;
     std::memcpy(d, s, n);
     return hipSuccess;
 }
@@ -88,9 +88,9 @@ hipError_t scratch_address(int, void **p) { *p = nullptr; return hipSuccess; }
 hipError_t xcd_dispatch_check(int, hipStream_t, bool *ok) { *ok = false; return hipSuccess; }
 hipError_t launch_base_pack(bool, const BasePackArgs &a, hipStream_t)
 {
+    ++tried;
     if (fails())
         return hipErrorLaunchFailure;
-    ++enqueued;
     // the last bytes of every source and destination are there
     const int64_t kb = (a.d_in + kBaseK - 1) / kBaseK, nb = (a.rows + kBaseCols - 1) / kBaseCols;
     volatile uint8_t sink = a.q[(int64_t)a.rows * a.d_in / 2 - 1];
@@ -144,7 +144,7 @@ int main()
                 CHECK(launched_spb == 1 && !launched_bias);
                 const void *sc = launched_sc;
                 // groups of 32 and a bias: every allocation that a reload can make
-                enqueued = 0;
+                tried = 0;
                 countdown = k;
                 const int rc = lora_base_load(ctx, 0, pq, ps, pz, 32, bias.data());
                 done = countdown > 0;          // no call was left to fail
@@ -155,7 +155,7 @@ int main()
                     CHECK(launched_spb == 4 && launched_bias && launched_sc != sc);
                 } else {
                     CHECK(rc != LORA_OK);
-                    if (enqueued) {
+                    if (tried) {
                         CHECK(run == LORA_ERR_INVALID_ARGUMENT);
                         CHECK(std::strstr(lora_last_error(ctx), "no base weight"));
                     } else {
