@@ -11,9 +11,14 @@
 // the mantissa), so a pair of weights costs a shift and one and-or, no weight is
 // ever rounded, and the products x q' are exact in the matrix cores' fp32 sums.
 // The second sum is the same matrix product with a column of ones.  The offset
-// costs accuracy only in the ratio of 16 + q to |q - z|, about two bits of fp32.
-// An fp32 x is split into three bf16 numbers (8 + 8 + 8 bits, exact) that are
-// multiplied in turn.
+// costs accuracy in the ratio of the two sums to their difference: some two bits of
+// fp32 where x has no mean, but a sum of 128 inputs near 1 is 3000, and each step that
+// rounds it off by up to 2^-13.  bf16 results, off by 2^-9 of their value anyway, do not
+// see it.  An fp32 x is split into three bf16 numbers (8 + 8 + 8 bits, exact) that are
+// multiplied in turn, and its products keep the large sums short: see base_few_kernel
+// and base_tile_kernel.  Their errors in the 2-norm are 0.5e-7 to 4.3e-7, with or without
+// a mean (4096 -> 8200: 1 token 1.6e-7 to 2.4e-7, 300 tokens 3.3e-7 to 4.3e-7; a plain
+// fp32 product 2.5e-7 to 5.6e-7 and 0.9e-6 to 1.1e-6).
 //
 // An infinity or NaN in x (or an overflow of an intermediate) makes a sum that
 // is not finite; such an output is recomputed alone from the formula, so it is
@@ -163,6 +168,19 @@ __device__ __forceinline__ bf16x8 unpack(uint32_t w, const Constants &c)
     return __builtin_bit_cast(bf16x8, r);
 }
 
+// The eight weights of a word as bf16 numbers q - z, exact, at three instructions a weight:
+// sums of their products are the formula's own.
+__device__ __forceinline__ bf16x8 unpack_exact(uint32_t w, float z)
+{
+    const uint32_t r = __builtin_rotateright32(w, 3);
+    const uint32_t half[2] = {r & 0x0f0f0f0fu, (r >> 4) & 0x0f0f0f0fu};
+    bf16x8 out;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)                   // input i: nibble i / 2 + 4 (i % 2)
+        out[i] = (__bf16)((float)((half[(i >> 1) & 1] >> (16 * (i & 1) + 8 * (i >> 2))) & 255u) - z);
+    return out;
+}
+
 template <typename XT> struct Scale;
 template <> struct Scale<uint16_t> {
     typedef uint32_t word;
@@ -288,6 +306,13 @@ __device__ __forceinline__ void finish_again(const BaseArgs &a, int mi, int t, i
 // 4096 -> 4096 (27 MB) takes 7.1 us, gate and up of 4096 -> 11008 (49 MB) 10.9 us, 3.8
 // and 4.5 TB/s with the launch and the first load's latency in it.  With more tokens
 // the bytes of x count, which every workgroup reads whole: see launch_sized.
+//
+// fp32 (see the top): two token blocks multiply q - z itself (EXACT), whose unpacking two
+// blocks share; one token block joins the sums after every 32 inputs, where each is rounded
+// once at its full size, since the small pieces of x come first (4096 -> 4096: 24 tokens
+// 16.3 us against 17.0 with sums of a whole group, 64 tokens 33.8 / 34.3; one token of
+// 4096 -> 4096 8.7 / 8.5, 5120 -> 10240 15.2 / 14.3, gated 4096 -> 11008 21.2 / 18.9, and
+// 27 with q - z).
 template <typename XT> struct RawX;        // eight inputs of a token as they were loaded
 template <> struct RawX<uint16_t> {
     u32x4 v;
@@ -368,6 +393,9 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
     constexpr int PIECES = XT_PIECES<XT>;
     constexpr int P = GATED ? 2 : 1;
     constexpr int B = P * C;                      // weight blocks, each weight's C together
+    constexpr bool EXACT = PIECES > 1 && MT > 1;  // products of q - z, without sums of x
+    constexpr int JOINS = PIECES > 1 && !EXACT ? 4 : SPB;    // of the sums of a block
+    constexpr int PG = JOINS > SPB && B > 4 ? 4 : B;         // weight blocks whose sums are held at once
     constexpr uint32_t kScBytes = 16 * SPB * sizeof(word);
     __shared__ __attribute__((aligned(16))) float red[W][B][MT][256];
 
@@ -443,7 +471,7 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
             f32x4 acc[B][MT], sum[MT];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if ((j * SPB) % 4 == 0) {
+                if ((j * JOINS) % 4 == 0) {
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         sum[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -452,33 +480,49 @@ __global__ __launch_bounds__(W * 64) void base_few_kernel(BaseArgs a)
                             acc[p][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
                     }
                 }
-                bf16x8 b[B];
 #pragma unroll
-                for (int p = 0; p < B; ++p)
-                    b[p] = unpack(wq[d][p][j], con);
+                for (int p0 = 0; p0 < B; p0 += PG) {
+                    bf16x8 b[PG];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    bf16x8 x[PIECES];
-                    xr[d][mt][j].split(x);
-#pragma unroll
-                    for (int c = PIECES - 1; c >= 0; --c) {      // small pieces first
-#pragma unroll
-                        for (int p = 0; p < B; ++p)
-                            acc[p][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[c], b[p], acc[p][mt], 0, 0, 0);
-                        sum[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[c], ones, sum[mt], 0, 0, 0);
+                    for (int p = 0; p < PG; ++p) {
+                        uint32_t q8 = wq[d][p0 + p][j];
+                        if constexpr (PG < B)         // in its turn
+                            asm volatile("" : "+v"(q8));
+                        b[p] = EXACT ? unpack_exact(q8, Scale<XT>::zero(ws[d][p0 + p][j * SPB / 4]) - 16.f)
+                                     : unpack(q8, con);
                     }
-                }
-                if (((j + 1) * SPB) % 4 == 0) {
-                    const int sub = j * SPB / 4;
 #pragma unroll
-                    for (int p = 0; p < B; ++p) {
-                        const float s = Scale<XT>::scale(ws[d][p][sub]);
-                        const float z = Scale<XT>::zero(ws[d][p][sub]);
+                    for (int mt = 0; mt < MT; ++mt) {
+                        bf16x8 x[PIECES];
+                        xr[d][mt][j].split(x);
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
+                        for (int c = PIECES - 1; c >= 0; --c) {      // small pieces first
 #pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                tot[p][mt][r] = fmaf(s, fmaf(-z, sum[mt][r], acc[p][mt][r]), tot[p][mt][r]);
+                            for (int p = 0; p < PG; ++p)
+                                acc[p0 + p][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[c], b[p], acc[p0 + p][mt],
+                                                                                          0, 0, 0);
+                            if (!EXACT && p0 == 0)
+                                sum[mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[c], ones, sum[mt], 0, 0, 0);
+                        }
+                    }
+                    if (((j + 1) * JOINS) % 4 == 0) {
+                        const int sub = j * SPB / 4;
+#pragma unroll
+                        for (int p = p0; p < p0 + PG; ++p) {
+                            const float s = Scale<XT>::scale(ws[d][p][sub]);
+                            const float z = Scale<XT>::zero(ws[d][p][sub]);
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    tot[p][mt][r] = fmaf(s, EXACT ? acc[p][mt][r]
+                                                                  : fmaf(-z, sum[mt][r], acc[p][mt][r]),
+                                                         tot[p][mt][r]);
+                                // joined here, not behind the next block's loads, which need the registers
+                                if constexpr (JOINS > SPB)
+                                    asm volatile("" : "+v"(tot[p][mt]));
+                            }
+                        }
                     }
                 }
             }
@@ -714,9 +758,9 @@ __device__ __forceinline__ void base_tile(const BaseArgs &a, TileLds<XT, MT, NT,
         for (int sub = 0; sub < SPB; ++sub) {
             f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = sub * NK; j < (sub + 1) * NK; ++j)
+            for (int c = PIECES - 1; c >= 0; --c)          // small pieces first
 #pragma unroll
-                for (int c = PIECES - 1; c >= 0; --c)
+                for (int j = sub * NK; j < (sub + 1) * NK; ++j)
                     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x_frag(stage, c, wn * 16, j), ones, acc, 0, 0, 0);
             store_sum(acc, kb, sub);
         }
@@ -773,9 +817,9 @@ __device__ __forceinline__ void base_tile(const BaseArgs &a, TileLds<XT, MT, NT,
         const int r0 = step / SPB * 16, sub = step % SPB;
         c0[step & 1] = *(const f32x4 *)&sums[k & 1][sub][r0 + 4 * g];
 #pragma unroll
-        for (int j = 0; j < NK; ++j)
+        for (int c = 0; c < PIECES; ++c)
 #pragma unroll
-            for (int c = 0; c < PIECES; ++c)
+            for (int j = 0; j < NK; ++j)
                 x[step & 1][j][c] = x_frag(stage, c, r0, sub * NK + j);
     };
     read_x(0, 0, 0);
@@ -836,10 +880,13 @@ __device__ __forceinline__ void base_tile(const BaseArgs &a, TileLds<XT, MT, NT,
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 acc[n] = ZERO ? c0[step & 1] * z[n][sub] : c0[step & 1];
+            // large pieces first (fp32): they bring the sum down from -z' sum x, and the others
+            // are added to what is small then.  With the pieces of each step together twelve
+            // steps a group round a large sum, not four: 2.5 times the error, 1.5 to 4% faster
 #pragma unroll
-            for (int j = 0; j < NK; ++j)
+            for (int c = 0; c < PIECES; ++c)
 #pragma unroll
-                for (int c = PIECES - 1; c >= 0; --c)
+                for (int j = 0; j < NK; ++j)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[step & 1][j][c], w[n][sub * NK + j],
