@@ -537,6 +537,8 @@ def lora_profile_end(ctx) -> dict:
 class Slots:
     """A slot pool for a list of (d_in, d_out) modules, in bf16 or fp32."""
 
+    LOADING_BYTES = 1 << 30      # sources of base loads kept alive before one is waited for
+
     def __init__(self, max_loras: int, max_rank: int, modules: Sequence[Sequence[int]],
                  dtype: str = "bf16", max_tokens: int = 8192, device: int = 0):
         self.modules = [(int(a), int(b)) for a, b in modules]
@@ -544,6 +546,7 @@ class Slots:
         self.max_loras, self.max_rank, self.max_tokens = max_loras, max_rank, max_tokens
         self.device = int(device)
         self._loading = []       # sources of base loads that may still be read
+        self._loading_bytes = 0
         self.ctx = lora_slots_create(max_loras, max_rank, self.modules,
                                      LORA_BF16 if dtype == "bf16" else LORA_FP32, max_tokens,
                                      device)
@@ -563,6 +566,7 @@ class Slots:
     def sync_loads(self):
         lora_sync_loads(self.ctx)
         self._loading.clear()
+        self._loading_bytes = 0
 
     def prepare(self, idx, n_tokens=None, stream=None, used_slots=None):
         if used_slots is None:
@@ -595,7 +599,8 @@ class Slots:
         lora_apply_group_noalloc(self.ctx, modules, x, y, idx, n_tokens, stream)
 
     def load_base(self, module, q, scale, zero=None, group_size=128, bias=None):
-        """lora_base_load; the tensors are kept alive until sync_loads."""
+        """lora_base_load; the tensors are kept alive until sync_loads, which this call makes
+        itself before they add up to more than 1 GiB."""
         d_in, d_out = self.modules[module]
         groups = -(-d_in // (group_size or d_in)) if group_size >= 0 else 1
         for name, t, shape in (("q", q, (d_out, d_in // 2)), ("scale", scale, (d_out, groups)),
@@ -604,7 +609,12 @@ class Slots:
                 raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
         if bias is not None and not isinstance(bias, int) and bias.dtype != self.torch_dtype():
             raise ValueError(f"bias has dtype {bias.dtype}, expected {self.torch_dtype()}")
+        new = sum(t.numel() * t.element_size() for t in (q, scale, zero, bias)
+                  if t is not None and not isinstance(t, int))
+        if self._loading and self._loading_bytes + new > self.LOADING_BYTES:
+            self.sync_loads()
         self._loading.append((q, scale, zero, bias))
+        self._loading_bytes += new
         lora_base_load(self.ctx, module, q, scale, zero, group_size, bias)
 
     def torch_dtype(self):
