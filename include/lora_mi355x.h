@@ -398,19 +398,20 @@ int lora_apply_group_noalloc(lora_ctx *ctx, int32_t n, const int32_t *modules,
  *   bias        [d_out] values of the ctx dtype, or NULL
  * q, scale, zero and bias are pinned host or device memory, and stay unmodified
  * until lora_sync_loads returns (or a later call on a stream that waited for the
- * load has completed).  A bf16 ctx holds scales with 16 significant bits: exact
+ * load has completed). A bf16 ctx holds scales with 16 significant bits: exact
  * for scales that came from fp16 or bf16, else off by at most 2^-16 of their
- * value.  Asynchronous on the ctx's side stream, with the capture rule of
- * lora_slot_load: later base products wait for it, and a load over a weight in use
- * waits for the base products already enqueued.  Slot loads and base products do
- * not wait for each other.  Storage (d_out x d_in / 2 bytes and 4 or 8
- * bytes per scale, the sizes rounded up to 16 and 128) is allocated at the
- * module's first load, and that of the scales again by the first load with another
- * kind of scale storage (group sizes 32; 64; every other); all of it is kept until
- * lora_slots_destroy.  A replayed graph sees the weights loaded last, and their
- * zero points or that they have none, if their kind of scale storage and the
- * presence of a bias are those at the capture; else it needs a new capture.  A
- * load does not touch slots, adapters or saved modules.
+ * value, or of 2^-126 where that is more. Asynchronous on the ctx's side stream,
+ * with the capture rule of lora_slot_load: later base products wait for it, and a
+ * load over a weight in use waits for the base products already enqueued. Base
+ * products do not wait for slot loads, nor slot loads for them, but for the tail
+ * of a stream that has also read slots since the last slot load. Storage (d_out x
+ * d_in / 2 bytes and 4 or 8 bytes per scale, the sizes rounded up to 16 and 128)
+ * is allocated at the module's first load, and that of the scales again by the
+ * first load with another kind of scale storage (group sizes 32; 64; every
+ * other); all of it is kept until lora_slots_destroy. A replayed graph sees the
+ * weights loaded last, and their zero points or that they have none, if their
+ * kind of scale storage and the presence of a bias are those at the capture; else
+ * it needs a new capture. A load does not touch slots, adapters or saved modules.
  * Errors: LORA_ERR_BAD_MODULE; q or scale NULL, a bad group_size or a d_in above
  * 2^22 -> LORA_ERR_INVALID_ARGUMENT; LORA_ERR_HOST_NOT_PINNED;
  * LORA_ERR_OUT_OF_MEMORY.  After those the module has the weight it had; after
@@ -424,11 +425,14 @@ int lora_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *sc
  *   x    [n_tokens][d_in], y [n_tokens][d_out], row-major, device, ctx dtype
  *   add  [n_tokens][d_out] (a residual stream, say), or NULL; it may be y itself
  * y must not overlap x, and add must be y or apart from it.  Rows from n_tokens
- * on are left as they are; n_tokens == 0 is a no-op.  Products of x with q - zero
- * are summed in fp32 over each group, and the groups' sums are scaled and summed
- * in fp32, in an order that goes by the launch's tokens and columns and by x's
- * alignment alone (16 bytes is the fast one), so equal calls give equal bits; bf16
- * results are rounded once.  Infinities and NaNs in x give what the formula gives.
+ * on are left as they are; n_tokens == 0 is a no-op.  Each group is summed in fp32 and
+ * the groups' sums are scaled and summed in fp32, in an order that goes by the launch's
+ * tokens and columns, by x's alignment (16 bytes is the fast one) and by whether the
+ * weights of a module in the launch have zero points, so equal calls give equal bits;
+ * bf16 results are rounded once.  The products are of x with 16 + q, and the sums of x
+ * times 16 + zero are subtracted, so an error is a few 2^-24 of the larger sums (fp32
+ * keeps those short: its results are about as exact as those of a plain fp32 product).
+ * Infinities and NaNs in x give what the formula gives.
  * Errors: a module without a base weight, n_tokens < 0, NULL x or y, overlapping
  * buffers -> LORA_ERR_INVALID_ARGUMENT; LORA_ERR_BAD_MODULE;
  * n_tokens > max_tokens -> LORA_ERR_TOO_MANY_TOKENS.

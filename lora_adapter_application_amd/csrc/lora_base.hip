@@ -120,7 +120,9 @@ __global__ __launch_bounds__(256) void base_pack_scale_kernel(BasePackArgs a)
             z = a.zero[at] & 15u;
     }
     if constexpr (BF16) {
-        // 16 significant bits, to nearest; the freed byte holds 16 + z
+        // 16 significant bits, to nearest, so that a scale and its zero point are one word of
+        // 4 bytes: off by 2^-16 of a normal number at most, where a bf16 result is rounded by
+        // 2^-9 to 2^-8.  The freed byte holds 16 + z
         const uint32_t bits = __float_as_uint(s);
         uint32_t kept = (bits + 0x80u) & 0xffffff00u;
         if (s != s)
@@ -381,8 +383,8 @@ __device__ __forceinline__ void finish_again(const BaseArgs &a, int mi, int t, i
 // fp32 (see the top): two token blocks multiply q - z itself (EXACT), whose unpacking two
 // blocks share; one token block joins the sums after every 32 inputs, where each is rounded
 // once at its full size, since the small pieces of x come first (4096 -> 4096: 24 tokens
-// 16.3 us against 17.0 with sums of a whole group, 64 tokens 33.8 / 34.3; one token of
-// 4096 -> 4096 8.7 / 8.5, 5120 -> 10240 15.2 / 14.3, gated 4096 -> 11008 21.2 / 18.9, and
+// 16.4 us against 17.0 with sums of a whole group, 64 tokens 33.8 / 34.3; one token of
+// 4096 -> 4096 8.8 / 8.5, 5120 -> 10240 14.8 / 14.3, gated 4096 -> 11008 21.1 / 18.9, and
 // 27 with q - z).
 template <typename XT> struct RawX;        // eight inputs of a token as they were loaded
 template <> struct RawX<uint16_t> {
@@ -686,14 +688,13 @@ __device__ __forceinline__ bool item_of(const BaseArgs &a, int &mi, int &c_tile,
 //
 // bf16 takes 64 x 256 tiles (MT = NT = 4), whose 64 fp32 sums, 64 registers of
 // unpacked weights and two steps of x fill the 256 registers of two waves a SIMD: two
-// workgroups a CU, each under the other's waits.  Measured on 8192 tokens: 4096 -> 4096
-// with a residual 301 us (913 TFLOP/s), gated 4096 -> 11008 1495 us (988 TFLOP/s; a
+// workgroups a CU, each under the other's waits.  Groups of 32 with zero points spill 3
+// to 6 of them, and x through registers 4 to 16.  Measured on 8192 tokens: 4096 -> 4096
+// with a residual 302 us (909 TFLOP/s), gated 4096 -> 11008 1495 us (988 TFLOP/s; a
 // library's bf16 product of 8192^3 reaches 1375 on the same card).  The matrix cores
-// are busy half of the time and the vector unit, which unpacks, scales and also issues
-// the matrix instructions, 0.7 of it; taking out the reads of x from LDS gains 23%,
-// unpacking 10%, scaling 6%, the loads of x or w 8% each, so no single one bounds it.
-// One workgroup of eight waves on 128 x 256 with weights in LDS too was slower (1642
-// against 1562 us then).
+// are busy half of the time, and the vector unit, which unpacks, scales and also issues
+// the matrix instructions, 0.7 of it.  One workgroup of eight waves on 128 x 256 with
+// weights in LDS too was slower (1642 against 1562 us then).
 template <typename XT, int MT, int NT, int KW, int SPB, bool GATED> struct TileLds {
     static constexpr int P = GATED ? 2 : 1;
     static constexpr int BM = 16 * MT, BN = 64 * (NT / P);
@@ -860,8 +861,8 @@ __device__ __forceinline__ void base_tile(const BaseArgs &a, TileLds<XT, MT, NT,
     auto w_block = [&](int k) __attribute__((always_inline)) { return min(k * KW + kg, KB - 1); };
 
     load_w(w_block(0));
-    // blocks past the last one are read as zeros, staged and never multiplied, so that
-    // the loop has no branches
+    // blocks past the last one are staged too (as zeros, or with DX the rows' last inputs
+    // again) and never multiplied, so that the loop has no branches
     if constexpr (DX) {
         dma_x(0, kg);
         dma_x(1, KW + kg);
@@ -1039,21 +1040,22 @@ __global__ __launch_bounds__(256 * KW, KW == 1 ? 2 : 1) void base_tile_kernel(Ba
 // 16 MT tokens x CW waves of 16 NT columns splits the K blocks over KW groups of waves,
 // and x, weights and scales are all brought to LDS by direct-to-LDS loads, S - 1 blocks
 // ahead and without registers.  Each wave forms the sums of x of all its rows itself,
-// in the block they belong to.  24 tokens of 11008 -> 4096 take 15.7 us (few-token
-// kernel 19.4), 64 tokens of gated 4096 -> 11008 23.3 (54).  Per K block of a group the
+// in the block they belong to.  24 tokens of 11008 -> 4096 take 15.8 us (few-token
+// kernel 19.4), 64 tokens of gated 4096 -> 11008 23.0 (54).  Per K block of a group the
 // LDS reads, the unpacking and a chain of products follow each other: that latency,
 // times the blocks of a group, is the time.  So LDS goes to groups before stages: with 2
 // stages of more groups in place of 3 or 4 of 2 groups, 100 tokens of 11008 -> 11008 take
 // 48.2 us (51.8), 64 tokens of it 33.8 (35.4), and 64 tokens of 4096 -> 11008 in groups of
-// 32 19.4 (22.7).  The small tiles, with 4 groups already, keep 3 or 4 stages; the
-// largest, 64 x 384 on 8 waves of 48 columns, fill LDS with one group of 3 (4 waves of 96
-// columns, one a SIMD: 512 tokens of 5120 -> 10240 86.5 us against 68.5).  A wave takes NT
-// weight blocks in a row of gate's and then up's, so it may have blocks of one only.
+// 32 19.4 (22.7).  The 32 x 32 tiles, whose 4 groups are small, keep 3 stages, and so do
+// the 32 x 64 where there is one scale a block; the largest, 64 x 384 on 8 waves of 48
+// columns, fill LDS with one group of 3 (4 waves of 96 columns, one a SIMD: 512 tokens of
+// 5120 -> 10240 86.5 us against 68.5).  A wave takes NT weight blocks in a row of gate's
+// and then up's, so it may have blocks of one only.
 // Without zero points the products start at -24 sum x, which halves the vector work per
 // sum but waits for that sum first: 512 tokens of 5120 -> 10240 in groups of 64 84 -> 74
 // us, gated 256 tokens 63 -> 60, 64 tokens of 4096 -> 11008 in groups of 32 19.1 -> 17.3;
-// the smallest grids, which wait most, lose a little (64 tokens of 4096 -> 4096 8.8 -> 8.9,
-// of gated 4096 -> 11008 23.0 -> 24.4).
+// the smallest grids, which wait most, gain nothing or lose a little (64 tokens of 4096 ->
+// 4096 8.8 us with zero points and 8.9 without, of gated 4096 -> 11008 23.0 and 23.4).
 //
 // Block k of a group lies in stage k % S; block k + S - 1 is loaded into the stage of
 // block k - 1 once every wave has read that.  Every wave issues the same number of loads
@@ -1352,7 +1354,7 @@ bool one_per_cu(const BaseArgs &args, int BM, int BN)
 // bf16, 5120 -> 10240: 1 token 8.3 against 8.5, 4 tokens 10.2 / 8.6, 16 tokens
 // 17.1 / 9.4; gated 4096 -> 11008, whose two weights share x already: 8 tokens
 // 12.2 / 12.2, 16 tokens 15.8 / 13.0; fp32, which also splits x into bf16 pieces less
-// often: 1 token of 5120 -> 10240 21.0 / 14.4).  With fewer blocks they would leave CUs
+// often: 1 token of 5120 -> 10240 21.8 / 14.8).  With fewer blocks they would leave CUs
 // idle (4096 -> 4096, 16 tokens: 6.5 / 7.8).  Groups of 32 keep four scales a block: two
 // column blocks of gate and of up are what the registers hold.
 //
@@ -1380,8 +1382,8 @@ hipError_t launch_sized(const BaseArgs &a, hipStream_t st)
         return launch_few<XT, 1, 1, SPB, GATED, 8, GATED && !WIDE ? 1 : 2>(a, st);
     }
     if constexpr (WIDE) {
-        // (24 tokens: 4096 -> 4096 16.8 us against 34, 5120 -> 10240 51 against 41; 128 tokens
-        // of 1000 -> 1296 11.6 against 14.4, 256 tokens 16.6 against 14.7)
+        // (24 tokens: 4096 -> 4096 16.4 us against 34, 5120 -> 10240 51 against 42; 128 tokens
+        // of 1000 -> 1296 9.4 against 12.0, 256 tokens 13.1 against 12.4)
         if ((int64_t)blocks * ((a.T + 31) / 32) <= 2 * kCus)
             return launch_few<XT, 2, 1, SPB, GATED, 8, 1>(a, st);
         if (one_per_cu<GATED>(a, 32, GATED ? 64 : 128))

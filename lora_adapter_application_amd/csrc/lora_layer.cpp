@@ -7,8 +7,9 @@
 // side stream and records an event of its own, which the stream of every later
 // base product waits for once; before it overwrites weights the side stream waits
 // for the tail of each stream that has launched a base product since the last base
-// load.  Slot loads and base products do not wait for each other: the adapters that
-// a step misses can be uploaded under its base products.
+// load.  A slot load waits for a stream only if that has read slots since the last one (and
+// then for all that is on it), and base products wait for no slot load: the adapters that a
+// step misses can be uploaded under its base products.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -202,8 +203,9 @@ int do_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scal
         st.base_since_load = false;
     }
     // Weights on this device are repacked from where they are, others through the
-    // ctx's stage, as many rows at a time as it takes (16 at least: it holds
-    // 16 (d_in + d_out) elements of 2 or 4 bytes, and 16 rows need under 11 d_in).
+    // ctx's stage, as many rows at a time as it takes (16 at least: it holds 16 (d_in + d_out)
+    // elements of 2 or 4 bytes, 32 d_in + 256 or more, and 16 rows with groups of 32 or more
+    // need at most 16 (d_in / 2 + 5 (d_in / 32 + 1)) + 48, under 11 d_in + 128).
     const int64_t row_q = sh.d_in / 2, row_s = 4ll * groups, row_z = zero ? groups : 0;
     int64_t row_bytes = (local[0] ? 0 : row_q) + (local[1] ? 0 : row_s) + (local[2] ? 0 : row_z);
     int64_t rows = sh.d_out;

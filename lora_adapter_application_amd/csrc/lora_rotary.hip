@@ -11,9 +11,12 @@
 // A workgroup owns one token and a share of its heads: it forms the token's
 // table of cosines and sines in LDS once, and each thread keeps the entries of
 // its piece of a head in registers while it walks the heads.  Bytes bound it:
-// 32,556 tokens of 64 heads of 128 (1.07 GB) take 177 us, 6.0 TB/s (a copy of 2 GiB
-// reaches 4.85; a third of these bytes fits the last-level cache); 512 tokens of 72
-// heads (19 MB) 5.7 us, of which a call costs the host 3.4.
+// 32,556 tokens of 64 heads of 128 (1.07 GB) take 176 us, 6.1 TB/s (a copy of 2 GiB
+// reaches 4.85; a third of these bytes fits the last-level cache).  Few tokens take one
+// chain, position, angle, sine and cosine, barrier, first load: 512 tokens of 72 heads
+// (19 MB) 5.7 us.  Sizes and addresses off 16 bytes go one element at a time (V = 1):
+// 8192 tokens of 40 heads of 128 off a boundary 85 us, on it 34; of 40 heads of 80 with 20
+// turned 49 us out of place, 19 in place.
 #include <hip/hip_runtime.h>
 
 #include "lora_layer.h"
