@@ -415,7 +415,8 @@ int lora_apply_group_noalloc(lora_ctx *ctx, int32_t n, const int32_t *modules,
  * Errors: LORA_ERR_BAD_MODULE; q or scale NULL, a bad group_size or a d_in above
  * 2^22 -> LORA_ERR_INVALID_ARGUMENT; LORA_ERR_HOST_NOT_PINNED;
  * LORA_ERR_OUT_OF_MEMORY.  After those the module has the weight it had; after
- * LORA_ERR_HIP it may have none (its products are refused) until a load succeeds.
+ * LORA_ERR_HIP it may have none until a load succeeds: its products are refused,
+ * and a replayed graph must not read it.
  */
 int lora_base_load(lora_ctx *ctx, int32_t module, const void *q, const float *scale,
                    const uint8_t *zero, int32_t group_size, const void *bias);
