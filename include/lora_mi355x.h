@@ -91,6 +91,10 @@ enum {
 #define LORA_FLAG_SLOT_INDEX_TOO_LARGE 0x1u  /* a token carried idx >= max_loras (skipped) */
 #define LORA_FLAG_FUSED_TIMEOUT 0x2u         /* a fused decode launch gave up waiting for a
                                                 tile's partials (its rows were left untouched) */
+#define LORA_FLAG_ATTEND_BATCH 0x4u          /* a prepared batch held a length, start or bound out of
+                                                range or out of order */
+#define LORA_FLAG_CACHE_PAGE 0x8u            /* an attended page was not in 0..pages-1 (skipped) */
+#define LORA_FLAG_CACHE_SLOT 0x10u           /* a stored or loaded slot was past the cache (skipped) */
 
 typedef struct {
     int64_t loads;          /* lora_slot_load calls that succeeded */
@@ -559,6 +563,167 @@ int lora_rotary_init(lora_rotary *out, const lora_rotary_params *params);
 int lora_rotary_group(lora_ctx *ctx, const lora_rotary *rotary, int32_t n,
                       const int32_t *modules, const void *const *x, void *const *y,
                       const int32_t *positions, int32_t n_tokens, void *stream);
+
+/* Limit of head_dim for lora_norm_rotary_group. */
+#define LORA_NORM_MAX_DIM 512
+
+/*
+ * lora_rotary_group with an RMS norm of each head in the same pass: for head h of token t,
+ *
+ *     z = x / sqrt( sum_i x_i^2 / head_dim + eps ) * weight
+ *
+ * and z is turned as lora_rotary_group turns x.  Norm and turn are formed in fp32 and
+ * rounded once.
+ *   weight  NULL, or [n] pointers: per member head_dim values of the ctx dtype on the
+ *           device, or NULL (1)
+ *   eps     finite, >= 0
+ * Other arguments, in-place use and errors as lora_rotary_group; a head_dim above
+ * LORA_NORM_MAX_DIM, a bad eps, or a y that overlaps a weight -> LORA_ERR_INVALID_ARGUMENT.
+ */
+int lora_norm_rotary_group(lora_ctx *ctx, const lora_rotary *rotary, int32_t n,
+                           const int32_t *modules, const void *const *x,
+                           const void *const *weight, double eps, void *const *y,
+                           const int32_t *positions, int32_t n_tokens, void *stream);
+
+/*
+ * A paged cache of one layer's keys and values: `pages` pages of page_size tokens, each
+ * token with kv_heads heads of head_dim keys and as many values.  Which page holds which
+ * tokens of which request is the caller's affair; a token's slot is page * page_size + its
+ * place in the page.
+ */
+typedef struct lora_cache lora_cache;
+
+/* How a cache holds its elements. */
+enum {
+    LORA_CACHE_NATIVE = 0,   /* in the ctx dtype */
+    LORA_CACHE_FP8 = 1,      /* 8-bit float, 4 exponent and 3 mantissa bits, largest 448 (e4m3) */
+    LORA_CACHE_INT8 = 2      /* -127..127 */
+};
+
+/* Limit of a cache's head_dim. */
+#define LORA_CACHE_MAX_DIM 256
+
+/*
+ * Create a cache, all zeros, on the ctx's device.
+ *   kind       LORA_CACHE_*
+ *   kv_heads   1..1024
+ *   head_dim   a multiple of 8, 8..LORA_CACHE_MAX_DIM (stored as 64, 96, 128 or 256)
+ *   page_size  a power of two, 32 or more
+ *   pages      1 or more, pages * page_size < 2^31
+ * In 8 bits a head of a token has one fp32 scale, max|x| / top with top 448 (FP8) or 127
+ * (INT8), and the codes round(x * top / max|x|), to the nearest, ties to even; heads whose
+ * largest value is below 2^-100 are held at the scale of 2^-100, and a head with an
+ * infinity or NaN reads as NaN throughout.
+ * The cache belongs to the ctx until lora_cache_destroy or lora_slots_destroy.  Errors:
+ * values out of range, a stream of the ctx under graph capture ->
+ * LORA_ERR_INVALID_ARGUMENT; LORA_ERR_OUT_OF_MEMORY; *out is NULL on every error.
+ */
+int lora_cache_create(lora_ctx *ctx, lora_cache **out, int32_t kind, int32_t kv_heads,
+                      int32_t head_dim, int32_t page_size, int32_t pages);
+
+/* Wait for the streams the ctx has launched on, then free the cache.  NULL is accepted; a
+ * handle that is no cache of the ctx, or a stream of the ctx under graph capture ->
+ * LORA_ERR_INVALID_ARGUMENT.  A captured graph that uses the cache must not be replayed any more. */
+int lora_cache_destroy(lora_ctx *ctx, lora_cache *cache);
+
+/*
+ * Write the keys and values of n_tokens tokens into their slots.
+ *   k, v   [n_tokens][kv_heads * head_dim], row-major, device, ctx dtype, e.g. the outputs of
+ *          the k and v projections after lora_norm_rotary_group
+ *   slots  int32[n_tokens], device: negative values skip their token (padding of a batch);
+ *          values past the cache skip theirs and set LORA_FLAG_CACHE_SLOT.  No slot may be
+ *          given twice.
+ * n_tokens == 0 is a no-op.  Errors: a handle that is no cache of the ctx, NULL pointers,
+ * n_tokens < 0 -> LORA_ERR_INVALID_ARGUMENT; n_tokens > max_tokens ->
+ * LORA_ERR_TOO_MANY_TOKENS.
+ */
+int lora_cache_store(lora_ctx *ctx, lora_cache *cache, const void *k, const void *v,
+                     const int32_t *slots, int32_t n_tokens, void *stream);
+
+/*
+ * Read tokens back: k[t], v[t] become what slots[t] holds, in 8 bits code * scale rounded to
+ * the ctx dtype.  Rows of skipped tokens (slots as in lora_cache_store; a slot may be given
+ * more than once) are left as they are.  k, v and slots must not overlap.  Errors as
+ * lora_cache_store.
+ */
+int lora_cache_load(lora_ctx *ctx, const lora_cache *cache, const int32_t *slots, void *k,
+                    void *v, int32_t n_tokens, void *stream);
+
+/* Limit of the requests, and of the prefixes, of one batch. */
+#define LORA_ATTEND_MAX_SEQS (1 << 20)
+
+/*
+ * The requests of one batch and what each attends to.  Arrays are int32 device memory of the
+ * caller, read by lora_attend_prepare and the lora_attend calls behind it, who keeps them
+ * alive and unchanged until the stream has passed those.
+ *
+ * Request i has the new tokens q_start[i] .. q_start[i+1]-1 of the batch (rows of q), the
+ * last ones of the lengths[i] tokens that its pages hold: its token number lengths[i] - n + j
+ * is new token j of n.  Token number s of the request is in page pages[i][s / page_size].
+ * Requests prefix_seqs[p] .. prefix_seqs[p+1]-1 share prefix p, prefix_lengths[p] tokens in
+ * the pages prefix_pages[p][...], in front of their own: the keys and values of one adapter's
+ * system prompt, say, which requests of other adapters cannot use, since their k and v
+ * projections differ.  Requests before prefix_seqs[0] and from prefix_seqs[n_prefixes] on
+ * have no prefix.
+ */
+typedef struct {
+    int32_t n_tokens;               /* rows of q and y */
+    int32_t n_seqs;                 /* requests */
+    int32_t max_queries;            /* most new tokens of one request, >= 1 */
+    int32_t max_pages;              /* columns of pages */
+    const int32_t *q_start;         /* [n_seqs + 1], ascending, or NULL: request i has token i */
+    const int32_t *lengths;         /* [n_seqs], 0..max_pages * page_size */
+    const int32_t *pages;           /* [n_seqs][max_pages] */
+    int32_t n_prefixes;             /* 0: none, and the rest is not read */
+    int32_t prefix_max_pages;       /* columns of prefix_pages */
+    const int32_t *prefix_seqs;     /* [n_prefixes + 1], ascending, 0..n_seqs */
+    const int32_t *prefix_lengths;  /* [n_prefixes], 0..prefix_max_pages * page_size */
+    const int32_t *prefix_pages;    /* [n_prefixes][prefix_max_pages] */
+} lora_attend_batch;
+
+/*
+ * Cut the attention of a batch into work of equal size, on the device, for lora_attend calls
+ * with q_heads query heads and caches of `cache`'s kv_heads, head_dim and page_size (of any
+ * kind): once a step for all layers.  q_heads is a multiple of kv_heads; query head h reads
+ * key-value head h / (q_heads / kv_heads).
+ * The plan stays valid until the next lora_attend_prepare.  It and the parts of lora_attend
+ * are kept in the ctx's attention workspace, which grows with the batches prepared.  Under
+ * graph capture it cannot grow: prepare a batch of the same sizes once before.  A captured
+ * lora_attend needs its lora_attend_prepare in the same capture; the replayed graph reads the
+ * batch's arrays as they are then, so it serves every batch of these sizes (requests without
+ * new tokens pad it).  Graphs and eager calls share the workspace and must be ordered, as
+ * every other use of the ctx.
+ * Values in the arrays that are out of range or out of order are clamped and set
+ * LORA_FLAG_ATTEND_BATCH; a batch whose requests claim the same tokens may get no work at all.
+ * Errors: a handle that is no cache of the ctx, sizes out of range, NULL arrays, a workspace
+ * too small under capture -> LORA_ERR_INVALID_ARGUMENT; n_tokens > max_tokens or n_tokens *
+ * q_heads >= 2^31 -> LORA_ERR_TOO_MANY_TOKENS; LORA_ERR_OUT_OF_MEMORY.
+ */
+int lora_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads,
+                        const lora_attend_batch *batch, void *stream);
+
+/*
+ * Attention of the prepared batch over one layer's cache: for query head h of new token j of
+ * request i, with s over the tokens of its prefix and its request's up to token j itself,
+ *
+ *     y = sum_s p_s v_s / sum_s p_s,   p_s = exp( scale * q . k_s )
+ *
+ *   q, y   [n_tokens][q_heads * head_dim], row-major, device, ctx dtype; must not overlap
+ *   scale  > 0, e.g. 1 / sqrt(head_dim)
+ * The keys and values of the batch's new tokens must be stored before (lora_cache_store on
+ * the same stream).  A prefix is read once for all of its requests of few new tokens.  Scores,
+ * maxima, sums and outputs are kept in fp32; a bf16 ctx rounds the weights p_s to bf16 for
+ * their product with the values, and y once.  The order of the sums goes by the batch, so
+ * equal calls give equal bits.  Tokens that a row does not see change nothing, whatever their
+ * slots hold.  A token that sees nothing (a request of length 0 without a prefix) gets zeros;
+ * rows of q that belong to no request leave their row of y as it is.  Tokens on a page
+ * outside the cache are skipped and set LORA_FLAG_CACHE_PAGE; a row that they leave with nothing becomes NaN.
+ * Errors: no prepared batch, or one prepared outside of the capture that the call is in, or in
+ * one that it is not in -> LORA_ERR_NO_PLAN; a cache of another shape than the prepared, NULL or
+ * overlapping buffers, a bad scale -> LORA_ERR_INVALID_ARGUMENT.
+ */
+int lora_attend(lora_ctx *ctx, const lora_cache *cache, const void *q, void *y, double scale,
+                void *stream);
 
 /* Wait for the streams the ctx has launched on (not for the whole device),
  * return the sticky LORA_FLAG_* bits in *flags and clear them. */

@@ -35,6 +35,9 @@ LORA_ERR_NO_PLAN = -9
 
 LORA_FLAG_SLOT_INDEX_TOO_LARGE = 0x1
 LORA_FLAG_FUSED_TIMEOUT = 0x2
+LORA_FLAG_ATTEND_BATCH = 0x4
+LORA_FLAG_CACHE_PAGE = 0x8
+LORA_FLAG_CACHE_SLOT = 0x10
 
 # Every symbol the header declares, for the export check.
 EXPORTS = ("lora_slots_create", "lora_slots_destroy", "lora_slot_load", "lora_slot_load_ex",
@@ -44,7 +47,9 @@ EXPORTS = ("lora_slots_create", "lora_slots_destroy", "lora_slot_load", "lora_sl
            "lora_shrink_group", "lora_expand_group", "lora_apply_group",
            "lora_apply_group_noalloc", "lora_apply_group_fused",
            "lora_base_load", "lora_base", "lora_base_group", "lora_base_gated",
-           "lora_rotary_init", "lora_rotary_group",
+           "lora_rotary_init", "lora_rotary_group", "lora_norm_rotary_group",
+           "lora_cache_create", "lora_cache_destroy", "lora_cache_store", "lora_cache_load",
+           "lora_attend_prepare", "lora_attend",
            "lora_get_device_flags", "lora_get_stats", "lora_profile_begin", "lora_profile_end",
            "lora_status_string", "lora_last_error")
 
@@ -58,6 +63,8 @@ ACTIVATIONS = {"silu": LORA_ACT_SILU, "gelu": LORA_ACT_GELU, "gelu_tanh": LORA_A
 LORA_ROTARY_MAX_DIM = 256
 ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "yarn": 2, "banded": 3}
+
+CACHE_KINDS = {"native": 0, "fp8": 1, "int8": 2}
 
 
 class LoraError(RuntimeError):
@@ -92,6 +99,13 @@ class Rotary(ctypes.Structure):
     _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
                 ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
                 ("turns", ctypes.c_double * (LORA_ROTARY_MAX_DIM // 2))]
+
+
+class _AttendBatch(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_tokens", "n_seqs", "max_queries", "max_pages")] +
+                [(n, ctypes.c_void_p) for n in ("q_start", "lengths", "pages")] +
+                [(n, ctypes.c_int32) for n in ("n_prefixes", "prefix_max_pages")] +
+                [(n, ctypes.c_void_p) for n in ("prefix_seqs", "prefix_lengths", "prefix_pages")])
 
 
 _lib = None
@@ -140,6 +154,15 @@ def load_library(path: str = LIB_PATH):
                              ctypes.c_int),
         "lora_rotary_group": ([P, ctypes.POINTER(Rotary), I32, ctypes.POINTER(I32),
                                ctypes.POINTER(P), ctypes.POINTER(P), P, I32, P], ctypes.c_int),
+        "lora_norm_rotary_group": ([P, ctypes.POINTER(Rotary), I32, ctypes.POINTER(I32),
+                                    ctypes.POINTER(P), ctypes.POINTER(P), D, ctypes.POINTER(P), P,
+                                    I32, P], ctypes.c_int),
+        "lora_cache_create": ([P, ctypes.POINTER(P), I32, I32, I32, I32, I32], ctypes.c_int),
+        "lora_cache_destroy": ([P, P], ctypes.c_int),
+        "lora_cache_store": ([P, P, P, P, P, I32, P], ctypes.c_int),
+        "lora_cache_load": ([P, P, P, P, P, I32, P], ctypes.c_int),
+        "lora_attend_prepare": ([P, P, I32, ctypes.POINTER(_AttendBatch), P], ctypes.c_int),
+        "lora_attend": ([P, P, P, P, D, P], ctypes.c_int),
         "lora_get_device_flags": ([P, ctypes.POINTER(ctypes.c_uint32)], ctypes.c_int),
         "lora_get_stats": ([P, ctypes.POINTER(_Stats)], ctypes.c_int),
         "lora_profile_begin": ([P, I32], ctypes.c_int),
@@ -506,6 +529,145 @@ def lora_rotary_group(ctx, rotary: Rotary, modules: Sequence[int], x: Sequence, 
                                             _stream_of(stream, positions)), ctx)
 
 
+def _weights(n, weight):
+    if weight is None:
+        return None
+    return _group([0] * n, weight, "weight")[2]
+
+
+def lora_norm_rotary_group(ctx, rotary: Rotary, modules: Sequence[int], x: Sequence, y: Sequence,
+                           positions, weight: Optional[Sequence] = None, eps: float = 1e-6,
+                           n_tokens: Optional[int] = None, stream=None) -> None:
+    """lora_rotary_group with an RMS norm of each head in front, times weight[i] ([head_dim],
+    or None: 1)."""
+    import torch
+    if n_tokens is None:
+        n_tokens = positions.numel()
+    if n_tokens:
+        _require_cuda(positions, "positions", torch.int32, n_tokens)
+    n, mods, xp = _group(modules, x, "x")
+    _, _, yp = _group(modules, y, "y")
+    _check(load_library().lora_norm_rotary_group(ctx, ctypes.byref(rotary), n, mods, xp,
+                                                 _weights(n, weight), float(eps), yp,
+                                                 _ptr(positions), int(n_tokens),
+                                                 _stream_of(stream, positions)), ctx)
+
+
+# the paged cache and attention over it
+
+def _cache_kind(kind) -> int:
+    if isinstance(kind, str):
+        if kind not in CACHE_KINDS:
+            raise ValueError(f"cache kind {kind!r} is not one of {sorted(CACHE_KINDS)}")
+        return CACHE_KINDS[kind]
+    return int(kind)
+
+
+def lora_cache_create(ctx, kv_heads: int, head_dim: int, pages: int, page_size: int = 64,
+                      kind="native"):
+    """Returns an opaque cache handle (int).  kind: "native", "fp8" or "int8"."""
+    out = ctypes.c_void_p()
+    _check(load_library().lora_cache_create(ctx, ctypes.byref(out), _cache_kind(kind),
+                                            int(kv_heads), int(head_dim), int(page_size),
+                                            int(pages)), ctx)
+    return out.value
+
+
+def lora_cache_destroy(ctx, cache) -> None:
+    _check(load_library().lora_cache_destroy(ctx, cache), ctx)
+
+
+def lora_cache_store(ctx, cache, k, v, slots, n_tokens: Optional[int] = None, stream=None) -> None:
+    """Write the keys and values of n_tokens tokens into their slots (int32)."""
+    import torch
+    if n_tokens is None:
+        n_tokens = slots.numel()
+    if n_tokens:
+        _require_cuda(slots, "slots", torch.int32, n_tokens)
+        _require_cuda(k, "k")
+        _require_cuda(v, "v")
+    _check(load_library().lora_cache_store(ctx, cache, _ptr(k), _ptr(v), _ptr(slots),
+                                           int(n_tokens), _stream_of(stream, slots)), ctx)
+
+
+def lora_cache_load(ctx, cache, slots, k, v, n_tokens: Optional[int] = None, stream=None) -> None:
+    """Read the keys and values of slots (int32) back into k and v."""
+    import torch
+    if n_tokens is None:
+        n_tokens = slots.numel()
+    if n_tokens:
+        _require_cuda(slots, "slots", torch.int32, n_tokens)
+        _require_cuda(k, "k")
+        _require_cuda(v, "v")
+    _check(load_library().lora_cache_load(ctx, cache, _ptr(slots), _ptr(k), _ptr(v),
+                                          int(n_tokens), _stream_of(stream, slots)), ctx)
+
+
+class AttendBatch:
+    """The requests of one batch (lora_attend_batch): int32 device tensors lengths
+    [requests], pages [requests][most pages] and q_start [requests + 1] (None: request i has
+    the new token i), which this object keeps alive."""
+
+    def __init__(self, lengths, pages, q_start=None, max_queries: int = 1,
+                 n_tokens: Optional[int] = None):
+        self.lengths, self.pages, self.q_start = lengths, pages, q_start
+        self.max_queries, self.n_tokens = int(max_queries), n_tokens
+        self.n_seqs = int(lengths.numel())
+        self._table("pages", pages, self.n_seqs)
+        self._require("lengths", lengths, self.n_seqs)
+        if q_start is not None:
+            self._require("q_start", q_start, self.n_seqs + 1)
+        self.prefix_seqs = self.prefix_lengths = self.prefix_pages = None
+
+    @staticmethod
+    def _require(name, t, numel):
+        import torch
+        _require_cuda(t, name, torch.int32, numel)
+
+    def _table(self, name, t, rows):
+        if t.dim() != 2 or t.shape[0] < rows:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {rows} rows")
+        self._require(name, t, 0)
+
+    def share(self, prefix_seqs, prefix_lengths, prefix_pages):
+        """Requests prefix_seqs[p] .. prefix_seqs[p + 1] - 1 share prefix p."""
+        n = int(prefix_lengths.numel())
+        self._require("prefix_lengths", prefix_lengths, n)
+        self._require("prefix_seqs", prefix_seqs, n + 1)
+        self._table("prefix_pages", prefix_pages, n)
+        self.prefix_seqs, self.prefix_lengths, self.prefix_pages = prefix_seqs, prefix_lengths, prefix_pages
+        return self
+
+    def tensors(self):
+        return [t for t in (self.lengths, self.pages, self.q_start, self.prefix_seqs,
+                            self.prefix_lengths, self.prefix_pages) if t is not None]
+
+    def _struct(self, n_tokens):
+        shared = self.prefix_lengths is not None
+        return _AttendBatch(int(n_tokens), self.n_seqs, self.max_queries, int(self.pages.shape[1]),
+                            _ptr(self.q_start), _ptr(self.lengths), _ptr(self.pages),
+                            int(self.prefix_lengths.numel()) if shared else 0,
+                            int(self.prefix_pages.shape[1]) if shared else 0,
+                            _ptr(self.prefix_seqs), _ptr(self.prefix_lengths),
+                            _ptr(self.prefix_pages))
+
+
+def lora_attend_prepare(ctx, cache, q_heads: int, batch: AttendBatch, n_tokens: int,
+                        stream=None) -> None:
+    """Plan the attention of a batch of n_tokens new tokens, once a step for all layers."""
+    s = batch._struct(n_tokens)
+    _check(load_library().lora_attend_prepare(ctx, cache, int(q_heads), ctypes.byref(s),
+                                              _stream_of(stream, batch.lengths)), ctx)
+
+
+def lora_attend(ctx, cache, q, y, scale: float, stream=None) -> None:
+    """Attention of the prepared batch over one layer's cache."""
+    _require_cuda(q, "q")
+    _require_cuda(y, "y")
+    _check(load_library().lora_attend(ctx, cache, _ptr(q), _ptr(y), float(scale),
+                                      _stream_of(stream, q)), ctx)
+
+
 def lora_get_device_flags(ctx) -> int:
     v = ctypes.c_uint32(0)
     _check(load_library().lora_get_device_flags(ctx, ctypes.byref(v)), ctx)
@@ -532,7 +694,27 @@ def lora_profile_end(ctx) -> dict:
 
 
 # ---------------------------------------------------------------------------
-# convenience owner of a ctx
+# convenience owners of a ctx and of a cache
+
+class Cache:
+    """A paged cache of a slot pool (Slots.cache)."""
+
+    def __init__(self, slots, kv_heads, head_dim, pages, page_size, kind):
+        self.slots, self.kv_heads, self.head_dim = slots, int(kv_heads), int(head_dim)
+        self.pages, self.page_size, self.kind = int(pages), int(page_size), kind
+        self.handle = lora_cache_create(slots.ctx, kv_heads, head_dim, pages, page_size, kind)
+
+    def close(self):
+        if self.handle and self.slots.ctx:
+            lora_cache_destroy(self.slots.ctx, self.handle)
+        self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
 
 class Slots:
     """A slot pool for a list of (d_in, d_out) modules, in bf16 or fp32."""
@@ -547,6 +729,7 @@ class Slots:
         self.device = int(device)
         self._loading = []       # sources of base loads that may still be read
         self._loading_bytes = 0
+        self._attended = None    # the prepared batch, its tokens and query heads
         self.ctx = lora_slots_create(max_loras, max_rank, self.modules,
                                      LORA_BF16 if dtype == "bf16" else LORA_FP32, max_tokens,
                                      device)
@@ -672,6 +855,62 @@ class Slots:
         self._check_rotary(modules, x, y, positions, n)
         lora_rotary_group(self.ctx, rotary, modules, x, y, positions, n, stream)
 
+    def _check_weights(self, rotary, weight):
+        for w in weight or ():
+            self._check_rows("weight", w, 1, rotary.head_dim)
+
+    def norm_rotary_group(self, rotary, modules, x, y, positions, weight=None, eps=1e-6,
+                          n_tokens=None, stream=None):
+        n = positions.numel() if n_tokens is None else int(n_tokens)
+        self._check_rotary(modules, x, y, positions, n)
+        self._check_weights(rotary, weight)
+        lora_norm_rotary_group(self.ctx, rotary, modules, x, y, positions, weight, eps, n, stream)
+
+    def cache(self, kv_heads, head_dim, pages, page_size=64, kind="native"):
+        """A paged cache of keys and values (lora_cache_create)."""
+        return Cache(self, kv_heads, head_dim, pages, page_size, kind)
+
+    def _check_slots(self, cache, k, v, slots, n_tokens):
+        import torch
+        _require_cuda(slots, "slots", torch.int32, n_tokens)
+        for name, t in (("k", k), ("v", v)):
+            self._check_rows(name, t, n_tokens, cache.kv_heads * cache.head_dim)
+
+    def cache_store(self, cache, k, v, slots, n_tokens=None, stream=None):
+        n = slots.numel() if n_tokens is None else int(n_tokens)
+        self._check_slots(cache, k, v, slots, n)
+        lora_cache_store(self.ctx, cache.handle, k, v, slots, n, stream)
+
+    def cache_load(self, cache, slots, k, v, n_tokens=None, stream=None):
+        n = slots.numel() if n_tokens is None else int(n_tokens)
+        self._check_slots(cache, k, v, slots, n)
+        lora_cache_load(self.ctx, cache.handle, slots, k, v, n, stream)
+
+    def _check_batch(self, batch):
+        for t in batch.tensors():
+            if t.device.index != self.device:
+                raise ValueError(f"the batch is on {t.device}, the slot pool on device {self.device}")
+
+    def attend_prepare(self, cache, q_heads, batch, n_tokens=None, stream=None):
+        """lora_attend_prepare; n_tokens: the rows of q (default: those of the batch, or one
+        a request)."""
+        if n_tokens is None:
+            n_tokens = batch.n_seqs if batch.n_tokens is None else batch.n_tokens
+        self._check_batch(batch)
+        lora_attend_prepare(self.ctx, cache.handle, q_heads, batch, n_tokens, stream)
+        self._attended = (batch, int(n_tokens), int(q_heads))
+
+    def _check_attend(self, cache, q_heads, q, y, n_tokens):
+        for name, t in (("q", q), ("y", y)):
+            self._check_rows(name, t, n_tokens, q_heads * cache.head_dim)
+
+    def attend(self, cache, q, y, scale=None, stream=None):
+        """Attention of the prepared batch; scale: default 1 / sqrt(head_dim)."""
+        if self._attended is not None:
+            self._check_attend(cache, self._attended[2], q, y, self._attended[1])
+        lora_attend(self.ctx, cache.handle, q, y, cache.head_dim ** -0.5 if scale is None else scale,
+                    stream)
+
     def _bound(self, fn, args, refs):
         """A function that makes the library call fn(ctx, *args), whose arguments `refs`
         keep alive."""
@@ -712,6 +951,55 @@ class Slots:
         return self._bound(load_library().lora_rotary_group,
                            (ctypes.byref(rotary), n, mods, xp, yp, _ptr(positions), n_tok,
                             _stream_of(stream, positions)), (rotary, x, y, positions))
+
+    def bind_norm_rotary(self, rotary, modules, x, y, positions, weight=None, eps=1e-6,
+                         n_tokens=None, stream=None):
+        """norm_rotary_group with its arguments marshalled once."""
+        n_tok = positions.numel() if n_tokens is None else int(n_tokens)
+        self._check_rotary(modules, x, y, positions, n_tok)
+        self._check_weights(rotary, weight)
+        n, mods, xp = _group(modules, x, "x")
+        _, _, yp = _group(modules, y, "y")
+        return self._bound(load_library().lora_norm_rotary_group,
+                           (ctypes.byref(rotary), n, mods, xp, _weights(n, weight), float(eps), yp,
+                            _ptr(positions), n_tok, _stream_of(stream, positions)),
+                           (rotary, x, y, positions, weight))
+
+    def bind_cache_store(self, cache, k, v, slots, n_tokens=None, stream=None):
+        """cache_store with its arguments marshalled once."""
+        n_tok = slots.numel() if n_tokens is None else int(n_tokens)
+        self._check_slots(cache, k, v, slots, n_tok)
+        return self._bound(load_library().lora_cache_store,
+                           (cache.handle, _ptr(k), _ptr(v), _ptr(slots), n_tok,
+                            _stream_of(stream, slots)), (cache, k, v, slots))
+
+    def bind_cache_load(self, cache, slots, k, v, n_tokens=None, stream=None):
+        """cache_load with its arguments marshalled once."""
+        n_tok = slots.numel() if n_tokens is None else int(n_tokens)
+        self._check_slots(cache, k, v, slots, n_tok)
+        return self._bound(load_library().lora_cache_load,
+                           (cache.handle, _ptr(slots), _ptr(k), _ptr(v), n_tok,
+                            _stream_of(stream, slots)), (cache, k, v, slots))
+
+    def bind_attend(self, cache, q_heads, q, y, batch, scale=None, prepare=True, stream=None):
+        """attend_prepare (unless prepare is False: then the batch prepared last is used, as the
+        layers of a model share one) and attend, marshalled once."""
+        n_tok = int(q.shape[0])
+        self._check_attend(cache, q_heads, q, y, n_tok)
+        self._check_batch(batch)
+        lib, st = load_library(), _stream_of(stream, q)
+        s = batch._struct(n_tok)
+        ctx, handle, qp, yp = self.ctx, cache.handle, _ptr(q), _ptr(y)
+        factor = float(cache.head_dim ** -0.5 if scale is None else scale)
+        refs = (cache, q, y, batch, s)
+
+        def call():
+            _ = refs
+            rc = lib.lora_attend_prepare(ctx, handle, q_heads, ctypes.byref(s), st) if prepare else 0
+            rc = rc or lib.lora_attend(ctx, handle, qp, yp, factor, st)
+            if rc:
+                _check(rc, ctx)
+        return call
 
     def bind_step(self, groups, idx, stream=None, prepare=True, fused=False):
         """One step with its arguments marshalled once: lora_plan_prepare of idx

@@ -6,7 +6,10 @@ The library is the C ABI of ``include/lora_mi355x.h``: the runtime
 (``csrc/lora_runtime.cpp``), the low-rank kernels (``csrc/lora_kernels.hip``),
 the saved-module kernels (``csrc/lora_saved.hip``), and the frozen part of a
 layer: its host side (``csrc/lora_layer.cpp``), the 4-bit base products
-(``csrc/lora_base.hip``) and rotary positions (``csrc/lora_rotary.hip``).
+(``csrc/lora_base.hip``) and rotary positions (``csrc/lora_rotary.hip``); and what stands
+between its projections: the host side (``csrc/lora_attend.cpp``), head norms with rotary
+positions (``csrc/lora_norm.hip``), the paged cache (``csrc/lora_cache.hip``) and attention
+over it (``csrc/lora_attend.hip``).
 """
 from __future__ import annotations
 
@@ -26,7 +29,8 @@ ARCH = "gfx950"
 
 SOURCES = [os.path.join(CSRC, name) for name in
            ("lora_kernels.hip", "lora_saved.hip", "lora_base.hip", "lora_rotary.hip",
-            "lora_runtime.cpp", "lora_layer.cpp")]
+            "lora_norm.hip", "lora_cache.hip", "lora_attend.hip",
+            "lora_runtime.cpp", "lora_layer.cpp", "lora_attend.cpp")]
 
 # Packed-fp32 instructions stay disabled for device code (the host pass warns
 # that it does not know the feature; that is harmless).

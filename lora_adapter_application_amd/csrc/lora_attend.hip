@@ -1,0 +1,738 @@
+// lora_attend.hip -- gfx950 kernels of attention over the paged cache.
+//
+//     o = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale q . k_t - m),
+//
+// over the tokens t that a row sees: its prefix's and its own request's up to itself.  Both
+// products run on the matrix cores with the tokens as rows, S^T = K Q^T and O^T = V^T P^T: the
+// result layout of the first is the operand layout of the second (a lane keeps 8 tokens of one
+// row), so weights go from product to product in registers, and the cache's order makes every
+// operand one contiguous read.  The running maximum m is raised only when a score passes it by
+// 2^8, which keeps weights far inside fp32 and skips most rescalings; sums are fp32.  Weights are
+// rounded to bf16 for the second product of a bf16 ctx, by 2^-8 of a weight at most (as large an error
+// as that of the rounded result); the sum is that of the unrounded ones.
+#include <hip/hip_runtime.h>
+
+#include "lora_attend.h"
+
+namespace lora {
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+
+constexpr float kRaise = 8.f;        // a maximum is raised when a score passes it by 2^8
+#define kNone (-__builtin_inff())
+
+// ---------------------------------------------------------------------------
+// plan: one workgroup turns the batch's lengths into the two lists of tiles
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanTilesInLds = 4096;
+
+
+template <typename V>
+__device__ __forceinline__ V wave_scan(V v, int lane)
+{
+    for (int d = 1; d < 64; d <<= 1) {
+        const V o = __shfl_up(v, d);
+        if (lane >= d)
+            v += o;
+    }
+    return v;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b)
+{
+    __shared__ int32_t wave_sum[5][kPlanThreads / 64];
+    __shared__ int64_t unit_sum[kPlanThreads / 64];
+    __shared__ int32_t unit0[kPlanTilesInLds];
+    __shared__ int bad_all;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (!tid)
+        bad_all = 0;
+    const int entities = b.n_seqs + b.n_prefixes;
+    int32_t base[5] = {};
+    bool bad = false;
+
+    // requests, then prefixes (which need the requests' list)
+    for (int part = 0; part < 2; ++part) {
+        const int first = part ? b.n_seqs : 0, end = part ? entities : b.n_seqs;
+        if (part) {
+            if (!tid)
+                b.list_before[b.n_seqs] = base[4];
+            __threadfence_block();
+            __syncthreads();
+        }
+        for (int at = first; at < end; at += kPlanThreads) {
+            const int i = at + tid;
+            AttendEntity e{};
+            if (i < end) {
+                if (!part) {
+                    e = request_of(b, i, &bad);
+                } else {
+                    const int p = i - b.n_seqs;
+                    const int s0 = b.prefix_seqs[p], s1 = b.prefix_seqs[p + 1];
+                    bad |= s0 < 0 || s1 < s0 || s1 > b.n_seqs;
+                    const int lo = clamp_to(s0, 0, b.n_seqs), hi = clamp_to(s1, lo, b.n_seqs);
+                    const int l0 = b.list_before[lo];
+                    e = prefix_of_batch(b, p, l0, b.list_before[hi] - l0, &bad);
+                    b.prefix_list[p] = e.list;
+                }
+            }
+            int32_t mine[5] = {e.list ? 0 : e.tiles, e.list ? e.tiles : 0,
+                               e.keeps && !e.list ? e.tiles : 0, e.keeps && e.list ? e.tiles : 0, e.listed};
+            int32_t incl[5];
+            for (int c = 0; c < 5; ++c) {
+                incl[c] = wave_scan(mine[c], lane);
+                if (lane == 63)
+                    wave_sum[c][wave] = incl[c];
+            }
+            __syncthreads();
+            for (int c = 0; c < 5; ++c) {
+                int32_t before = base[c] + incl[c] - mine[c], all = 0;
+                for (int w = 0; w < kPlanThreads / 64; ++w) {
+                    const int32_t s = wave_sum[c][w];
+                    before += w < wave ? s : 0;
+                    all += s;
+                }
+                base[c] += all;
+                mine[c] = before;
+            }
+            __syncthreads();
+            if (i < end) {
+                for (int l = 0; l < 2; ++l) {
+                    b.tiles_before[l][i] = mine[l];
+                    b.kept_before[l][i] = mine[2 + l];
+                }
+                if (!part) {
+                    b.list_before[i] = mine[4];
+                    for (int j = 0; j < e.listed; ++j)
+                        if (mine[4] + j < b.n_tokens)
+                            b.listed[mine[4] + j] = e.token0 + j;
+                        else
+                            bad = true;
+                }
+            }
+        }
+    }
+    if (bad)
+        bad_all = 1;
+    if (!tid)
+        for (int l = 0; l < 2; ++l) {
+            b.tiles_before[l][entities] = base[l];
+            b.kept_before[l][entities] = base[2 + l];
+        }
+    __threadfence_block();
+    __syncthreads();
+    // a batch that fits no capacity gets no work; one that is only out of order, the work that
+    // its clamped values name
+    bool none = base[4] > b.n_tokens;
+    for (int l = 0; l < 2; ++l)
+        none |= base[l] > b.cap[l] || base[2 + l] > b.kept_cap[l];
+    const bool told = bad_all;
+
+    for (int l = 0; l < 2; ++l) {
+        const int tiles = none ? 0 : base[l];
+        int64_t total = 0;
+        for (int at = 0; at < tiles; at += kPlanThreads) {
+            const int x = at + tid;
+            AttendTile t{};
+            if (x < tiles) {
+                int lo = 0, hi = entities - 1;               // the last entity that starts at or before x
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (b.tiles_before[l][mid] <= x)
+                        lo = mid;
+                    else
+                        hi = mid - 1;
+                }
+                const int j = x - b.tiles_before[l][lo];
+                bool again = false;
+                AttendEntity e;
+                int list0 = 0;
+                if (lo < b.n_seqs) {
+                    e = request_of(b, lo, &again);
+                    if (e.prefix >= 0)
+                        list0 = b.list_before[lo] - b.list_before[clamp_to(b.prefix_seqs[e.prefix], 0, lo)];
+                } else {
+                    const int p = lo - b.n_seqs;
+                    const int s0 = clamp_to(b.prefix_seqs[p], 0, b.n_seqs);
+                    const int s1 = clamp_to(b.prefix_seqs[p + 1], s0, b.n_seqs);
+                    e = prefix_of_batch(b, p, b.list_before[s0], b.list_before[s1] - b.list_before[s0], &again);
+                }
+                t = tile_of(e, j, b.group, list0);
+                t.kept = e.keeps ? b.kept_before[l][lo] + j : -1;
+            }
+            const int64_t incl = wave_scan((int64_t)t.units, lane);
+            if (lane == 63)
+                unit_sum[wave] = incl;
+            __syncthreads();
+            int64_t before = total + incl - t.units;
+            for (int w = 0; w < kPlanThreads / 64; ++w) {
+                before += w < wave ? unit_sum[w] : 0;
+                total += unit_sum[w];
+            }
+            __syncthreads();
+            if (x < tiles) {
+                t.unit0 = (int32_t)before;
+                b.tiles[l][x] = t;
+                if (x < kPlanTilesInLds)
+                    unit0[x] = (int32_t)before;
+            }
+        }
+        const bool over = total > (1 << 30);
+        none |= over;
+        AttendList out{};
+        out.tiles = over ? 0 : tiles;
+        out.units = over ? 0 : (int32_t)total;
+        out.kept = base[2 + l];
+        const int64_t run = worker_run((int64_t)out.units * b.kv_heads, kAttendWorkers);
+        out.run = (int32_t)(run < 1 ? 1 : run);
+        if (!tid)
+            b.plan->list[l] = out;
+        __threadfence_block();
+        __syncthreads();
+        if (tid < kAttendWorkers && out.units) {
+            const int64_t u = (int64_t)tid * out.run;
+            if (u < (int64_t)out.units * b.kv_heads) {
+                const int32_t want = (int32_t)(u % out.units);
+                int lo = 0, hi = out.tiles - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    const int32_t v = mid < kPlanTilesInLds ? unit0[mid] : b.tiles[l][mid].unit0;
+                    if (v <= want)
+                        lo = mid;
+                    else
+                        hi = mid - 1;
+                }
+                b.start[l][tid] = lo;
+            }
+        }
+        __syncthreads();
+    }
+    if (!tid) {
+        b.plan->bad = none;
+        if (told || none)
+            atomicOr(b.flags, LORA_FLAG_ATTEND_BATCH);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// elements
+
+template <typename T> struct Frag;                       // 8 inputs of a matrix instruction's lane
+template <> struct Frag<uint16_t> { bf16x8 v; };
+template <> struct Frag<float> { float v[8]; };
+
+__device__ __forceinline__ f32x4 mma(const Frag<uint16_t> &a, const Frag<uint16_t> &b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(const Frag<float> &a, const Frag<float> &b, f32x4 c)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
+    return c;
+}
+
+__device__ __forceinline__ Frag<uint16_t> to_frag(const float *p, uint16_t)
+{
+    Frag<uint16_t> f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        f.v[j] = (__bf16)p[j];
+    return f;
+}
+__device__ __forceinline__ Frag<float> to_frag(const float *p, float)
+{
+    Frag<float> f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        f.v[j] = p[j];
+    return f;
+}
+
+// 8 elements as the cache holds them, and as a matrix instruction takes them.  Codes are
+// exact in bf16 (4 and 8 significant bits).
+template <typename T, int KIND> struct Held;
+template <> struct Held<uint16_t, kCacheNative> { uint4 r; };
+template <> struct Held<float, kCacheNative> { float4 r[2]; };
+template <typename T> struct Held<T, kCacheFp8> { uint2 r; };
+template <typename T> struct Held<T, kCacheInt8> { uint2 r; };
+
+template <typename T, int KIND>
+__device__ __forceinline__ Held<T, KIND> held_load(const char *base, int unit)
+{
+    return *(const Held<T, KIND> *)(base + (int64_t)unit * sizeof(Held<T, KIND>));
+}
+
+__device__ __forceinline__ void fp8_values(uint2 r, float *v)
+{
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int x = w ? r.y : r.x;
+        v[4 * w + 0] = __builtin_amdgcn_cvt_f32_fp8(x, 0);
+        v[4 * w + 1] = __builtin_amdgcn_cvt_f32_fp8(x, 1);
+        v[4 * w + 2] = __builtin_amdgcn_cvt_f32_fp8(x, 2);
+        v[4 * w + 3] = __builtin_amdgcn_cvt_f32_fp8(x, 3);
+    }
+}
+__device__ __forceinline__ void int8_values(uint2 r, float *v)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = (float)(int8_t)((j < 4 ? r.x : r.y) >> (8 * (j & 3)));
+}
+
+__device__ __forceinline__ Frag<uint16_t> frag_of(const Held<uint16_t, kCacheNative> &h)
+{
+    return {__builtin_bit_cast(bf16x8, h.r)};
+}
+__device__ __forceinline__ Frag<float> frag_of(const Held<float, kCacheNative> &h)
+{
+    return {{h.r[0].x, h.r[0].y, h.r[0].z, h.r[0].w, h.r[1].x, h.r[1].y, h.r[1].z, h.r[1].w}};
+}
+template <typename T>
+__device__ __forceinline__ Frag<T> frag_of(const Held<T, kCacheFp8> &h)
+{
+    float v[8];
+    fp8_values(h.r, v);
+    return to_frag(v, T());
+}
+template <typename T>
+__device__ __forceinline__ Frag<T> frag_of(const Held<T, kCacheInt8> &h)
+{
+    float v[8];
+    int8_values(h.r, v);
+    return to_frag(v, T());
+}
+
+// Elements from `keep` on become zero.
+template <typename T>
+__device__ __forceinline__ void cut(Frag<T> &f, int keep)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j >= keep)
+            f.v[j] = 0;
+}
+
+template <typename T> struct Io;
+template <> struct Io<uint16_t> {
+    static __device__ __forceinline__ float get(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+    static __device__ __forceinline__ uint16_t put(float f)
+    {
+        __bf16 h = (__bf16)f;
+        return __builtin_bit_cast(uint16_t, h);
+    }
+};
+template <> struct Io<float> {
+    static __device__ __forceinline__ float get(float v) { return v; }
+    static __device__ __forceinline__ float put(float f) { return f; }
+};
+
+template <typename T, int N> struct alignas(sizeof(T) * N) Pack { T v[N]; };
+
+// Four results of a row from dim d on; dims past head_dim are padding (head_dim is a multiple of 8).
+template <typename T>
+__device__ __forceinline__ void put4(T *y, const float *v, bool vec)
+{
+    if (vec) {
+        Pack<T, 4> p;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p.v[i] = Io<T>::put(v[i]);
+        *(Pack<T, 4> *)y = p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[i] = Io<T>::put(v[i]);
+    }
+}
+
+// 8 elements of a q row
+template <typename T>
+__device__ __forceinline__ Frag<T> q_frag(const T *q, bool vec)
+{
+    Frag<T> f;
+    if (vec) {
+        f = __builtin_bit_cast(Frag<T>, *(const Pack<T, 8> *)q);
+    } else {
+        Pack<T, 8> p;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            p.v[j] = q[j];
+        f = __builtin_bit_cast(Frag<T>, p);
+    }
+    return f;
+}
+
+__device__ __forceinline__ int row_token(const AttendBatch &b, const AttendTile &t, int r)
+{
+    const int at = t.token0 + r / b.group;
+    return t.shared ? b.listed[at] : at;
+}
+
+// Workgroups of one XCD take neighbouring runs: tiles of one prefix or request, and so the pages
+// they read, stay in one L2.
+__device__ __forceinline__ int worker_of_block() { return (blockIdx.x & 7) * (kAttendWorkers / 8) + (blockIdx.x >> 3); }
+
+__device__ __forceinline__ float fexp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ---------------------------------------------------------------------------
+// narrow tiles: 16 rows, four waves on 32 tokens each of a unit of 128
+
+// The contribution of values that are infinite or NaN, for blocks of which rows see different
+// tokens: a hidden token's weight is 0, and 0 times those is NaN.  Their places are taken out of
+// the product (v becomes 0 there), and each row gets what the tokens that it sees bring.
+template <typename T>
+__device__ __forceinline__ void odd_values(Frag<T> &v, const Frag<T> &sees, f32x4 &o)
+{
+    Frag<T> nan{}, up{}, down{};
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float x = (float)v.v[j];
+        const bool odd = !(__builtin_fabsf(x) < __builtin_inff());
+        any |= odd;
+        nan.v[j] = x != x ? 1.f : 0.f;
+        up.v[j] = x == __builtin_inff() ? 1.f : 0.f;
+        down.v[j] = x == -__builtin_inff() ? 1.f : 0.f;
+        if (odd)
+            v.v[j] = 0.f;
+    }
+    if (!__any(any))
+        return;
+    const f32x4 zero = {0, 0, 0, 0};
+    const f32x4 n = mma(nan, sees, zero), u = mma(up, sees, zero), d = mma(down, sees, zero);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (u[i] > 0)
+            o[i] += __builtin_inff();
+        if (d[i] > 0)
+            o[i] -= __builtin_inff();
+        if (n[i] > 0)
+            o[i] = __builtin_nanf("");
+    }
+}
+
+template <typename T, int KIND, int DP>
+__global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
+{
+    constexpr int NS = DP / 32, ND = DP / 16, W = DP + 4;
+    __shared__ float lds_o[4][kNarrowRows][W];
+    __shared__ float lds_m[4][kNarrowRows], lds_l[4][kNarrowRows];
+    const AttendBatch &b = a.b;
+    const AttendList list = b.plan->list[0];
+    const int w = worker_of_block();
+    const int64_t total = b.plan->bad ? 0 : (int64_t)list.units * b.kv_heads;
+    int64_t at = (int64_t)w * list.run;
+    const int64_t end = at + list.run < total ? at + list.run : total;
+    if (at >= end)
+        return;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+    const int heads = b.group * b.kv_heads, hd = a.c.head_dim;
+    const bool vec = (((uintptr_t)a.q | (uintptr_t)a.y) & 15) == 0;
+    int head = (int)(at / list.units), x = b.start[0][w];
+
+    for (; at < end; ++x) {
+        if (x == list.tiles) {
+            x = 0;
+            ++head;
+        }
+        const AttendTile t = b.tiles[0][x];
+        const int64_t base = (int64_t)head * list.units + t.unit0;
+        const int u0 = (int)(at - base);
+        const int u1 = (int)((end < base + t.units ? end : base + t.units) - base);
+
+        const int row = t.row0 + n;
+        const bool mine = n < t.rows;
+        Frag<T> q[NS];
+        {
+            const int r = mine ? row : t.row0;
+            const int token = row_token(b, t, r);
+            const T *p = (const T *)a.q + ((int64_t)token * heads + head * b.group + r % b.group) * hd;
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const int d = 32 * s + 8 * g;
+                q[s] = Frag<T>{};
+                if (mine && d < hd)
+                    q[s] = q_frag<T>(p + d, vec);
+            }
+        }
+        // tokens of the request's own pages that this lane's row sees, the fewest and the most of the tile
+        const int per = t.shared ? 0 : t.len - t.q_len + 1;
+        const int see = t.shared ? t.len : per + (mine ? row : t.row0 + t.rows - 1) / b.group;
+        const int see_min = t.shared ? t.len : per + t.row0 / b.group;
+        const int see_max = t.shared ? t.len : per + (t.row0 + t.rows - 1) / b.group;
+        const int pre_units = units_for(t.pre_len, kNarrowUnit);
+        const int32_t *own_pages = t.shared ? b.prefix_pages + (int64_t)t.seq * b.prefix_max_pages
+                                            : b.pages + (int64_t)t.seq * b.max_pages;
+        const int32_t *pre_pages = t.pre_len ? b.prefix_pages + (int64_t)t.pre_seq * b.prefix_max_pages : nullptr;
+
+        f32x4 o[ND];
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+            o[d] = f32x4{0, 0, 0, 0};
+        float m = kNone, l = 0;
+
+        for (int u = u0; u < u1; ++u) {
+            const bool in_pre = u < pre_units;
+            const int tok0 = (in_pre ? u : u - pre_units) * kNarrowUnit + wave * kBlock;
+            int most = in_pre ? t.pre_len : see_max, least = in_pre ? t.pre_len : see_min;
+            int here = (in_pre ? t.pre_len : see) - tok0;    // tokens of the block this row sees
+            if (tok0 >= most)
+                continue;
+            const int page = (in_pre ? pre_pages : own_pages)[tok0 >> a.c.page_shift];
+            const bool good = (uint32_t)page < (uint32_t)a.c.pages;
+            if (!good) {                                     // its tokens are seen by no row
+                if (!lane)
+                    atomicOr(b.flags, LORA_FLAG_CACHE_PAGE);
+                continue;
+            }
+            const char *blk = a.c.base + cache_block(a.c, page, head, (tok0 >> 5) & ((1 << (a.c.page_shift - 5)) - 1));
+            Held<T, KIND> kh[2][NS], vh[ND];
+            const int km = 8 * (n >> 2) + (n & 3);
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    kh[c][s] = held_load<T, KIND>(blk, (4 * s + g) * kBlock + km + 4 * c);
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                vh[d] = held_load<T, KIND>(blk + a.c.half, g * DP + 16 * d + n);
+            f32x4 ks[2], vs[2];
+            if constexpr (KIND != kCacheNative) {
+                const float *sc = (const float *)(blk + 2 * a.c.half);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    ks[c] = *(const f32x4 *)(sc + 8 * g + 4 * c);
+                    vs[c] = *(const f32x4 *)(sc + kBlock + 8 * g + 4 * c);
+                }
+            }
+            f32x4 st[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    st[c] = mma(frag_of(kh[c][s]), q[s], st[c]);
+            // scores in powers of two; token 8 g + 4 c + i of the block
+            float p[8];
+            float top = kNone;
+            const bool part = tok0 + kBlock > least;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float v = st[c][i] * a.scale;
+                    if constexpr (KIND != kCacheNative)
+                        v *= ks[c][i];
+                    if (part && 8 * g + 4 * c + i >= here)
+                        v = kNone;
+                    p[4 * c + i] = v;
+                    top = __builtin_fmaxf(top, v);
+                }
+            top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+            if (__any(top > m + kRaise)) {
+                const float up = __builtin_fmaxf(m, top);
+                const float f = up == kNone ? 1.f : fexp2(m - up);
+                m = up;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+                    o[d] *= f;
+            }
+            const float off = m == kNone ? 0.f : m;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                p[j] = fexp2(p[j] - off);
+                l += p[j];
+                if constexpr (KIND != kCacheNative)
+                    p[j] = part && 8 * g + j >= here ? 0.f : p[j] * vs[j >> 2][j & 3];
+            }
+            const Frag<T> pf = to_frag(p, T());
+            if (!part) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+                    o[d] = mma(frag_of(vh[d]), pf, o[d]);
+            } else {
+                // what no row sees may hold anything
+                const int keep = most - tok0 - 8 * g;
+                float sees[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    sees[j] = 8 * g + j < here ? 1.f : 0.f;
+                const Frag<T> sf = to_frag(sees, T());
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    Frag<T> v = frag_of(vh[d]);
+                    cut(v, keep);
+                    if constexpr (KIND == kCacheNative)
+                        if (least < most)
+                            odd_values<T>(v, sf, o[d]);
+                    o[d] = mma(v, pf, o[d]);
+                }
+            }
+        }
+
+        // join the waves
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (g == 0) {
+            lds_m[wave][n] = m;
+            lds_l[wave][n] = l;
+        }
+        __syncthreads();
+        {
+            const float top = __builtin_fmaxf(__builtin_fmaxf(lds_m[0][n], lds_m[1][n]),
+                                              __builtin_fmaxf(lds_m[2][n], lds_m[3][n]));
+            const float f = m == kNone ? (l != l ? l : 0.f) : fexp2(m - top);
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                *(f32x4 *)&lds_o[wave][n][16 * d + 4 * g] = o[d] * f;
+        }
+        __syncthreads();
+        const bool whole = t.kept < 0 && u0 == 0 && u1 == t.units;
+        const int64_t slot = part_slot(list, head, t, w);
+        for (int i = threadIdx.x; i < t.rows * (DP / 4); i += 256) {
+            const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+            float top = kNone, sum = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                top = __builtin_fmaxf(top, lds_m[k][r]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                sum += lds_m[k][r] == kNone ? lds_l[k][r] : lds_l[k][r] * fexp2(lds_m[k][r] - top);
+            f32x4 v = *(const f32x4 *)&lds_o[0][r][d];
+#pragma unroll
+            for (int k = 1; k < 4; ++k)
+                v += *(const f32x4 *)&lds_o[k][r][d];
+            if (whole) {
+                if (d < hd) {
+                    const int rr = t.row0 + r;
+                    const int sees = t.shared ? t.len : per + rr / b.group;
+                    const bool empty = sees <= 0 && !t.pre_len;
+                    float out[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        out[k] = empty ? 0.f : v[k] / sum;
+                    const int64_t token = row_token(b, t, rr);
+                    put4((T *)a.y + (token * heads + head * b.group + rr % b.group) * hd + d, out, vec);
+                }
+            } else {
+                *(f32x4 *)(a.parts[0] + (slot * kNarrowRows + r) * DP + d) = v;
+                if (d == 0) {
+                    a.sums[0][(slot * kNarrowRows + r) * 2] = top;
+                    a.sums[0][(slot * kNarrowRows + r) * 2 + 1] = sum;
+                }
+            }
+        }
+        __syncthreads();
+        at = base + u1;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// joining parts
+
+// One workgroup a tile and key-value head; a row's dims four to a lane.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
+{
+    const AttendBatch &b = a.b;
+    if (b.plan->bad)
+        return;
+    const int l = (int)blockIdx.x >= b.cap[0];
+    const int x = l ? blockIdx.x - b.cap[0] : blockIdx.x, head = blockIdx.y;
+    const AttendList list = b.plan->list[l];
+    if (x >= list.tiles)
+        return;
+    const AttendTile t = b.tiles[l][x];
+    const int w0 = first_worker(list, head, t), w1 = last_worker(list, head, t);
+    if (t.shared || (t.kept < 0 && w0 == w1))
+        return;
+    const int R = list_rows(l), hd = a.c.head_dim, heads = b.group * b.kv_heads;
+    const int L = t.prefix >= 0 ? b.prefix_list[t.prefix] : 0;
+    const AttendList shared = b.plan->list[L];
+    const bool vec = ((uintptr_t)a.y & 15) == 0;
+    for (int i = threadIdx.x; i < t.rows * (DP / 4); i += 256) {
+        const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+        float top = kNone, sum = 0;
+        f32x4 v = {0, 0, 0, 0};
+        auto add = [&](const float *parts, const float *sums, int64_t at) {
+            const float m = sums[at * 2], s = sums[at * 2 + 1];
+            const f32x4 o = *(const f32x4 *)(parts + at * DP + d);
+            const float up = __builtin_fmaxf(top, m);
+            const float f = top == kNone ? 1.f : fexp2(top - up), e = m == kNone ? 1.f : fexp2(m - up);
+            sum = sum * f + s * e;
+            v = v * f + o * e;
+            top = up;
+        };
+        for (int w = w0; w <= w1; ++w)
+            add(a.parts[l], a.sums[l], part_slot(list, head, t, w) * R + r);
+        if (t.prefix >= 0) {
+            const int pr = t.pre_row + r, PR = list_rows(L);
+            const AttendTile s = b.tiles[L][b.tiles_before[L][b.n_seqs + t.prefix] + pr / PR];
+            const int s0 = first_worker(shared, head, s), s1 = last_worker(shared, head, s);
+            for (int w = s0; w <= s1; ++w)
+                add(a.parts[L], a.sums[L], part_slot(shared, head, s, w) * PR + pr % PR);
+        }
+        if (d < hd) {
+            const int rr = t.row0 + r;
+            const bool empty = t.len - t.q_len + 1 + rr / b.group <= 0 && !t.pre_len && t.prefix < 0;
+            float out[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                out[k] = empty ? 0.f : v[k] / sum;
+            put4((T *)a.y + ((int64_t)(t.token0 + rr / b.group) * heads + head * b.group + rr % b.group) * hd + d,
+                 out, vec);
+        }
+    }
+}
+
+template <typename T, int KIND>
+hipError_t launch_narrow(const AttendArgs &a, hipStream_t st)
+{
+    switch (a.c.dp) {
+    case 64: attend_narrow_kernel<T, KIND, 64><<<kAttendWorkers, 256, 0, st>>>(a); break;
+    case 96: attend_narrow_kernel<T, KIND, 96><<<kAttendWorkers, 256, 0, st>>>(a); break;
+    case 128: attend_narrow_kernel<T, KIND, 128><<<kAttendWorkers, 256, 0, st>>>(a); break;
+    default: attend_narrow_kernel<T, KIND, 256><<<kAttendWorkers, 256, 0, st>>>(a); break;
+    }
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_all(const AttendArgs &a, hipStream_t st)
+{
+    hipError_t e = a.c.kind == kCacheNative ? launch_narrow<T, kCacheNative>(a, st)
+                 : a.c.kind == kCacheFp8 ? launch_narrow<T, kCacheFp8>(a, st)
+                                         : launch_narrow<T, kCacheInt8>(a, st);
+    if (e != hipSuccess)
+        return e;
+    const dim3 grid(a.b.cap[0] + a.b.cap[1], a.b.kv_heads);
+    switch (a.c.dp) {
+    case 64: attend_join_kernel<T, 64><<<grid, 256, 0, st>>>(a); break;
+    case 96: attend_join_kernel<T, 96><<<grid, 256, 0, st>>>(a); break;
+    case 128: attend_join_kernel<T, 128><<<grid, 256, 0, st>>>(a); break;
+    default: attend_join_kernel<T, 256><<<grid, 256, 0, st>>>(a); break;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attend_plan(const AttendBatch &b, hipStream_t st)
+{
+    attend_plan_kernel<<<1, kPlanThreads, 0, st>>>(b);
+    return hipGetLastError();
+}
+
+hipError_t launch_attend(bool bf16, const AttendArgs &a, hipStream_t st)
+{
+    return bf16 ? launch_all<uint16_t>(a, st) : launch_all<float>(a, st);
+}
+
+}  // namespace lora

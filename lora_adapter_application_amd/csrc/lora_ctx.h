@@ -5,10 +5,12 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <memory>
 #include <string>
 #include <vector>
 
 #include "../../include/lora_mi355x.h"
+#include "lora_attend.h"
 #include "lora_internal.h"
 #include "lora_layer.h"
 
@@ -68,7 +70,23 @@ struct BatchState {
     const void *last_x[kMaxGroup] = {};   // inputs of the last shrink (saved modules read them)
 };
 
+// The prepared batch of lora_attend and the workspace that its plan and parts are cut from.
+struct AttendState {
+    bool prepared = false;
+    AttendBatch batch{};
+    int head_dim = 0;
+    unsigned long long capture = 0;      // the capture its plan was prepared in, or 0
+    char *base = nullptr;
+    size_t bytes = 0;
+    float *parts[2] = {}, *sums[2] = {};
+};
+
 }  // namespace lora
+
+// A paged cache; its memory is one of the ctx's allocations.
+struct lora_cache {
+    lora::CacheView view{};
+};
 
 struct lora_ctx {
     int device = 0;
@@ -123,6 +141,8 @@ struct lora_ctx {
     std::vector<lora::BasePack> base;        // per module its 4-bit base weight (lora_base_load)
     hipEvent_t base_done = nullptr;          // the last base load; slot loads have load_done
     uint64_t base_gen = 0, base_synced = 0;  // base loads, and those the host has seen complete
+    std::vector<std::unique_ptr<lora_cache>> caches;
+    lora::AttendState attend;
     std::vector<void *> allocations;
     uint32_t flags_host = 0;                 // lora_get_device_flags' copy of the sticky word
 };

@@ -1,0 +1,203 @@
+// lora_norm.hip -- gfx950 kernel of head norms with rotary positions.
+//
+//     z = x / sqrt(sum x^2 / head_dim + eps) * weight, its pairs turned as lora_rotary.hip turns them
+//
+// with the sum, the norm and the turn in fp32 and one rounding at the end.  A workgroup owns one
+// token and a share of its heads.  A head is cut in items, a pair of 16-byte pieces that turn
+// against each other, a piece of neighbouring pairs, or a piece behind rotary_dim; the items go
+// to a power of two of neighbouring lanes, which keep them in registers while their sums of
+// squares meet in log2 shuffles.  One read and one write of x: bytes bound it, and for few tokens
+// the chain position, sine and cosine, barrier, load, shuffles, store.
+#include <hip/hip_runtime.h>
+
+#include "lora_attend.h"
+
+namespace lora {
+namespace {
+
+constexpr int kPairs = LORA_ROTARY_MAX_DIM / 2;
+
+template <typename T> struct Elem;
+template <> struct Elem<uint16_t> {
+    static __device__ __forceinline__ float get(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+    static __device__ __forceinline__ uint16_t put(float f)
+    {
+        __bf16 h = (__bf16)f;
+        return __builtin_bit_cast(uint16_t, h);
+    }
+};
+template <> struct Elem<float> {
+    static __device__ __forceinline__ float get(float v) { return v; }
+    static __device__ __forceinline__ float put(float f) { return f; }
+};
+
+template <typename T, int V> struct alignas(sizeof(T) * V) Pack { T v[V]; };
+
+// V elements a piece (16 bytes, or 1); NI items a lane.
+template <typename T, bool HALF, int V, int NI>
+__global__ __launch_bounds__(256) void norm_rotary_kernel(NormArgs a, int lanes)
+{
+    typedef Pack<T, V> P;
+    __shared__ float2 cs[kPairs];
+    const RotaryArgs &ro = a.rot;
+    const int t = blockIdx.x;
+    const int rd = ro.rot.rotary_dim, pairs = rd >> 1, hd = ro.rot.head_dim;
+    const double pos = (double)ro.positions[t];
+    for (int p = threadIdx.x; p < pairs; p += 256) {
+        const double turns = pos * ro.rot.turns[p];
+        const double frac = turns - rint(turns);
+        float c, s;
+        if constexpr (sizeof(T) == 4) {
+            double sd, cd;
+            sincospi(2.0 * frac, &sd, &cd);
+            c = (float)(cd * ro.rot.amplitude);
+            s = (float)(sd * ro.rot.amplitude);
+        } else {
+            sincospif(2.f * (float)frac, &s, &c);
+            c *= ro.rot.amplitude;
+            s *= ro.rot.amplitude;
+        }
+        cs[p] = make_float2(c, s);
+    }
+    __syncthreads();
+
+    // Items of a head: `turning` of them hold N pairs each, in one or two pieces, the rest one piece.
+    constexpr bool TWO = HALF || V == 1;                 // a turning item has two pieces
+    constexpr int N = V == 1 ? 1 : HALF ? V : V / 2;
+    const int turning = pairs / N, items = turning + (hd - rd) / V;
+    const int per_pass = 256 / lanes, lane = threadIdx.x & (lanes - 1), first = threadIdx.x / lanes;
+    int at0[NI], at1[NI];                                // first elements of an item's pieces
+    bool turn[NI], used[NI];
+    float2 w[NI][N];
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+        const int item = lane + k * lanes;
+        used[k] = item < items;
+        turn[k] = item < turning;
+        at0[k] = !turn[k] ? rd + (item - turning) * V : HALF ? item * N : 2 * item * N;
+        at1[k] = HALF ? pairs + item * N : 2 * item + 1;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            w[k][i] = turn[k] ? cs[item * N + i] : make_float2(1.f, 0.f);
+    }
+    int mi = 0, base = 0;
+    for (int h0 = blockIdx.y * per_pass; h0 < ro.total_heads; h0 += gridDim.y * per_pass) {
+        const int h = h0 + first;
+        const bool live = h < ro.total_heads;            // all lanes take part in the shuffles
+        while (live && h - base >= ro.m[mi].heads)
+            base += ro.m[mi++].heads;
+        const int64_t at = live ? (int64_t)t * ro.m[mi].width + (int64_t)(h - base) * hd : 0;
+        const T *x = (const T *)ro.m[mi].x + at;
+        T *y = (T *)ro.m[mi].y + at;
+        const T *g = (const T *)a.weight[mi];
+        P u[NI], v[NI], gu[NI], gv[NI];
+        float sum = 0;
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            if (!live || !used[k])
+                continue;
+            u[k] = *(const P *)(x + at0[k]);
+            if (TWO && turn[k])
+                v[k] = *(const P *)(x + at1[k]);
+            if (g) {
+                gu[k] = *(const P *)(g + at0[k]);
+                if (TWO && turn[k])
+                    gv[k] = *(const P *)(g + at1[k]);
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float e = Elem<T>::get(u[k].v[i]);
+                sum = fmaf(e, e, sum);
+            }
+            if (TWO && turn[k])
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float e = Elem<T>::get(v[k].v[i]);
+                    sum = fmaf(e, e, sum);
+                }
+        }
+        for (int d = 1; d < lanes; d <<= 1)
+            sum += __shfl_xor(sum, d);
+        const float r = 1.f / sqrtf(sum / (float)hd + a.eps);
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            if (!live || !used[k])
+                continue;
+            float p[V], q[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                p[i] = Elem<T>::get(u[k].v[i]) * r * (g ? Elem<T>::get(gu[k].v[i]) : 1.f);
+                if (TWO && turn[k])
+                    q[i] = Elem<T>::get(v[k].v[i]) * r * (g ? Elem<T>::get(gv[k].v[i]) : 1.f);
+            }
+            P out0, out1;
+            if (!turn[k]) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    out0.v[i] = Elem<T>::put(p[i]);
+            } else if constexpr (TWO) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    out0.v[i] = Elem<T>::put(fmaf(-q[i], w[k][i].y, p[i] * w[k][i].x));
+                    out1.v[i] = Elem<T>::put(fmaf(p[i], w[k][i].y, q[i] * w[k][i].x));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    out0.v[2 * i] = Elem<T>::put(fmaf(-p[2 * i + 1], w[k][i].y, p[2 * i] * w[k][i].x));
+                    out0.v[2 * i + 1] = Elem<T>::put(fmaf(p[2 * i], w[k][i].y, p[2 * i + 1] * w[k][i].x));
+                }
+            }
+            *(P *)(y + at0[k]) = out0;
+            if (TWO && turn[k])
+                *(P *)(y + at1[k]) = out1;
+        }
+    }
+}
+
+template <typename T, bool HALF, int V, int NI>
+void launch_items(const NormArgs &a, int lanes, dim3 grid, hipStream_t st)
+{
+    norm_rotary_kernel<T, HALF, V, NI><<<grid, 256, 0, st>>>(a, lanes);
+}
+
+template <typename T, int V>
+hipError_t launch(const NormArgs &a, hipStream_t st)
+{
+    const lora_rotary &rot = a.rot.rot;
+    const bool half = rot.layout == LORA_ROTARY_HALF;
+    const int pairs = rot.rotary_dim / 2, N = V == 1 ? 1 : half ? V : V / 2;
+    const int items = pairs / N + (rot.head_dim - rot.rotary_dim) / V;
+    int lanes = 1;
+    while (lanes < items && lanes < 64)
+        lanes *= 2;
+    const int each = (items + lanes - 1) / lanes;        // at most 8: head_dim is at most 512
+    const int passes = (a.rot.total_heads + 256 / lanes - 1) / (256 / lanes);
+    // enough workgroups for the chip when tokens are few
+    const int split = a.rot.T >= 2048 ? 1 : passes < 2048 / a.rot.T ? passes : 2048 / a.rot.T;
+    const dim3 grid(a.rot.T, split < 1 ? 1 : split);
+#define LORA_NORM(NI) half ? launch_items<T, true, V, NI>(a, lanes, grid, st) : launch_items<T, false, V, NI>(a, lanes, grid, st)
+    if (each == 1)
+        LORA_NORM(1);
+    else if (each == 2)
+        LORA_NORM(2);
+    else if constexpr (V == 1) {
+        if (each <= 4)
+            LORA_NORM(4);
+        else
+            LORA_NORM(8);
+    }
+#undef LORA_NORM
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm_rotary(bool bf16, bool vec, const NormArgs &a, hipStream_t st)
+{
+    if (bf16)
+        return vec ? launch<uint16_t, 8>(a, st) : launch<uint16_t, 1>(a, st);
+    return vec ? launch<float, 4>(a, st) : launch<float, 1>(a, st);
+}
+
+}  // namespace lora
