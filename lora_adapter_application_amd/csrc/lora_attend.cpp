@@ -383,7 +383,7 @@ int do_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads, c
     b.group = q_heads / v.kv_heads;
     b.kv_heads = v.kv_heads;
     b.page_shift = v.page_shift;
-    b.wide = 0;
+    b.wide = ctx->dtype == LORA_BF16;
     b.flags = ctx->ws.plan.flags;
     if (b.n_tokens && b.n_seqs) {
         int64_t cap[2], kept[2];

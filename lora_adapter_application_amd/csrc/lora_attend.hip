@@ -13,11 +13,13 @@
 #include <hip/hip_runtime.h>
 
 #include "lora_attend.h"
+#include "lora_dma.h"
 
 namespace lora {
 namespace {
 
 typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 
 constexpr float kRaise = 8.f;        // a maximum is raised when a score passes it by 2^8
@@ -228,6 +230,10 @@ __device__ __forceinline__ f32x4 mma(const Frag<uint16_t> &a, const Frag<uint16_
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
 }
+__device__ __forceinline__ f32x16 mma(const Frag<uint16_t> &a, const Frag<uint16_t> &b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.v, b.v, c, 0, 0, 0);
+}
 __device__ __forceinline__ f32x4 mma(const Frag<float> &a, const Frag<float> &b, f32x4 c)
 {
 #pragma unroll
@@ -374,6 +380,19 @@ __device__ __forceinline__ int row_token(const AttendBatch &b, const AttendTile 
     return t.shared ? b.listed[at] : at;
 }
 
+// Plan words that a whole workgroup works by, in scalar registers.
+template <typename P>
+__device__ __forceinline__ P scalar(const P *p)
+{
+    P r;
+    const int32_t *from = (const int32_t *)p;
+    int32_t *to = (int32_t *)&r;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(P) / 4); ++i)
+        to[i] = __builtin_amdgcn_readfirstlane(from[i]);
+    return r;
+}
+
 // Workgroups of one XCD take neighbouring runs: tiles of one prefix or request, and so the pages
 // they read, stay in one L2.
 __device__ __forceinline__ int worker_of_block() { return (blockIdx.x & 7) * (kAttendWorkers / 8) + (blockIdx.x >> 3); }
@@ -386,35 +405,34 @@ __device__ __forceinline__ float fexp2(float x) { return __builtin_amdgcn_exp2f(
 // The contribution of values that are infinite or NaN, for blocks of which rows see different
 // tokens: a hidden token's weight is 0, and 0 times those is NaN.  Their places are taken out of
 // the product (v becomes 0 there), and each row gets what the tokens that it sees bring.
-template <typename T>
-__device__ __forceinline__ void odd_values(Frag<T> &v, const Frag<T> &sees, f32x4 &o)
+template <typename T, typename Acc>
+__device__ __forceinline__ void odd_values(Frag<T> &v, const Frag<T> &sees, Acc &o)
 {
-    Frag<T> nan{}, up{}, down{};
     bool any = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float x = (float)v.v[j];
-        const bool odd = !(__builtin_fabsf(x) < __builtin_inff());
-        any |= odd;
-        nan.v[j] = x != x ? 1.f : 0.f;
-        up.v[j] = x == __builtin_inff() ? 1.f : 0.f;
-        down.v[j] = x == -__builtin_inff() ? 1.f : 0.f;
-        if (odd)
-            v.v[j] = 0.f;
-    }
+    for (int j = 0; j < 8; ++j)
+        any |= !(__builtin_fabsf((float)v.v[j]) < __builtin_inff());
     if (!__any(any))
         return;
-    const f32x4 zero = {0, 0, 0, 0};
-    const f32x4 n = mma(nan, sees, zero), u = mma(up, sees, zero), d = mma(down, sees, zero);
+    const float bring[3] = {__builtin_inff(), -__builtin_inff(), __builtin_nanf("")};
+#pragma unroll 1
+    for (int k = 0; k < 3; ++k) {
+        Frag<T> where{};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (u[i] > 0)
-            o[i] += __builtin_inff();
-        if (d[i] > 0)
-            o[i] -= __builtin_inff();
-        if (n[i] > 0)
-            o[i] = __builtin_nanf("");
+        for (int j = 0; j < 8; ++j) {
+            const float x = (float)v.v[j];
+            where.v[j] = (k == 2 ? x != x : x == bring[k]) ? 1.f : 0.f;
+        }
+        const Acc seen = mma(where, sees, Acc{});
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(Acc) / 4); ++i)
+            if (seen[i] > 0)
+                o[i] += bring[k];
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (!(__builtin_fabsf((float)v.v[j]) < __builtin_inff()))
+            v.v[j] = 0.f;
 }
 
 template <typename T, int KIND, int DP>
@@ -424,9 +442,9 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
     __shared__ float lds_o[4][kNarrowRows][W];
     __shared__ float lds_m[4][kNarrowRows], lds_l[4][kNarrowRows];
     const AttendBatch &b = a.b;
-    const AttendList list = b.plan->list[0];
+    const AttendList list = scalar(&b.plan->list[0]);
     const int w = worker_of_block();
-    const int64_t total = b.plan->bad ? 0 : (int64_t)list.units * b.kv_heads;
+    const int64_t total = scalar(&b.plan->bad) ? 0 : (int64_t)list.units * b.kv_heads;
     int64_t at = (int64_t)w * list.run;
     const int64_t end = at + list.run < total ? at + list.run : total;
     if (at >= end)
@@ -434,14 +452,14 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
     const int heads = b.group * b.kv_heads, hd = a.c.head_dim;
     const bool vec = (((uintptr_t)a.q | (uintptr_t)a.y) & 15) == 0;
-    int head = (int)(at / list.units), x = b.start[0][w];
+    int head = __builtin_amdgcn_readfirstlane((int)(at / list.units)), x = scalar(b.start[0] + w);
 
     for (; at < end; ++x) {
         if (x == list.tiles) {
             x = 0;
             ++head;
         }
-        const AttendTile t = b.tiles[0][x];
+        const AttendTile t = scalar(b.tiles[0] + x);
         const int64_t base = (int64_t)head * list.units + t.unit0;
         const int u0 = (int)(at - base);
         const int u1 = (int)((end < base + t.units ? end : base + t.units) - base);
@@ -635,6 +653,328 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
 }
 
 // ---------------------------------------------------------------------------
+// wide tiles: 128 rows, four waves on 32 rows each of a unit of 64 tokens
+
+// A unit's keys and values stand in LDS in the order of the cache, as bf16, twice: the waves read
+// one while the other is filled.  Token and dim operands are 32 lanes of 16 neighbouring bytes,
+// free of bank conflicts.
+template <int KIND, int DP>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(AttendArgs a)
+{
+    typedef uint16_t T;
+    typedef Frag<T> F;
+    constexpr int NS = DP / 16, ND = DP / 32;
+    constexpr int kSide = kBlock * DP * 2;                   // bytes of a block's keys, and of its values
+    constexpr int kBuf = 4 * kSide;                          // keys of two blocks, values of two blocks
+    constexpr bool CODED = KIND != kCacheNative;
+    __shared__ alignas(16) char lds[2 * kBuf];
+    __shared__ float scales[2][CODED ? 4 * kBlock : 1];      // of two blocks' keys, of their values
+    const AttendBatch &b = a.b;
+    const AttendList list = scalar(&b.plan->list[1]);
+    const int w = worker_of_block();
+    const int64_t total = scalar(&b.plan->bad) ? 0 : (int64_t)list.units * b.kv_heads;
+    int64_t at = (int64_t)w * list.run;
+    const int64_t end = at + list.run < total ? at + list.run : total;
+    if (at >= end)
+        return;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = tid & 63, h = lane >> 5, n = lane & 31;
+    const int heads = b.group * b.kv_heads, hd = a.c.head_dim;
+    const int in_page = (1 << (a.c.page_shift - 5)) - 1;
+    const bool vec = (((uintptr_t)a.q | (uintptr_t)a.y) & 15) == 0;
+    // row r of a result holds token 16 (r / 16) + 8 h + 0..7 in its registers when the rows of
+    // the operand take the tokens with bits 2 and 3 of their number exchanged
+    const int ktok = (n & 19) | (n & 4) << 1 | (n & 8) >> 1;
+    int head = __builtin_amdgcn_readfirstlane((int)(at / list.units)), x = scalar(b.start[1] + w);
+
+    for (; at < end; ++x) {
+        if (x == list.tiles) {
+            x = 0;
+            ++head;
+        }
+        const AttendTile t = scalar(b.tiles[1] + x);
+        const int64_t base = (int64_t)head * list.units + t.unit0;
+        const int u0 = (int)(at - base);
+        const int u1 = (int)((end < base + t.units ? end : base + t.units) - base);
+
+        const int wr = wave * 32;                            // the wave's first row of the tile
+        const bool works = wr < t.rows;
+        const int wl = t.rows < wr + 32 ? t.rows - 1 : wr + 31;   // its last
+        const bool mine = wr + n < t.rows;
+        const int row = t.row0 + (mine ? wr + n : works ? wl : 0);
+        F q[NS];
+        {
+            const int token = row_token(b, t, row);
+            const T *p = (const T *)a.q + ((int64_t)token * heads + head * b.group + row % b.group) * hd;
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const int d = 16 * s + 8 * h;
+                q[s] = F{};
+                if (mine && d < hd)
+                    q[s] = q_frag<T>(p + d, vec);
+            }
+        }
+        // own tokens that this lane's row sees, the fewest and the most of the wave, the most of the tile
+        const int per = t.shared ? 0 : t.len - t.q_len + 1;
+        const int see = t.shared ? t.len : per + row / b.group;
+        const int see_min = t.shared ? t.len : per + (t.row0 + wr) / b.group;
+        const int see_max = t.shared ? t.len : per + (t.row0 + wl) / b.group;
+        const int see_all = t.shared ? t.len : per + (t.row0 + t.rows - 1) / b.group;
+        const int pre_units = units_for(t.pre_len, kWideUnit);
+        const int32_t *own_pages = t.shared ? b.prefix_pages + (int64_t)t.seq * b.prefix_max_pages
+                                            : b.pages + (int64_t)t.seq * b.max_pages;
+        const int32_t *pre_pages = t.pre_len ? b.prefix_pages + (int64_t)t.pre_seq * b.prefix_max_pages : nullptr;
+
+        // A unit's two blocks: their pages, and which of them are there.
+        auto pages_of = [&](int u, int (&page)[2]) {
+            const bool in_pre = u < pre_units;
+            const int tok0 = (in_pre ? u : u - pre_units) * kWideUnit, most = in_pre ? t.pre_len : see_all;
+            const int32_t *pages = in_pre ? pre_pages : own_pages;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                page[j] = -1;
+                if (u < u1 && tok0 + j * kBlock < most) {
+                    const int v = __builtin_amdgcn_readfirstlane(pages[(tok0 + j * kBlock) >> a.c.page_shift]);
+                    if ((uint32_t)v < (uint32_t)a.c.pages)
+                        page[j] = v;
+                    else if (!tid)
+                        atomicOr(b.flags, LORA_FLAG_CACHE_PAGE);
+                }
+            }
+        };
+        auto block_of = [&](int u, int j, int page) -> const char * {
+            const int tok0 = (u < pre_units ? u : u - pre_units) * kWideUnit + j * kBlock;
+            const uint64_t p = (uint64_t)(a.c.base + cache_block(a.c, page, head, (tok0 >> 5) & in_page));
+            const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+            return (const char *)((uint64_t)hi << 32 | lo);
+        };
+        constexpr int NC = CODED ? (kBlock * DP / 16 + 255) / 256 : 1;   // 16-byte pieces a thread takes of a side
+        uint4 held[2][2][NC];
+        float held_scale;
+        // native: straight into LDS; codes: into registers, and from there as bf16
+        auto fetch = [&](int u, int buf, const int (&page)[2]) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (page[j] < 0)
+                    continue;
+                const char *blk = block_of(u, j, page[j]);
+                if constexpr (!CODED) {
+                    const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds +
+                                        buf * kBuf + j * kSide;
+#pragma unroll
+                    for (int i = wave; i < 2 * kSide / 1024; i += 4) {
+                        const int side = i >= kSide / 1024, k = i - side * (kSide / 1024);
+                        dma16_off(blk, (uint32_t)(i * 1024 + lane * 16), to + side * 2 * kSide + k * 1024);
+                    }
+                } else {
+#pragma unroll
+                    for (int side = 0; side < 2; ++side)
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+                            if (tid + 256 * c < kBlock * DP / 16)
+                                held[j][side][c] = *(const uint4 *)(blk + side * kBlock * DP + (tid + 256 * c) * 16);
+                }
+            }
+            if constexpr (CODED)                             // a wave each: of a block's keys, of its values
+                if (lane < kBlock && page[wave & 1] >= 0)
+                    held_scale = ((const float *)(block_of(u, wave & 1, page[wave & 1]) + 2 * kBlock * DP))
+                        [(wave >> 1) * kBlock + lane];
+        };
+        auto settle = [&](int buf, const int (&page)[2]) {
+            if constexpr (CODED) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (page[j] < 0)
+                        continue;
+#pragma unroll
+                    for (int side = 0; side < 2; ++side)
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {
+                            if (tid + 256 * c >= kBlock * DP / 16)
+                                continue;
+                            const uint4 r = held[j][side][c];
+                            char *to = lds + buf * kBuf + (2 * side + j) * kSide + (tid + 256 * c) * 32;
+                            const Held<T, KIND> lo{make_uint2(r.x, r.y)}, hi{make_uint2(r.z, r.w)};
+                            *(bf16x8 *)to = frag_of(lo).v;
+                            *(bf16x8 *)(to + 16) = frag_of(hi).v;
+                        }
+                }
+                if (lane < kBlock)
+                    scales[buf][wave * kBlock + lane] = held_scale;
+            }
+        };
+
+        f32x16 o[ND];
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+            o[d] = f32x16{};
+        float m = kNone, l = 0;
+        int page[2], next[2], after[2];
+        pages_of(u0, page);
+        fetch(u0, 0, page);
+        settle(0, page);
+        pages_of(u0 + 1, next);
+        int buf = 0;
+        for (int u = u0; u < u1; ++u, buf ^= 1) {
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            fetch(u + 1, buf ^ 1, next);
+            pages_of(u + 2, after);
+            const bool in_pre = u < pre_units;
+            const int tok0 = (in_pre ? u : u - pre_units) * kWideUnit;
+            const int most = in_pre ? t.pre_len : see_max, least = in_pre ? t.pre_len : see_min;
+            const int here = (in_pre ? t.pre_len : see) - tok0;          // tokens of the unit this row sees
+            if (works && tok0 < most) {
+                const char *kb = lds + buf * kBuf, *vb = kb + 2 * kSide;
+                f32x16 st[2] = {};
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const F k{*(const bf16x8 *)(kb + j * kSide + ((2 * s + h) * kBlock + ktok) * 16)};
+                        st[j] = mma(k, q[s], st[j]);
+                    }
+                const bool part = tok0 + kWideUnit > least || page[0] < 0 || page[1] < 0;
+                float top = kNone;
+                if constexpr (CODED) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int r = 0; r < 16; r += 4) {
+                            const f32x4 ks = *(const f32x4 *)&scales[buf][j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7)];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                st[j][r + i] *= ks[i];
+                        }
+                }
+                if (part) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (page[j] < 0 || j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7) >= here)
+                                st[j][r] = kNone;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        top = __builtin_fmaxf(top, st[j][r]);
+                top = __builtin_fmaxf(top, __shfl_xor(top, 32)) * a.scale;
+                if (__any(top > m + kRaise)) {
+                    const float up = __builtin_fmaxf(m, top);
+                    const float f = up == kNone ? 1.f : fexp2(m - up);
+                    m = up;
+                    l *= f;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+                        o[d] *= f;
+                }
+                const float off = m == kNone ? 0.f : -m;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        st[j][r] = fexp2(fmaf(st[j][r], a.scale, off));
+                        l += st[j][r];
+                    }
+                if constexpr (CODED) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int r = 0; r < 16; r += 4) {
+                            const f32x4 vs = *(const f32x4 *)&scales[buf][(2 + j) * kBlock + 16 * (r >> 3) + 8 * h + (r & 7)];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (part && (page[j] < 0 || j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7) + i >= here))
+                                    st[j][r + i] = 0.f;
+                                else
+                                    st[j][r + i] *= vs[i];
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float p[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            p[i] = st[j][8 * c + i];
+                        const F pf = to_frag(p, T());
+                        if (!part) {
+#pragma unroll
+                            for (int d = 0; d < ND; ++d) {
+                                const F v{*(const bf16x8 *)(vb + j * kSide + ((2 * c + h) * DP + 32 * d + n) * 16)};
+                                o[d] = mma(v, pf, o[d]);
+                            }
+                        } else {
+                            // what no row sees may hold anything
+                            const int first = j * kBlock + 16 * c + 8 * h;
+                            const int keep = page[j] < 0 ? 0 : most - tok0 - first;
+                            float sees[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                sees[i] = first + i < here ? 1.f : 0.f;
+                            const F sf = to_frag(sees, T());
+#pragma unroll
+                            for (int d = 0; d < ND; ++d) {
+                                F v{*(const bf16x8 *)(vb + j * kSide + ((2 * c + h) * DP + 32 * d + n) * 16)};
+                                cut(v, keep);
+                                if constexpr (!CODED)
+                                    if (least < most)
+                                        odd_values<T>(v, sf, o[d]);
+                                o[d] = mma(v, pf, o[d]);
+                            }
+                        }
+                    }
+            }
+            settle(buf ^ 1, next);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                page[j] = next[j];
+                next[j] = after[j];
+            }
+        }
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+        l += __shfl_xor(l, 32);
+        const bool whole = t.kept < 0 && u0 == 0 && u1 == t.units;
+        if (mine) {
+            if (whole) {
+                const bool empty = see <= 0 && !t.pre_len;
+                const float by = empty ? 0.f : 1.f / l;
+                const int64_t token = row_token(b, t, row);
+                T *y = (T *)a.y + (token * heads + head * b.group + row % b.group) * hd;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; r += 4) {
+                        const int dim = 32 * d + 2 * r + 4 * h;
+                        float out[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            out[i] = empty ? 0.f : o[d][r + i] * by;
+                        if (dim < hd)
+                            put4(y + dim, out, vec);
+                    }
+            } else {
+                const int64_t slot = part_slot(list, head, t, w) * kWideRows + wr + n;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; r += 4)
+                        *(f32x4 *)(a.parts[1] + slot * DP + 32 * d + 2 * r + 4 * h) =
+                            f32x4{o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]};
+                if (!h) {
+                    a.sums[1][slot * 2] = m;
+                    a.sums[1][slot * 2 + 1] = l;
+                }
+            }
+        }
+        at = base + u1;
+    }
+}
+
+// ---------------------------------------------------------------------------
 // joining parts
 
 // One workgroup a tile and key-value head; a row's dims four to a lane.
@@ -704,10 +1044,29 @@ hipError_t launch_narrow(const AttendArgs &a, hipStream_t st)
     return hipGetLastError();
 }
 
+template <int KIND>
+hipError_t launch_wide(const AttendArgs &a, hipStream_t st)
+{
+    switch (a.c.dp) {
+    case 64: attend_wide_kernel<KIND, 64><<<kAttendWorkers, 256, 0, st>>>(a); break;
+    case 96: attend_wide_kernel<KIND, 96><<<kAttendWorkers, 256, 0, st>>>(a); break;
+    case 128: attend_wide_kernel<KIND, 128><<<kAttendWorkers, 256, 0, st>>>(a); break;
+    default: attend_wide_kernel<KIND, 256><<<kAttendWorkers, 256, 0, st>>>(a); break;
+    }
+    return hipGetLastError();
+}
+
 template <typename T>
 hipError_t launch_all(const AttendArgs &a, hipStream_t st)
 {
-    hipError_t e = a.c.kind == kCacheNative ? launch_narrow<T, kCacheNative>(a, st)
+    hipError_t e = hipSuccess;
+    if (a.b.cap[1])
+        e = a.c.kind == kCacheNative ? launch_wide<kCacheNative>(a, st)
+          : a.c.kind == kCacheFp8 ? launch_wide<kCacheFp8>(a, st)
+                                  : launch_wide<kCacheInt8>(a, st);
+    if (e != hipSuccess)
+        return e;
+    e = a.c.kind == kCacheNative ? launch_narrow<T, kCacheNative>(a, st)
                  : a.c.kind == kCacheFp8 ? launch_narrow<T, kCacheFp8>(a, st)
                                          : launch_narrow<T, kCacheInt8>(a, st);
     if (e != hipSuccess)

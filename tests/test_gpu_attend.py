@@ -78,6 +78,13 @@ CASES = [
     ("bf16", "fp8", 16, 2, 128, 64, [1] * 40, list(range(1, 41)), [(0, 17, 1000), (17, 18, 65), (18, 39, 64)]),
     ("bf16", "int8", 16, 2, 64, 64, [1, 2, 3] * 20, [50] * 60, [(0, 50, 513)]),
     ("bf16", "native", 10, 2, 80, 32, [2, 90, 1, 6, 7] * 4, [101] * 20, [(0, 3, 150), (3, 20, 33)]),
+    # tiles of many rows in 8 bits and of every width, parts of long ones
+    ("bf16", "fp8", 8, 1, 256, 64, [100, 3], [200, 30], [(0, 2, 100)]),
+    ("bf16", "int8", 8, 1, 96, 32, [100, 3], [200, 30], [(0, 2, 100)]),
+    ("bf16", "fp8", 16, 2, 64, 128, [100, 3, 33], [100, 30, 40], [(0, 2, 100)]),
+    ("bf16", "native", 8, 1, 256, 32, [100, 3], [200, 30], [(0, 2, 100)]),
+    ("bf16", "native", 8, 1, 128, 64, [700], [1500], [(0, 1, 900)]),
+    ("bf16", "int8", 8, 1, 128, 32, [200], [1500], [(0, 1, 900)]),
     # more work than workers
     ("bf16", "native", 32, 32, 64, 32, [1] * 70, [5 * i + 1 for i in range(70)], [(10, 60, 200)]),
 ]
