@@ -310,17 +310,14 @@ struct Cut {
 size_t cut_workspace(char *base, AttendBatch &b, AttendState &st, int dp)
 {
     Cut c{base};
-    const int64_t entities = (int64_t)b.n_seqs + b.n_prefixes + 1;
     c.take(b.plan, 1);
     for (int l = 0; l < 2; ++l) {
         c.take(b.tiles[l], b.cap[l]);
         c.take(b.start[l], kAttendWorkers);
-        c.take(b.tiles_before[l], entities);
-        c.take(b.kept_before[l], entities);
     }
     c.take(b.list_before, (int64_t)b.n_seqs + 1);
     c.take(b.listed, b.n_tokens);
-    c.take(b.prefix_list, b.n_prefixes);
+    c.take(b.prefix_tile, b.n_prefixes);
     for (int l = 0; l < 2; ++l) {
         const int64_t rows = b.cap[l] ? part_slots(b.kept_cap[l], b.kv_heads) * list_rows(l) : 0;
         c.take(st.sums[l], rows * 2);

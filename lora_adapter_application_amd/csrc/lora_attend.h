@@ -96,7 +96,7 @@ struct AttendTile {
     int32_t unit0, units;        // units before the tile, and its own, of one key-value head
     int32_t kept;                // its number among the tiles whose parts are always kept, or -1
     int32_t prefix;              // prefix whose shared tiles hold the other part, or -1
-    int32_t pre_row;             // the row of that prefix's list at which this tile starts
+    int32_t pre_row;             // the row of the list of all such tokens at which this tile starts
     int32_t pre_seq;             // prefix read by itself (pre_len > 0)
     int32_t pad[2];
 };
@@ -112,6 +112,9 @@ struct AttendPlan {
     int32_t bad;                 // the batch does not fit what the host was told: no work
     int32_t pad[7];
 };
+
+// A prefix's first shared tile.
+struct PrefixTile { int32_t list, tile; };
 
 struct AttendBatch {
     const int32_t *q_start, *lengths, *pages;
@@ -129,31 +132,35 @@ struct AttendBatch {
     int32_t cap[2];              // tiles a list can hold
     int32_t kept_cap[2];         // kept tiles a list can hold
     int32_t *start[2];           // [kAttendWorkers] tile at which a worker starts
-    // by entity, the requests and then the prefixes: tiles and kept tiles of the entities before
-    int32_t *tiles_before[2], *kept_before[2];   // [n_seqs + n_prefixes + 1]
     int32_t *list_before;        // [n_seqs + 1] listed tokens (of requests that share) before a request
     int32_t *listed;             // [n_tokens] those tokens
-    int32_t *prefix_list;        // [n_prefixes] list of a prefix's shared tiles
+    PrefixTile *prefix_tile;     // [n_prefixes]
     uint32_t *flags;
 };
 
 __host__ __device__ inline int clamp_to(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-// The new tokens first..end of request i, and whether the starts are in order.
-struct Queries { int32_t first, count; bool bad; };
-__host__ __device__ inline Queries queries_of(const AttendBatch &b, int i)
+// What the arrays say of request i.
+struct Request { int32_t start, end, length; };
+__host__ __device__ inline Request request_words(const AttendBatch &b, int i)
 {
-    const int a = b.q_start ? b.q_start[i] : i, e = b.q_start ? b.q_start[i + 1] : i + 1;
-    const int first = clamp_to(a, 0, b.n_tokens), end = clamp_to(e, first, b.n_tokens);
-    const int most = end - first < b.max_queries ? end - first : b.max_queries;
-    return {first, most, a != first || e != end || most != end - first};
+    return {b.q_start ? b.q_start[i] : i, b.q_start ? b.q_start[i + 1] : i + 1, b.lengths[i]};
 }
 
-// Tokens of request i in its pages, bounded by what its row of the table can name.
-__host__ __device__ inline int held_of(const int32_t *lengths, int i, int max_pages, int page_shift, bool *bad)
+// The new tokens first..end of a request, and whether the starts are in order.
+struct Queries { int32_t first, count; bool bad; };
+__host__ __device__ inline Queries queries_of(const AttendBatch &b, const Request &r)
+{
+    const int first = clamp_to(r.start, 0, b.n_tokens), end = clamp_to(r.end, first, b.n_tokens);
+    const int most = end - first < b.max_queries ? end - first : b.max_queries;
+    return {first, most, r.start != first || r.end != end || most != end - first};
+}
+
+// A length bounded by what a row of the table of pages can name.
+__host__ __device__ inline int held_of(int n, int max_pages, int page_shift, bool *bad)
 {
     const int64_t most = (int64_t)max_pages << page_shift;
-    const int n = lengths[i], fit = most < n ? (int)most : n;
+    const int fit = most < n ? (int)most : n;
     *bad |= n < 0 || fit != n;
     return fit < 0 ? 0 : fit;
 }
@@ -190,13 +197,13 @@ __host__ __device__ inline int list_rows(int l) { return l ? kWideRows : kNarrow
 __host__ __device__ inline int list_unit(int l) { return l ? kWideUnit : kNarrowUnit; }
 __host__ __device__ inline int share_rows(int group) { return group > kShareRows ? group : kShareRows; }
 
-__host__ __device__ inline AttendEntity request_of(const AttendBatch &b, int i, bool *bad)
+__host__ __device__ inline AttendEntity request_of(const AttendBatch &b, int i, const Request &r, bool *bad)
 {
     AttendEntity t{};
-    const Queries q = queries_of(b, i);
+    const Queries q = queries_of(b, r);
     *bad |= q.bad;
     t.seq = i;
-    t.len = held_of(b.lengths, i, b.max_pages, b.page_shift, bad);
+    t.len = held_of(r.length, b.max_pages, b.page_shift, bad);
     t.prefix = -1;
     t.pre_seq = -1;
     if (!q.count)
@@ -205,7 +212,7 @@ __host__ __device__ inline AttendEntity request_of(const AttendBatch &b, int i, 
     t.q_len = q.count;
     t.rows = q.count * b.group;
     const int p = prefix_of(b, i);
-    const int pre = p < 0 ? 0 : held_of(b.prefix_lengths, p, b.prefix_max_pages, b.page_shift, bad);
+    const int pre = p < 0 ? 0 : held_of(b.prefix_lengths[p], b.prefix_max_pages, b.page_shift, bad);
     t.keeps = pre > 0 && t.rows <= share_rows(b.group);
     t.list = b.wide && t.rows > kShareRows;
     t.tiles = units_for(t.rows, list_rows(t.list));
@@ -223,7 +230,7 @@ __host__ __device__ inline AttendEntity prefix_of_batch(const AttendBatch &b, in
     t.seq = p;
     t.shared = 1;
     t.prefix = t.pre_seq = -1;
-    t.len = held_of(b.prefix_lengths, p, b.prefix_max_pages, b.page_shift, bad);
+    t.len = held_of(b.prefix_lengths[p], b.prefix_max_pages, b.page_shift, bad);
     if (t.len <= 0 || listed <= 0)
         return t;
     t.token0 = list0;
@@ -234,7 +241,7 @@ __host__ __device__ inline AttendEntity prefix_of_batch(const AttendBatch &b, in
     return t;
 }
 
-// Tile j of an entity; `list0`: where the list of its prefix's tokens has the request's first.
+// Tile j of an entity; `list0`: where the list of tokens that share has the request's first.
 __host__ __device__ inline AttendTile tile_of(const AttendEntity &e, int j, int group, int list0)
 {
     const int R = list_rows(e.list), unit = list_unit(e.list);
@@ -262,6 +269,16 @@ __host__ __device__ inline AttendTile tile_of(const AttendEntity &e, int j, int 
             t.units = 1;                                   // a row that sees nothing is written too
     }
     return t;
+}
+
+// Whether a batch may be worked on: no token claimed twice, by requests (`tokens` new ones in all) or by
+// prefixes (`listed`), no more than 2^30 units, and then, as the capacities are made, every list
+// within its own (count: tiles of the lists, kept tiles, ...).
+__host__ __device__ inline bool attend_fits(const AttendBatch &b, unsigned long long tokens, unsigned long long listed,
+                                            unsigned long long units, const int32_t *count)
+{
+    return tokens <= (unsigned long long)b.n_tokens && listed <= (unsigned long long)b.n_tokens && units <= 1ull << 30 &&
+           count[0] <= b.cap[0] && count[1] <= b.cap[1] && count[2] <= b.kept_cap[0] && count[3] <= b.kept_cap[1];
 }
 
 // Where worker w keeps its part of a tile of key-value head `head`: a kept tile's parts follow
@@ -302,7 +319,7 @@ inline void attend_capacity(int64_t n_tokens, int64_t n_seqs, int64_t n_prefixes
             continue;
         // every request may end in a tile that is not full
         const bool all = l || !wide;                                  // else those of few rows only
-        cap[l] = all ? seqs + rows / R : seqs * ((kShareRows + R - 1) / R);
+        cap[l] = all ? seqs + rows / R : seqs * (((most < kShareRows ? most : kShareRows) + R - 1) / R);
         if (n_prefixes && (l ? group > kShareRows : true))
             kept[l] = seqs * ((per + R - 1) / R);
     }

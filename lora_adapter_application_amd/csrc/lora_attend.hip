@@ -28,193 +28,263 @@ constexpr float kRaise = 8.f;        // a maximum is raised when a score passes 
 // ---------------------------------------------------------------------------
 // plan: one workgroup turns the batch's lengths into the two lists of tiles
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanTilesInLds = 4096;
+constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
+constexpr int kPlanUnits = 2048;     // tiles of a list whose first units stand in LDS for the workers' search
+constexpr int kPlanPrefixes = 512;   // prefixes whose bounds and lengths stand in LDS
+constexpr int kPlanSeqs = 2048;      // requests whose listed tokens stand in LDS
+constexpr int kPlanEach = 4;         // tiles a thread writes by itself; a wave writes those of larger entities
 
+// What an entity adds to the lists.  Where requests, or prefixes, claim more tokens than there are
+// these sums may wrap; such a batch is found by sums of 64 bits and gets no work.
+struct PlanCount { int32_t v[7]; };  // tiles, kept tiles, units of the two lists, listed tokens
 
-template <typename V>
-__device__ __forceinline__ V wave_scan(V v, int lane)
+// Inclusive sums over the lanes of a wave, and over each 16 of them.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int32_t from_lane(int32_t v)
 {
-    for (int d = 1; d < 64; d <<= 1) {
-        const V o = __shfl_up(v, d);
-        if (lane >= d)
-            v += o;
-    }
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int32_t row_scan(int32_t v)
+{
+    v += from_lane<0x111, 0xf>(v);       // the lane 1 before, in its row of 16
+    v += from_lane<0x112, 0xf>(v);
+    v += from_lane<0x114, 0xf>(v);
+    v += from_lane<0x118, 0xf>(v);
     return v;
+}
+__device__ __forceinline__ int32_t wave_scan(int32_t v)
+{
+    v = row_scan(v);
+    v += from_lane<0x142, 0xa>(v);       // the last of the row before, to rows 1 and 3
+    v += from_lane<0x143, 0xc>(v);       // lane 31, to rows 2 and 3
+    return v;
+}
+
+static_assert(2 * kAttendWorkers == kPlanThreads, "a thread finds a worker's start");
+// A barrier behind which the workgroup sees its writes to LDS; unlike __syncthreads it does not wait
+// for writes to memory, about 1 us each.
+__device__ __forceinline__ void lds_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b)
 {
-    __shared__ int32_t wave_sum[5][kPlanThreads / 64];
-    __shared__ int64_t unit_sum[kPlanThreads / 64];
-    __shared__ int32_t unit0[kPlanTilesInLds];
-    __shared__ int bad_all;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (!tid)
-        bad_all = 0;
-    const int entities = b.n_seqs + b.n_prefixes;
-    int32_t base[5] = {};
+    constexpr int threads = kPlanThreads, waves = kPlanWaves;
+    __shared__ int32_t wave_sum[7][kPlanWaves];
+    __shared__ int32_t unit0[2][kPlanUnits];
+    __shared__ int32_t bounds[kPlanPrefixes + 1], pre_len[kPlanPrefixes];
+    __shared__ int32_t large[kPlanThreads], large_at[kPlanThreads][4], n_large;
+    __shared__ int32_t listed_before[kPlanSeqs + 1];
+    __shared__ unsigned long long sums[3];   // new tokens, tokens listed for prefixes, units
+    __shared__ int bad_any;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // the first requests' words are on their way before the first barrier
+    Request words{};
+    if (tid < b.n_seqs)
+        words = request_words(b, tid);
+    const bool small = b.n_seqs <= kPlanSeqs;
+    const int32_t *before = small ? listed_before : b.list_before;
+    if (tid < 3)
+        sums[tid] = 0;
+    if (!tid) {
+        bad_any = 0;
+        n_large = 0;
+    }
+    AttendBatch c = b;                   // with the prefixes' bounds and lengths from LDS, if they fit
+    if (b.n_prefixes && b.n_prefixes <= kPlanPrefixes) {
+        for (int i = tid; i <= b.n_prefixes; i += threads)
+            bounds[i] = b.prefix_seqs[i];
+        for (int i = tid; i < b.n_prefixes; i += threads)
+            pre_len[i] = b.prefix_lengths[i];
+        c.prefix_seqs = bounds;
+        c.prefix_lengths = pre_len;
+    }
+    lds_sync();
+    int32_t base[7] = {};
     bool bad = false;
+    unsigned long long sum[3] = {};
 
-    // requests, then prefixes (which need the requests' list)
+    // requests, then prefixes, which need the requests' list
     for (int part = 0; part < 2; ++part) {
-        const int first = part ? b.n_seqs : 0, end = part ? entities : b.n_seqs;
+        const int first = part ? b.n_seqs : 0, end = part ? b.n_seqs + b.n_prefixes : b.n_seqs;
         if (part) {
-            if (!tid)
-                b.list_before[b.n_seqs] = base[4];
-            __threadfence_block();
-            __syncthreads();
+            if (!tid) {
+                if (small)
+                    listed_before[b.n_seqs] = base[6];
+                else
+                    b.list_before[b.n_seqs] = base[6];
+            }
+            if (small)
+                lds_sync();
+            else
+                __syncthreads();
         }
-        for (int at = first; at < end; at += kPlanThreads) {
-            const int i = at + tid;
+        for (int from = first; from < end; from += threads) {
+            const int i = from + tid;
             AttendEntity e{};
+            PlanCount n{};
             if (i < end) {
                 if (!part) {
-                    e = request_of(b, i, &bad);
+                    e = request_of(c, i, words, &bad);
+                    if (i + threads < end)
+                        words = request_words(b, i + threads);
                 } else {
-                    const int p = i - b.n_seqs;
-                    const int s0 = b.prefix_seqs[p], s1 = b.prefix_seqs[p + 1];
+                    const int p = i - b.n_seqs, s0 = c.prefix_seqs[p], s1 = c.prefix_seqs[p + 1];
                     bad |= s0 < 0 || s1 < s0 || s1 > b.n_seqs;
                     const int lo = clamp_to(s0, 0, b.n_seqs), hi = clamp_to(s1, lo, b.n_seqs);
-                    const int l0 = b.list_before[lo];
-                    e = prefix_of_batch(b, p, l0, b.list_before[hi] - l0, &bad);
-                    b.prefix_list[p] = e.list;
+                    const int l0 = before[lo];
+                    e = prefix_of_batch(c, p, l0, before[hi] - l0, &bad);
                 }
-            }
-            int32_t mine[5] = {e.list ? 0 : e.tiles, e.list ? e.tiles : 0,
-                               e.keeps && !e.list ? e.tiles : 0, e.keeps && e.list ? e.tiles : 0, e.listed};
-            int32_t incl[5];
-            for (int c = 0; c < 5; ++c) {
-                incl[c] = wave_scan(mine[c], lane);
-                if (lane == 63)
-                    wave_sum[c][wave] = incl[c];
-            }
-            __syncthreads();
-            for (int c = 0; c < 5; ++c) {
-                int32_t before = base[c] + incl[c] - mine[c], all = 0;
-                for (int w = 0; w < kPlanThreads / 64; ++w) {
-                    const int32_t s = wave_sum[c][w];
-                    before += w < wave ? s : 0;
-                    all += s;
-                }
-                base[c] += all;
-                mine[c] = before;
-            }
-            __syncthreads();
-            if (i < end) {
+                unsigned long long units = 0;
+                for (int j = 0; j < e.tiles; ++j)
+                    units += tile_of(e, j, b.group, 0).units;
+                sum[0] += part ? 0 : e.q_len;
+                sum[1] += part ? e.rows / b.group : 0;
+                sum[2] += units;
+#pragma unroll
                 for (int l = 0; l < 2; ++l) {
-                    b.tiles_before[l][i] = mine[l];
-                    b.kept_before[l][i] = mine[2 + l];
+                    n.v[l] = e.list == l ? e.tiles : 0;
+                    n.v[2 + l] = e.list == l && e.keeps ? e.tiles : 0;
+                    n.v[4 + l] = e.list == l ? (int32_t)units : 0;
                 }
-                if (!part) {
-                    b.list_before[i] = mine[4];
-                    for (int j = 0; j < e.listed; ++j)
-                        if (mine[4] + j < b.n_tokens)
-                            b.listed[mine[4] + j] = e.token0 + j;
-                        else
-                            bad = true;
+                n.v[6] = e.listed;
+            }
+            PlanCount at{};
+            const bool any = from + wave * 64 < end;           // waves without entities only keep the barriers
+            if (!any) {
+                if (lane < 7)
+                    wave_sum[lane][wave] = 0;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 7; ++k) {
+                    const int32_t incl = wave_scan(n.v[k]);
+                    if (lane == 63)
+                        wave_sum[k][wave] = incl;
+                    at.v[k] = base[k] + incl - n.v[k];
                 }
             }
+            lds_sync();
+#pragma unroll
+            for (int k = 0; k < 7; ++k) {
+                const int32_t incl = row_scan((lane & 15) < waves ? wave_sum[k][lane & 15] : 0);
+                at.v[k] += wave ? __builtin_amdgcn_readlane(incl, wave - 1) : 0;
+                base[k] += __builtin_amdgcn_readlane(incl, 15);
+            }
+            if (i < end) {
+                const int l = e.list, tile = l ? at.v[1] : at.v[0];
+                const int kept = l ? at.v[3] : at.v[2], u0 = l ? at.v[5] : at.v[4];
+                int list0 = 0;
+                if (part) {
+                    b.prefix_tile[i - b.n_seqs] = PrefixTile{l, tile};
+                } else {
+                    b.list_before[i] = at.v[6];
+                    if (small)
+                        listed_before[i] = at.v[6];
+                    for (int j = 0; j < e.listed; ++j)
+                        if ((uint32_t)(at.v[6] + j) < (uint32_t)b.n_tokens)
+                            b.listed[at.v[6] + j] = e.token0 + j;
+                    list0 = at.v[6];
+                }
+                if (e.tiles > kPlanEach) {
+                    const int k = atomicAdd(&n_large, 1);      // their order changes no place
+                    large[k] = i;
+                    large_at[k][0] = tile;
+                    large_at[k][1] = kept;
+                    large_at[k][2] = u0;
+                    large_at[k][3] = list0;
+                } else {
+                    int u = u0;
+                    for (int j = 0; j < e.tiles && (uint32_t)(tile + j) < (uint32_t)b.cap[l]; ++j) {
+                        AttendTile t = tile_of(e, j, b.group, list0);
+                        t.kept = e.keeps ? kept + j : -1;
+                        t.unit0 = u;
+                        u += t.units;
+                        b.tiles[l][tile + j] = t;
+                        if (tile + j < kPlanUnits)
+                            unit0[l][tile + j] = t.unit0;
+                    }
+                }
+            }
+            lds_sync();
+            const int count = n_large;
+            for (int k = wave; k < count; k += waves) {
+                const int id = large[k], tile = large_at[k][0], kept = large_at[k][1];
+                bool again = false;
+                int list0 = 0;
+                AttendEntity g;
+                if (!part) {
+                    g = request_of(c, id, request_words(b, id), &again);
+                    list0 = large_at[k][3];
+                } else {
+                    const int p = id - b.n_seqs;
+                    const int lo = clamp_to(c.prefix_seqs[p], 0, b.n_seqs), hi = clamp_to(c.prefix_seqs[p + 1], lo, b.n_seqs);
+                    const int l0 = before[lo];
+                    g = prefix_of_batch(c, p, l0, before[hi] - l0, &again);
+                }
+                int u = large_at[k][2];
+                for (int j0 = 0; j0 < g.tiles; j0 += 64) {
+                    const int j = j0 + lane;
+                    AttendTile t{};
+                    if (j < g.tiles)
+                        t = tile_of(g, j, b.group, list0);
+                    const int32_t incl = wave_scan(t.units);
+                    t.kept = g.keeps ? kept + j : -1;
+                    t.unit0 = u + incl - t.units;
+                    u += __builtin_amdgcn_readlane(incl, 63);
+                    if (j < g.tiles && (uint32_t)(tile + j) < (uint32_t)b.cap[g.list]) {
+                        b.tiles[g.list][tile + j] = t;
+                        if (tile + j < kPlanUnits)
+                            unit0[g.list][tile + j] = t.unit0;
+                    }
+                }
+            }
+            lds_sync();
+            if (!tid)
+                n_large = 0;
         }
     }
     if (bad)
-        bad_all = 1;
-    if (!tid)
-        for (int l = 0; l < 2; ++l) {
-            b.tiles_before[l][entities] = base[l];
-            b.kept_before[l][entities] = base[2 + l];
-        }
-    __threadfence_block();
-    __syncthreads();
-    // a batch that fits no capacity gets no work; one that is only out of order, the work that
+        bad_any = 1;
+#pragma unroll 1
+    for (int k = 0; k < 3; ++k) {                              // whole numbers: their order changes nothing
+        const unsigned long long v = k == 0 ? sum[0] : k == 1 ? sum[1] : sum[2];
+        const uint32_t lo = wave_scan((int32_t)(v & 0xffffff)), hi = wave_scan((int32_t)(v >> 24));
+        if (lane == 63 && (lo | hi))
+            atomicAdd(&sums[k], ((unsigned long long)hi << 24) + lo);
+    }
+    lds_sync();
+    if (base[0] > kPlanUnits || base[1] > kPlanUnits)
+        __syncthreads();                                       // first units that the search reads from memory
+    // a batch that claims tokens twice gets no work; one that is only out of order, the work that
     // its clamped values name
-    bool none = base[4] > b.n_tokens;
-    for (int l = 0; l < 2; ++l)
-        none |= base[l] > b.cap[l] || base[2 + l] > b.kept_cap[l];
-    const bool told = bad_all;
-
-    for (int l = 0; l < 2; ++l) {
-        const int tiles = none ? 0 : base[l];
-        int64_t total = 0;
-        for (int at = 0; at < tiles; at += kPlanThreads) {
-            const int x = at + tid;
-            AttendTile t{};
-            if (x < tiles) {
-                int lo = 0, hi = entities - 1;               // the last entity that starts at or before x
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (b.tiles_before[l][mid] <= x)
-                        lo = mid;
-                    else
-                        hi = mid - 1;
-                }
-                const int j = x - b.tiles_before[l][lo];
-                bool again = false;
-                AttendEntity e;
-                int list0 = 0;
-                if (lo < b.n_seqs) {
-                    e = request_of(b, lo, &again);
-                    if (e.prefix >= 0)
-                        list0 = b.list_before[lo] - b.list_before[clamp_to(b.prefix_seqs[e.prefix], 0, lo)];
-                } else {
-                    const int p = lo - b.n_seqs;
-                    const int s0 = clamp_to(b.prefix_seqs[p], 0, b.n_seqs);
-                    const int s1 = clamp_to(b.prefix_seqs[p + 1], s0, b.n_seqs);
-                    e = prefix_of_batch(b, p, b.list_before[s0], b.list_before[s1] - b.list_before[s0], &again);
-                }
-                t = tile_of(e, j, b.group, list0);
-                t.kept = e.keeps ? b.kept_before[l][lo] + j : -1;
-            }
-            const int64_t incl = wave_scan((int64_t)t.units, lane);
-            if (lane == 63)
-                unit_sum[wave] = incl;
-            __syncthreads();
-            int64_t before = total + incl - t.units;
-            for (int w = 0; w < kPlanThreads / 64; ++w) {
-                before += w < wave ? unit_sum[w] : 0;
-                total += unit_sum[w];
-            }
-            __syncthreads();
-            if (x < tiles) {
-                t.unit0 = (int32_t)before;
-                b.tiles[l][x] = t;
-                if (x < kPlanTilesInLds)
-                    unit0[x] = (int32_t)before;
-            }
+    const bool none = !attend_fits(b, sums[0], sums[1], sums[2], base);
+    const int l = wave >= kPlanWaves / 2;                      // half of the threads for each list
+    AttendList out{none ? 0 : l ? base[1] : base[0], none ? 0 : l ? base[5] : base[4], none ? 0 : l ? base[3] : base[2], 1};
+    const int64_t all = (int64_t)out.units * b.kv_heads, run = worker_run(all, kAttendWorkers);
+    out.run = run < 1 ? 1 : (int32_t)run;
+    const int w = tid & (kAttendWorkers - 1);
+    if (!w)
+        b.plan->list[l] = out;
+    const int64_t u = (int64_t)w * out.run;
+    if (u < all) {
+        const int32_t want = (int32_t)(u >> 32 ? u % out.units : (uint32_t)u % (uint32_t)out.units);
+        int lo = 0, hi = out.tiles - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            const int32_t v = mid < kPlanUnits ? unit0[l][mid] : b.tiles[l][mid].unit0;
+            if (v <= want)
+                lo = mid;
+            else
+                hi = mid - 1;
         }
-        const bool over = total > (1 << 30);
-        none |= over;
-        AttendList out{};
-        out.tiles = over ? 0 : tiles;
-        out.units = over ? 0 : (int32_t)total;
-        out.kept = base[2 + l];
-        const int64_t run = worker_run((int64_t)out.units * b.kv_heads, kAttendWorkers);
-        out.run = (int32_t)(run < 1 ? 1 : run);
-        if (!tid)
-            b.plan->list[l] = out;
-        __threadfence_block();
-        __syncthreads();
-        if (tid < kAttendWorkers && out.units) {
-            const int64_t u = (int64_t)tid * out.run;
-            if (u < (int64_t)out.units * b.kv_heads) {
-                const int32_t want = (int32_t)(u % out.units);
-                int lo = 0, hi = out.tiles - 1;
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    const int32_t v = mid < kPlanTilesInLds ? unit0[mid] : b.tiles[l][mid].unit0;
-                    if (v <= want)
-                        lo = mid;
-                    else
-                        hi = mid - 1;
-                }
-                b.start[l][tid] = lo;
-            }
-        }
-        __syncthreads();
+        b.start[l][w] = lo;
     }
     if (!tid) {
         b.plan->bad = none;
-        if (told || none)
+        if (none || bad_any)
             atomicOr(b.flags, LORA_FLAG_ATTEND_BATCH);
     }
 }
@@ -442,8 +512,9 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
     __shared__ float lds_o[4][kNarrowRows][W];
     __shared__ float lds_m[4][kNarrowRows], lds_l[4][kNarrowRows];
     const AttendBatch &b = a.b;
-    const AttendList list = scalar(&b.plan->list[0]);
     const int w = worker_of_block();
+    const AttendList list = scalar(&b.plan->list[0]);
+    const int first = scalar(b.start[0] + w);                // stale if the worker has no work
     const int64_t total = scalar(&b.plan->bad) ? 0 : (int64_t)list.units * b.kv_heads;
     int64_t at = (int64_t)w * list.run;
     const int64_t end = at + list.run < total ? at + list.run : total;
@@ -452,7 +523,7 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
     const int heads = b.group * b.kv_heads, hd = a.c.head_dim;
     const bool vec = (((uintptr_t)a.q | (uintptr_t)a.y) & 15) == 0;
-    int head = __builtin_amdgcn_readfirstlane((int)(at / list.units)), x = scalar(b.start[0] + w);
+    int head = __builtin_amdgcn_readfirstlane((int)(at / list.units)), x = first;
 
     for (; at < end; ++x) {
         if (x == list.tiles) {
@@ -670,8 +741,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
     __shared__ alignas(16) char lds[2 * kBuf];
     __shared__ float scales[2][CODED ? 4 * kBlock : 1];      // of two blocks' keys, of their values
     const AttendBatch &b = a.b;
-    const AttendList list = scalar(&b.plan->list[1]);
     const int w = worker_of_block();
+    const AttendList list = scalar(&b.plan->list[1]);
+    const int first = scalar(b.start[1] + w);                // stale if the worker has no work
     const int64_t total = scalar(&b.plan->bad) ? 0 : (int64_t)list.units * b.kv_heads;
     int64_t at = (int64_t)w * list.run;
     const int64_t end = at + list.run < total ? at + list.run : total;
@@ -685,7 +757,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
     // row r of a result holds token 16 (r / 16) + 8 h + 0..7 in its registers when the rows of
     // the operand take the tokens with bits 2 and 3 of their number exchanged
     const int ktok = (n & 19) | (n & 4) << 1 | (n & 8) >> 1;
-    int head = __builtin_amdgcn_readfirstlane((int)(at / list.units)), x = scalar(b.start[1] + w);
+    int head = __builtin_amdgcn_readfirstlane((int)(at / list.units)), x = first;
 
     for (; at < end; ++x) {
         if (x == list.tiles) {
@@ -977,49 +1049,121 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
 // ---------------------------------------------------------------------------
 // joining parts
 
-// One workgroup a tile and key-value head; a row's dims four to a lane.
+// One workgroup a tile and key-value head, four dims a lane.  A group of lanes takes a row, or a
+// share of its parts where rows are few: each lane fetches the maximum and sum of one part, the
+// weights follow from them, and no load of a part waits for another.
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
 {
+    constexpr int NL = DP <= 64 ? 16 : DP <= 128 ? 32 : 64, NG = 256 / NL;
+    __shared__ f32x4 lds_o[NG][NL];
+    __shared__ float lds_m[NG], lds_l[NG];
     const AttendBatch &b = a.b;
-    if (b.plan->bad)
-        return;
     const int l = (int)blockIdx.x >= b.cap[0];
     const int x = l ? blockIdx.x - b.cap[0] : blockIdx.x, head = blockIdx.y;
-    const AttendList list = b.plan->list[l];
+    const AttendList list = b.plan->list[l], other = b.plan->list[!l];
+    const AttendTile t = b.tiles[l][x];                      // stale where x is past the list
     if (x >= list.tiles)
         return;
-    const AttendTile t = b.tiles[l][x];
     const int w0 = first_worker(list, head, t), w1 = last_worker(list, head, t);
     if (t.shared || (t.kept < 0 && w0 == w1))
         return;
     const int R = list_rows(l), hd = a.c.head_dim, heads = b.group * b.kv_heads;
-    const int L = t.prefix >= 0 ? b.prefix_list[t.prefix] : 0;
-    const AttendList shared = b.plan->list[L];
+    PrefixTile pre{0, 0};
+    int pre_row = 0;
+    if (t.prefix >= 0) {
+        pre = b.prefix_tile[t.prefix];
+        const int lo = clamp_to(b.prefix_seqs[t.prefix], 0, b.n_seqs);
+        pre_row = t.pre_row - b.list_before[lo] * b.group;
+    }
+    const AttendList shared = pre.list == l ? list : other;
+    const int PR = list_rows(pre.list);
     const bool vec = ((uintptr_t)a.y & 15) == 0;
-    for (int i = threadIdx.x; i < t.rows * (DP / 4); i += 256) {
-        const int r = i / (DP / 4), d = i % (DP / 4) * 4;
+    int split = 1;                                           // groups of a row
+    while (split < 8 && t.rows * split * 2 <= NG)
+        split *= 2;
+    const int grp = threadIdx.x / NL, lane = threadIdx.x % NL, sub = grp % split, d = lane * 4;
+    const int n_own = w1 - w0 + 1;
+    const int64_t own_at = part_slot(list, head, t, w0);
+    for (int r0 = 0; r0 < t.rows; r0 += NG / split) {
+        const int r = r0 + grp / split;
+        const bool live = r < t.rows;
         float top = kNone, sum = 0;
         f32x4 v = {0, 0, 0, 0};
-        auto add = [&](const float *parts, const float *sums, int64_t at) {
-            const float m = sums[at * 2], s = sums[at * 2 + 1];
-            const f32x4 o = *(const f32x4 *)(parts + at * DP + d);
-            const float up = __builtin_fmaxf(top, m);
-            const float f = top == kNone ? 1.f : fexp2(top - up), e = m == kNone ? 1.f : fexp2(m - up);
-            sum = sum * f + s * e;
-            v = v * f + o * e;
-            top = up;
-        };
-        for (int w = w0; w <= w1; ++w)
-            add(a.parts[l], a.sums[l], part_slot(list, head, t, w) * R + r);
-        if (t.prefix >= 0) {
-            const int pr = t.pre_row + r, PR = list_rows(L);
-            const AttendTile s = b.tiles[L][b.tiles_before[L][b.n_seqs + t.prefix] + pr / PR];
-            const int s0 = first_worker(shared, head, s), s1 = last_worker(shared, head, s);
-            for (int w = s0; w <= s1; ++w)
-                add(a.parts[L], a.sums[L], part_slot(shared, head, s, w) * PR + pr % PR);
+        if (live) {
+            // the parts of the row: its own ones, then those over its prefix
+            int n = n_own, pr = 0;
+            int64_t pre_at = 0;
+            if (t.prefix >= 0) {
+                pr = pre_row + r;
+                const AttendTile s = b.tiles[pre.list][pre.tile + pr / PR];
+                const int s0 = first_worker(shared, head, s);
+                n += last_worker(shared, head, s) - s0 + 1;
+                pre_at = part_slot(shared, head, s, s0);
+                pr %= PR;
+            }
+            for (int k0 = 0; k0 < n; k0 += NL * split) {
+                const bool there = k0 + lane * split + sub < n;
+                const int k = there ? k0 + lane * split + sub : 0;
+                const bool mine = k < n_own;
+                // of a tile that is not kept: its first worker's last part, the others' first
+                const int64_t slot = mine ? (t.kept >= 0 ? own_at + k : k ? 2ll * (w0 + k) : own_at) : pre_at + (k - n_own);
+                const int64_t at = mine ? slot * R + r : slot * PR + pr;
+                float m = kNone, one = 0;
+                if (there) {
+                    const float2 ms = *(const float2 *)((mine ? a.sums[l] : a.sums[pre.list]) + at * 2);
+                    m = ms.x;
+                    one = ms.y;
+                }
+                float up = m;
+#pragma unroll
+                for (int i = 1; i < NL; i <<= 1)
+                    up = __builtin_fmaxf(up, __shfl_xor(up, i, NL));
+                up = __builtin_fmaxf(up, top);
+                const float f = !there ? 0.f : m == kNone ? 1.f : fexp2(m - up), was = top == kNone ? 1.f : fexp2(top - up);
+                one *= f;
+#pragma unroll
+                for (int i = 1; i < NL; i <<= 1)
+                    one += __shfl_xor(one, i, NL);
+                sum = sum * was + one;
+                v *= was;
+                top = up;
+                const uint64_t from = (uint64_t)((mine ? a.parts[l] : a.parts[pre.list]) + at * DP);
+                const int here = (n - k0 - sub + split - 1) / split, count = here < NL ? here : NL;
+                for (int i0 = 0; i0 < count; i0 += 4)        // past the last: the row's first part, left out
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t lo = __shfl((uint32_t)from, i0 + i, NL), hi = __shfl((uint32_t)(from >> 32), i0 + i, NL);
+                        const float by = __shfl(f, i0 + i, NL);
+                        if (DP == 4 * NL || d < DP) {
+                            const f32x4 o = *(const f32x4 *)(((uint64_t)hi << 32 | lo) + d * 4) * by;
+                            v += i0 + i < count ? o : f32x4{0, 0, 0, 0};
+                        }
+                    }
+            }
         }
-        if (d < hd) {
+        if (split > 1) {
+            lds_o[grp][lane] = v;
+            if (!lane) {
+                lds_m[grp] = top;
+                lds_l[grp] = sum;
+            }
+            __syncthreads();
+            if (live && !sub) {
+                float up = top;
+                for (int k = 1; k < split; ++k)
+                    up = __builtin_fmaxf(up, lds_m[grp + k]);
+                float f = top == kNone ? 1.f : fexp2(top - up);
+                v *= f;
+                sum *= f;
+                for (int k = 1; k < split; ++k) {
+                    f = lds_m[grp + k] == kNone ? 1.f : fexp2(lds_m[grp + k] - up);
+                    v += lds_o[grp + k][lane] * f;
+                    sum += lds_l[grp + k] * f;
+                }
+            }
+        }
+        if (live && !sub && d < hd) {
             const int rr = t.row0 + r;
             const bool empty = t.len - t.q_len + 1 + rr / b.group <= 0 && !t.pre_len && t.prefix < 0;
             float out[4];

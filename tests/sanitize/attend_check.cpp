@@ -89,7 +89,7 @@ static void check_plan(const Batch &in, bool ordered)
     for (int i = 0; i < N; ++i) {
         if (i < b.n_seqs) {
             list_before[i] = list;
-            ent[i] = request_of(b, i, &bad);
+            ent[i] = request_of(b, i, request_words(b, i), &bad);
             CHECK(ent[i].listed <= share_rows(b.group) / b.group);
             for (int j = 0; j < ent[i].listed; ++j) {
                 CHECK(ent[i].token0 + j >= 0 && ent[i].token0 + j < b.n_tokens);
@@ -111,13 +111,21 @@ static void check_plan(const Batch &in, bool ordered)
         tiles[ent[i].list] += ent[i].tiles;
         kept[ent[i].list] += ent[i].keeps ? ent[i].tiles : 0;
     }
-    const bool fits = list <= b.n_tokens && tiles[0] <= b.cap[0] && tiles[1] <= b.cap[1] &&
-                      kept[0] <= b.kept_cap[0] && kept[1] <= b.kept_cap[1];
+    unsigned long long claimed = 0, shared = 0, all_units = 0;
+    for (int i = 0; i < N; ++i) {
+        (i < b.n_seqs ? claimed : shared) += ent[i].rows / b.group;
+        for (int j = 0; j < ent[i].tiles; ++j)
+            all_units += tile_of(ent[i], j, b.group, 0).units;
+    }
+    const int32_t count[4] = {(int32_t)tiles[0], (int32_t)tiles[1], (int32_t)kept[0], (int32_t)kept[1]};
+    const bool fits = attend_fits(b, claimed, shared, all_units, count);
     if (ordered) {
         CHECK(!bad);
         CHECK(fits);
     } else if (!fits) {
+        // nothing but tokens claimed twice and units without end is refused
         CHECK(bad);
+        CHECK(claimed > (unsigned long long)b.n_tokens || shared > (unsigned long long)b.n_tokens || all_units > 1ull << 30);
         return;
     }
     std::vector<int> rows_done((size_t)b.n_tokens * b.group, 0);
@@ -130,7 +138,7 @@ static void check_plan(const Batch &in, bool ordered)
                 continue;
             int list0 = 0;
             if (i < b.n_seqs && ent[i].prefix >= 0)
-                list0 = (int)(list_before[i] - list_before[clamp_to(b.prefix_seqs[ent[i].prefix], 0, i)]);
+                list0 = (int)list_before[i];
             for (int j = 0; j < ent[i].tiles; ++j) {
                 AttendTile t = tile_of(ent[i], j, b.group, list0);
                 CHECK((int64_t)all[l].size() == tiles_before[l][i] + j);
@@ -176,7 +184,9 @@ static void check_plan(const Batch &in, bool ordered)
                         ++rows_done[(size_t)tok * b.group + row % b.group];
                     if (t.prefix >= 0 && !h) {               // the row of the shared tile is the same token's
                         const AttendEntity &p = ent[b.n_seqs + t.prefix];
-                        const int pr = t.pre_row + r, PR = list_rows(p.list);
+                        const int lo = clamp_to(b.prefix_seqs[t.prefix], 0, b.n_seqs);
+                        const int pr = t.pre_row - (int)list_before[lo] * b.group + r, PR = list_rows(p.list);
+                        CHECK(pr >= 0);
                         CHECK(pr / PR < p.tiles);
                         const AttendTile &s = all[p.list][tiles_before[p.list][b.n_seqs + t.prefix] + pr / PR];
                         CHECK(s.shared && s.seq == t.prefix && pr % PR < s.rows && s.row0 + pr % PR == pr);
