@@ -42,6 +42,52 @@ __global__ __launch_bounds__(256) void norm_rotary_kernel(NormArgs a, int lanes)
     const RotaryArgs &ro = a.rot;
     const int t = blockIdx.x;
     const int rd = ro.rot.rotary_dim, pairs = rd >> 1, hd = ro.rot.head_dim;
+    // Items of a head: `turning` of them hold N pairs each, in one or two pieces, the rest one piece.
+    constexpr bool TWO = HALF || V == 1;                 // a turning item has two pieces
+    constexpr int N = V == 1 ? 1 : HALF ? V : V / 2;
+    const int turning = pairs / N, items = turning + (hd - rd) / V;
+    const int per_pass = 256 / lanes, lane = threadIdx.x & (lanes - 1), first = threadIdx.x / lanes;
+    int at0[NI], at1[NI];                                // first elements of an item's pieces
+    bool turn[NI], used[NI];
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+        const int item = lane + k * lanes;
+        used[k] = item < items;
+        turn[k] = item < turning;
+        at0[k] = !turn[k] ? rd + (item - turning) * V : HALF ? item * N : 2 * item * N;
+        at1[k] = HALF ? pairs + item * N : 2 * item + 1;
+    }
+    // A head's values, fetched while the table is formed or the head before is worked on.
+    struct Head {
+        bool live;
+        T *y;
+        const T *g;
+        P u[NI], v[NI];
+    };
+    int mi = 0, base = 0;
+    auto fetch = [&](int h, Head &s) {
+        s.live = h < ro.total_heads;                     // all lanes take part in the shuffles
+        while (s.live && h - base >= ro.m[mi].heads)
+            base += ro.m[mi++].heads;
+        if (!s.live)
+            return;
+        const int64_t at = (int64_t)t * ro.m[mi].width + (int64_t)(h - base) * hd;
+        const T *x = (const T *)ro.m[mi].x + at;
+        s.y = (T *)ro.m[mi].y + at;
+        s.g = (const T *)a.weight[mi];
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            if (!used[k])
+                continue;
+            s.u[k] = *(const P *)(x + at0[k]);
+            if (TWO && turn[k])
+                s.v[k] = *(const P *)(x + at1[k]);
+        }
+    };
+    const int step = gridDim.y * per_pass, h0 = blockIdx.y * per_pass + first;
+    Head s;
+    fetch(h0, s);
+
     const double pos = (double)ro.positions[t];
     for (int p = threadIdx.x; p < pairs; p += 256) {
         const double turns = pos * ro.rot.turns[p];
@@ -61,58 +107,42 @@ __global__ __launch_bounds__(256) void norm_rotary_kernel(NormArgs a, int lanes)
     }
     __syncthreads();
 
-    // Items of a head: `turning` of them hold N pairs each, in one or two pieces, the rest one piece.
-    constexpr bool TWO = HALF || V == 1;                 // a turning item has two pieces
-    constexpr int N = V == 1 ? 1 : HALF ? V : V / 2;
-    const int turning = pairs / N, items = turning + (hd - rd) / V;
-    const int per_pass = 256 / lanes, lane = threadIdx.x & (lanes - 1), first = threadIdx.x / lanes;
-    int at0[NI], at1[NI];                                // first elements of an item's pieces
-    bool turn[NI], used[NI];
     float2 w[NI][N];
 #pragma unroll
-    for (int k = 0; k < NI; ++k) {
-        const int item = lane + k * lanes;
-        used[k] = item < items;
-        turn[k] = item < turning;
-        at0[k] = !turn[k] ? rd + (item - turning) * V : HALF ? item * N : 2 * item * N;
-        at1[k] = HALF ? pairs + item * N : 2 * item + 1;
+    for (int k = 0; k < NI; ++k)
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            w[k][i] = turn[k] ? cs[item * N + i] : make_float2(1.f, 0.f);
-    }
-    int mi = 0, base = 0;
-    for (int h0 = blockIdx.y * per_pass; h0 < ro.total_heads; h0 += gridDim.y * per_pass) {
-        const int h = h0 + first;
-        const bool live = h < ro.total_heads;            // all lanes take part in the shuffles
-        while (live && h - base >= ro.m[mi].heads)
-            base += ro.m[mi++].heads;
-        const int64_t at = live ? (int64_t)t * ro.m[mi].width + (int64_t)(h - base) * hd : 0;
-        const T *x = (const T *)ro.m[mi].x + at;
-        T *y = (T *)ro.m[mi].y + at;
-        const T *g = (const T *)a.weight[mi];
-        P u[NI], v[NI], gu[NI], gv[NI];
+            w[k][i] = turn[k] ? cs[(lane + k * lanes) * N + i] : make_float2(1.f, 0.f);
+    const T *loaded = nullptr;                           // the weight in gu and gv
+    P gu[NI], gv[NI];
+    for (int h = h0 - first; h < ro.total_heads; h += step) {
+        Head next;
+        fetch(h + first + step, next);
+        if (s.live && s.g && s.g != loaded) {
+#pragma unroll
+            for (int k = 0; k < NI; ++k) {
+                if (!used[k])
+                    continue;
+                gu[k] = *(const P *)(s.g + at0[k]);
+                if (TWO && turn[k])
+                    gv[k] = *(const P *)(s.g + at1[k]);
+            }
+            loaded = s.g;
+        }
         float sum = 0;
 #pragma unroll
         for (int k = 0; k < NI; ++k) {
-            if (!live || !used[k])
+            if (!s.live || !used[k])
                 continue;
-            u[k] = *(const P *)(x + at0[k]);
-            if (TWO && turn[k])
-                v[k] = *(const P *)(x + at1[k]);
-            if (g) {
-                gu[k] = *(const P *)(g + at0[k]);
-                if (TWO && turn[k])
-                    gv[k] = *(const P *)(g + at1[k]);
-            }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float e = Elem<T>::get(u[k].v[i]);
+                const float e = Elem<T>::get(s.u[k].v[i]);
                 sum = fmaf(e, e, sum);
             }
             if (TWO && turn[k])
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float e = Elem<T>::get(v[k].v[i]);
+                    const float e = Elem<T>::get(s.v[k].v[i]);
                     sum = fmaf(e, e, sum);
                 }
         }
@@ -121,14 +151,14 @@ __global__ __launch_bounds__(256) void norm_rotary_kernel(NormArgs a, int lanes)
         const float r = 1.f / sqrtf(sum / (float)hd + a.eps);
 #pragma unroll
         for (int k = 0; k < NI; ++k) {
-            if (!live || !used[k])
+            if (!s.live || !used[k])
                 continue;
             float p[V], q[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                p[i] = Elem<T>::get(u[k].v[i]) * r * (g ? Elem<T>::get(gu[k].v[i]) : 1.f);
+                p[i] = Elem<T>::get(s.u[k].v[i]) * r * (s.g ? Elem<T>::get(gu[k].v[i]) : 1.f);
                 if (TWO && turn[k])
-                    q[i] = Elem<T>::get(v[k].v[i]) * r * (g ? Elem<T>::get(gv[k].v[i]) : 1.f);
+                    q[i] = Elem<T>::get(s.v[k].v[i]) * r * (s.g ? Elem<T>::get(gv[k].v[i]) : 1.f);
             }
             P out0, out1;
             if (!turn[k]) {
@@ -148,10 +178,11 @@ __global__ __launch_bounds__(256) void norm_rotary_kernel(NormArgs a, int lanes)
                     out0.v[2 * i + 1] = Elem<T>::put(fmaf(p[2 * i], w[k][i].y, p[2 * i + 1] * w[k][i].x));
                 }
             }
-            *(P *)(y + at0[k]) = out0;
+            *(P *)(s.y + at0[k]) = out0;
             if (TWO && turn[k])
-                *(P *)(y + at1[k]) = out1;
+                *(P *)(s.y + at1[k]) = out1;
         }
+        s = next;
     }
 }
 
