@@ -93,7 +93,7 @@ enum {
                                                 tile's partials (its rows were left untouched) */
 #define LORA_FLAG_ATTEND_BATCH 0x4u          /* a prepared batch held a length, start or bound out of
                                                 range or out of order */
-#define LORA_FLAG_CACHE_PAGE 0x8u            /* an attended page was not in 0..pages-1 (skipped) */
+#define LORA_FLAG_CACHE_PAGE 0x8u            /* an attended page was not in 0..pages-1 (its rows are NaN) */
 #define LORA_FLAG_CACHE_SLOT 0x10u           /* a stored or loaded slot was past the cache (skipped) */
 
 typedef struct {
@@ -716,8 +716,8 @@ int lora_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads,
  * their product with the values, and y once.  The order of the sums goes by the batch, so
  * equal calls give equal bits.  Tokens that a row does not see change nothing, whatever their
  * slots hold.  A token that sees nothing (a request of length 0 without a prefix) gets zeros;
- * rows of q that belong to no request leave their row of y as it is.  Tokens on a page
- * outside the cache are skipped and set LORA_FLAG_CACHE_PAGE; a row that they leave with nothing becomes NaN.
+ * rows of q that belong to no request leave their row of y as it is.  A page outside of the
+ * cache sets LORA_FLAG_CACHE_PAGE, and rows of the requests that it is named for may become NaN.
  * Errors: no prepared batch, or one prepared outside of the capture that the call is in, or in
  * one that it is not in -> LORA_ERR_NO_PLAN; a cache of another shape than the prepared, NULL or
  * overlapping buffers, a bad scale -> LORA_ERR_INVALID_ARGUMENT.

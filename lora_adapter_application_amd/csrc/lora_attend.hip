@@ -12,6 +12,8 @@
 // as that of the rounded result); the sum is that of the unrounded ones.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "lora_attend.h"
 #include "lora_dma.h"
 
@@ -21,6 +23,8 @@ namespace {
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+
+typedef const __attribute__((address_space(4))) int32_t *PageTable;   // read through the scalar cache
 
 constexpr float kRaise = 8.f;        // a maximum is raised when a score passes it by 2^8
 #define kNone (-__builtin_inff())
@@ -369,12 +373,24 @@ __device__ __forceinline__ Frag<float> frag_of(const Held<float, kCacheNative> &
 {
     return {{h.r[0].x, h.r[0].y, h.r[0].z, h.r[0].w, h.r[1].x, h.r[1].y, h.r[1].z, h.r[1].w}};
 }
-template <typename T>
-__device__ __forceinline__ Frag<T> frag_of(const Held<T, kCacheFp8> &h)
+__device__ __forceinline__ Frag<float> frag_of(const Held<float, kCacheFp8> &h)
 {
     float v[8];
     fp8_values(h.r, v);
-    return to_frag(v, T());
+    return to_frag(v, float());
+}
+__device__ __forceinline__ Frag<uint16_t> frag_of(const Held<uint16_t, kCacheFp8> &h)
+{
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+    Frag<uint16_t> f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const bf16x2 v = w & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w < 2 ? h.r.x : h.r.y, 1.f, true)
+                               : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w < 2 ? h.r.x : h.r.y, 1.f, false);
+        f.v[2 * w] = v[0];
+        f.v[2 * w + 1] = v[1];
+    }
+    return f;
 }
 template <typename T>
 __device__ __forceinline__ Frag<T> frag_of(const Held<T, kCacheInt8> &h)
@@ -575,12 +591,12 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
                 continue;
             const int page = (in_pre ? pre_pages : own_pages)[tok0 >> a.c.page_shift];
             const bool good = (uint32_t)page < (uint32_t)a.c.pages;
-            if (!good) {                                     // its tokens are seen by no row
+            if (!good) {                                     // rows that see it become NaN
+                l = __builtin_nanf("");
                 if (!lane)
                     atomicOr(b.flags, LORA_FLAG_CACHE_PAGE);
-                continue;
             }
-            const char *blk = a.c.base + cache_block(a.c, page, head, (tok0 >> 5) & ((1 << (a.c.page_shift - 5)) - 1));
+            const char *blk = a.c.base + cache_block(a.c, good ? page : 0, head, (tok0 >> 5) & ((1 << (a.c.page_shift - 5)) - 1));
             Held<T, KIND> kh[2][NS], vh[ND];
             const int km = 8 * (n >> 2) + (n & 3);
 #pragma unroll
@@ -723,6 +739,15 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
     }
 }
 
+// Four results of a block from register r on, times f.
+__device__ __forceinline__ f32x16 scaled(f32x16 v, int r, f32x4 f)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[r + i] *= f[i];
+    return v;
+}
+
 // ---------------------------------------------------------------------------
 // wide tiles: 128 rows, four waves on 32 rows each of a unit of 64 tokens
 
@@ -786,57 +811,57 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                     q[s] = q_frag<T>(p + d, vec);
             }
         }
-        // own tokens that this lane's row sees, the fewest and the most of the wave, the most of the tile
+        // own tokens that this lane's row sees, the most of the wave's rows, the fewest and the most of the tile's
         const int per = t.shared ? 0 : t.len - t.q_len + 1;
         const int see = t.shared ? t.len : per + row / b.group;
-        const int see_min = t.shared ? t.len : per + (t.row0 + wr) / b.group;
-        const int see_max = t.shared ? t.len : per + (t.row0 + wl) / b.group;
-        const int see_all = t.shared ? t.len : per + (t.row0 + t.rows - 1) / b.group;
+        const int see_wave = t.shared ? t.len : per + (t.row0 + (works ? wl : 0)) / b.group;
+        const int see_min = t.shared ? t.len : per + t.row0 / b.group;
+        const int see_max = t.shared ? t.len : per + (t.row0 + t.rows - 1) / b.group;
         const int pre_units = units_for(t.pre_len, kWideUnit);
-        const int32_t *own_pages = t.shared ? b.prefix_pages + (int64_t)t.seq * b.prefix_max_pages
-                                            : b.pages + (int64_t)t.seq * b.max_pages;
-        const int32_t *pre_pages = t.pre_len ? b.prefix_pages + (int64_t)t.pre_seq * b.prefix_max_pages : nullptr;
+        // units that every row sees whole: those before pre_full, and from pre_units on those before own_full
+        const int pre_full = t.pre_len / kWideUnit, own_full = pre_units + (see_min > 0 ? see_min / kWideUnit : 0);
+        const PageTable own_pages = (PageTable)(t.shared ? b.prefix_pages + (int64_t)t.seq * b.prefix_max_pages
+                                                         : b.pages + (int64_t)t.seq * b.max_pages);
+        const PageTable pre_pages = (PageTable)(b.prefix_pages + (t.pre_len ? (int64_t)t.pre_seq * b.prefix_max_pages : 0));
 
-        // A unit's two blocks: their pages, and which of them are there.
-        auto pages_of = [&](int u, int (&page)[2]) {
+        // The pages of a unit's two blocks, through the scalar cache: their wait is not the wait of the
+        // loads in flight.  Blocks that no row sees have the cache's first page.
+        auto pages_of = [&](int u, int (&page)[2]) __attribute__((always_inline)) {
             const bool in_pre = u < pre_units;
-            const int tok0 = (in_pre ? u : u - pre_units) * kWideUnit, most = in_pre ? t.pre_len : see_all;
-            const int32_t *pages = in_pre ? pre_pages : own_pages;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                page[j] = -1;
-                if (u < u1 && tok0 + j * kBlock < most) {
-                    const int v = __builtin_amdgcn_readfirstlane(pages[(tok0 + j * kBlock) >> a.c.page_shift]);
-                    if ((uint32_t)v < (uint32_t)a.c.pages)
-                        page[j] = v;
-                    else if (!tid)
-                        atomicOr(b.flags, LORA_FLAG_CACHE_PAGE);
-                }
-            }
+            const int tok0 = (in_pre ? u : u - pre_units) * kWideUnit, most = in_pre ? t.pre_len : see_max;
+            const PageTable pages = in_pre ? pre_pages : own_pages;
+            page[0] = page[1] = 0;
+            if (u < u1 && tok0 < most)
+                page[0] = pages[tok0 >> a.c.page_shift];
+            if (u < u1 && tok0 + kBlock < most)
+                page[1] = a.c.page_shift > 5 ? page[0] : pages[(tok0 + kBlock) >> a.c.page_shift];
         };
-        auto block_of = [&](int u, int j, int page) -> const char * {
+        bool lost = false;                                   // a page was not one of the cache's
+        auto block_of = [&](int u, int j, int page) __attribute__((always_inline)) -> const char * {
+            const bool good = (uint32_t)page < (uint32_t)a.c.pages;
+            lost |= !good;
             const int tok0 = (u < pre_units ? u : u - pre_units) * kWideUnit + j * kBlock;
-            const uint64_t p = (uint64_t)(a.c.base + cache_block(a.c, page, head, (tok0 >> 5) & in_page));
+            const uint64_t p = (uint64_t)(a.c.base + cache_block(a.c, good ? page : 0, head, (tok0 >> 5) & in_page));
             const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
             return (const char *)((uint64_t)hi << 32 | lo);
         };
         constexpr int NC = CODED ? (kBlock * DP / 16 + 255) / 256 : 1;   // 16-byte pieces a thread takes of a side
         uint4 held[2][2][NC];
         float held_scale;
+        const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
         // native: straight into LDS; codes: into registers, and from there as bf16
-        auto fetch = [&](int u, int buf, const int (&page)[2]) {
+        auto fetch = [&](int u, int buf, const int (&page)[2]) __attribute__((always_inline)) {
+            const char *blk[2] = {block_of(u, 0, page[0]), block_of(u, 1, page[1])};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                if (page[j] < 0)
-                    continue;
-                const char *blk = block_of(u, j, page[j]);
                 if constexpr (!CODED) {
-                    const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds +
-                                        buf * kBuf + j * kSide;
+                    constexpr int kPieces = 2 * kSide / 1024;      // of keys and values, which follow each other
 #pragma unroll
-                    for (int i = wave; i < 2 * kSide / 1024; i += 4) {
-                        const int side = i >= kSide / 1024, k = i - side * (kSide / 1024);
-                        dma16_off(blk, (uint32_t)(i * 1024 + lane * 16), to + side * 2 * kSide + k * 1024);
+                    for (int i = 0; i < (kPieces + 3) / 4; ++i) {
+                        const int k = wave + 4 * i, side = k >= kPieces / 2;
+                        if (kPieces % 4 == 0 || k < kPieces)
+                            dma16_off(blk[j], (uint32_t)(k * 1024 + lane * 16),
+                                      lds_at + buf * kBuf + j * kSide + side * kSide + k * 1024);
                     }
                 } else {
 #pragma unroll
@@ -844,20 +869,17 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
 #pragma unroll
                         for (int c = 0; c < NC; ++c)
                             if (tid + 256 * c < kBlock * DP / 16)
-                                held[j][side][c] = *(const uint4 *)(blk + side * kBlock * DP + (tid + 256 * c) * 16);
+                                held[j][side][c] = *(const uint4 *)(blk[j] + side * kBlock * DP + (tid + 256 * c) * 16);
                 }
             }
             if constexpr (CODED)                             // a wave each: of a block's keys, of its values
-                if (lane < kBlock && page[wave & 1] >= 0)
-                    held_scale = ((const float *)(block_of(u, wave & 1, page[wave & 1]) + 2 * kBlock * DP))
-                        [(wave >> 1) * kBlock + lane];
+                if (lane < kBlock)
+                    held_scale = ((const float *)(blk[wave & 1] + 2 * kBlock * DP))[(wave >> 1) * kBlock + lane];
         };
-        auto settle = [&](int buf, const int (&page)[2]) {
+        auto settle = [&](int buf) __attribute__((always_inline)) {
             if constexpr (CODED) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (page[j] < 0)
-                        continue;
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int side = 0; side < 2; ++side)
 #pragma unroll
@@ -870,9 +892,8 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                             *(bf16x8 *)to = frag_of(lo).v;
                             *(bf16x8 *)(to + 16) = frag_of(hi).v;
                         }
-                }
-                if (lane < kBlock)
-                    scales[buf][wave * kBlock + lane] = held_scale;
+                if (lane < kBlock)                           // keys' scales with that of q . k
+                    scales[buf][wave * kBlock + lane] = wave < 2 ? held_scale * a.scale : held_scale;
             }
         };
 
@@ -881,132 +902,153 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
         for (int d = 0; d < ND; ++d)
             o[d] = f32x16{};
         float m = kNone, l = 0;
-        int page[2], next[2], after[2];
-        pages_of(u0, page);
-        fetch(u0, 0, page);
-        settle(0, page);
-        pages_of(u0 + 1, next);
-        int buf = 0;
-        for (int u = u0; u < u1; ++u, buf ^= 1) {
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            fetch(u + 1, buf ^ 1, next);
-            pages_of(u + 2, after);
-            const bool in_pre = u < pre_units;
-            const int tok0 = (in_pre ? u : u - pre_units) * kWideUnit;
-            const int most = in_pre ? t.pre_len : see_max, least = in_pre ? t.pre_len : see_min;
-            const int here = (in_pre ? t.pre_len : see) - tok0;          // tokens of the unit this row sees
-            if (works && tok0 < most) {
-                const char *kb = lds + buf * kBuf, *vb = kb + 2 * kSide;
-                f32x16 st[2] = {};
+        // Raise the maximum to `top` of a lane's scores if it is passed by far.
+        auto raise = [&](float top) __attribute__((always_inline)) {
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+            if (!CODED)
+                top *= a.scale;
+            if (__any(top > m + kRaise)) {
+                const float up = __builtin_fmaxf(m, top);
+                const float f = up == kNone ? 1.f : fexp2(m - up);
+                m = up;
+                l *= f;
 #pragma unroll
-                for (int s = 0; s < NS; ++s)
+                for (int d = 0; d < ND; ++d)
+                    o[d] *= f;
+            }
+            return m == kNone ? 0.f : -m;
+        };
+        // NB blocks of a unit from block j0 on; MASKED: some rows do not see all of their tokens.
+        auto work = [&](auto masked, auto blocks, int u, int buf, int j0) __attribute__((always_inline)) {
+            constexpr bool MASKED = decltype(masked)::value;
+            constexpr int NB = decltype(blocks)::value;
+            const char *kb = lds + buf * kBuf + j0 * kSide, *vb = kb + 2 * kSide;
+            const float *sc = scales[buf] + (CODED ? j0 * kBlock : 0);
+            int here = 0, most = 0;                          // tokens from the block on that this row sees, that any of the wave does
+            if constexpr (MASKED) {
+                const bool in_pre = u < pre_units;
+                const int tok0 = (in_pre ? u : u - pre_units) * kWideUnit + j0 * kBlock;
+                here = (in_pre ? t.pre_len : see) - tok0;
+                most = (in_pre ? t.pre_len : see_wave) - tok0;
+                if (most <= 0)
+                    return;
+            }
+            f32x16 st[NB] = {};
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const F k{*(const bf16x8 *)(kb + j * kSide + ((2 * s + h) * kBlock + ktok) * 16)};
-                        st[j] = mma(k, q[s], st[j]);
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const F k{*(const bf16x8 *)(kb + j * kSide + ((2 * s + h) * kBlock + ktok) * 16)};
+                    st[j] = mma(k, q[s], st[j]);
+                }
+            float top = kNone;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; r += 4) {
+                    if constexpr (CODED)
+                        st[j] = scaled(st[j], r, *(const f32x4 *)&sc[j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7)]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (MASKED && j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7) + i >= here)
+                            st[j][r + i] = kNone;
+                        top = __builtin_fmaxf(top, st[j][r + i]);
                     }
-                const bool part = tok0 + kWideUnit > least || page[0] < 0 || page[1] < 0;
-                float top = kNone;
-                if constexpr (CODED) {
+                }
+            const float off = raise(top);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NB; ++j)
 #pragma unroll
-                        for (int r = 0; r < 16; r += 4) {
-                            const f32x4 ks = *(const f32x4 *)&scales[buf][j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7)];
+                for (int r = 0; r < 16; ++r) {
+                    st[j][r] = fexp2(CODED ? st[j][r] + off : fmaf(st[j][r], a.scale, off));
+                    l += st[j][r];
+                }
+            if constexpr (CODED) {
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; r += 4) {
+                        st[j] = scaled(st[j], r, *(const f32x4 *)&sc[(2 + j) * kBlock + 16 * (r >> 3) + 8 * h + (r & 7)]);
+                        if constexpr (MASKED)                // a hidden token's scale may be NaN
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                st[j][r + i] *= ks[i];
-                        }
-                }
-                if (part) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (page[j] < 0 || j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7) >= here)
-                                st[j][r] = kNone;
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        top = __builtin_fmaxf(top, st[j][r]);
-                top = __builtin_fmaxf(top, __shfl_xor(top, 32)) * a.scale;
-                if (__any(top > m + kRaise)) {
-                    const float up = __builtin_fmaxf(m, top);
-                    const float f = up == kNone ? 1.f : fexp2(m - up);
-                    m = up;
-                    l *= f;
-#pragma unroll
-                    for (int d = 0; d < ND; ++d)
-                        o[d] *= f;
-                }
-                const float off = m == kNone ? 0.f : -m;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        st[j][r] = fexp2(fmaf(st[j][r], a.scale, off));
-                        l += st[j][r];
-                    }
-                if constexpr (CODED) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int r = 0; r < 16; r += 4) {
-                            const f32x4 vs = *(const f32x4 *)&scales[buf][(2 + j) * kBlock + 16 * (r >> 3) + 8 * h + (r & 7)];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (part && (page[j] < 0 || j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7) + i >= here))
+                                if (j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7) + i >= here)
                                     st[j][r + i] = 0.f;
-                                else
-                                    st[j][r + i] *= vs[i];
-                        }
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float p[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            p[i] = st[j][8 * c + i];
-                        const F pf = to_frag(p, T());
-                        if (!part) {
-#pragma unroll
-                            for (int d = 0; d < ND; ++d) {
-                                const F v{*(const bf16x8 *)(vb + j * kSide + ((2 * c + h) * DP + 32 * d + n) * 16)};
-                                o[d] = mma(v, pf, o[d]);
-                            }
-                        } else {
-                            // what no row sees may hold anything
-                            const int first = j * kBlock + 16 * c + 8 * h;
-                            const int keep = page[j] < 0 ? 0 : most - tok0 - first;
-                            float sees[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                sees[i] = first + i < here ? 1.f : 0.f;
-                            const F sf = to_frag(sees, T());
-#pragma unroll
-                            for (int d = 0; d < ND; ++d) {
-                                F v{*(const bf16x8 *)(vb + j * kSide + ((2 * c + h) * DP + 32 * d + n) * 16)};
-                                cut(v, keep);
-                                if constexpr (!CODED)
-                                    if (least < most)
-                                        odd_values<T>(v, sf, o[d]);
-                                o[d] = mma(v, pf, o[d]);
-                            }
-                        }
                     }
             }
-            settle(buf ^ 1, next);
+            F p[2 * NB];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                page[j] = next[j];
+            for (int k = 0; k < 2 * NB; ++k) {
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = st[k >> 1][8 * (k & 1) + i];
+                p[k] = to_frag(v, T());
+            }
+#pragma unroll
+            for (int k = 0; k < 2 * NB; ++k) {
+                const int first = 16 * k + 8 * h;
+                F sees{};
+                if constexpr (MASKED && !CODED)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        sees.v[i] = first + i < here ? 1.f : 0.f;
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    F v{*(const bf16x8 *)(vb + (k >> 1) * kSide + ((2 * (k & 1) + h) * DP + 32 * d + n) * 16)};
+                    if constexpr (MASKED) {                  // what no row sees may hold anything
+                        cut(v, most - first);
+                        if constexpr (!CODED)
+                            odd_values<T>(v, sees, o[d]);
+                    }
+                    o[d] = mma(v, p[k], o[d]);
+                }
+            }
+        };
+
+        int next[2], after[2];
+        pages_of(u0, next);
+        fetch(u0, 0, next);
+        settle(0);
+        pages_of(u0 + 1, next);
+        auto turn = [&](int u) __attribute__((always_inline)) {          // unit u is there, u + 1 on its way
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            if (u + 1 < u1)
+                fetch(u + 1, (u - u0 + 1) & 1, next);
+            pages_of(u + 2, after);
+        };
+        auto pass = [&](int u) __attribute__((always_inline)) {
+            if (u + 1 < u1)
+                settle((u - u0 + 1) & 1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
                 next[j] = after[j];
+        };
+        for (int u = u0; u < u1;) {
+            const int full = u < pre_units ? pre_full : own_full;
+            const int stop = full < u1 ? full : u1;
+            for (; u < stop; ++u) {
+                turn(u);
+                if (works)
+                    work(std::false_type(), std::integral_constant<int, 2>(), u, (u - u0) & 1, 0);
+                pass(u);
+            }
+            if (u < u1) {
+                turn(u);
+                if (works)
+#pragma unroll 1
+                    for (int j = 0; j < 2; ++j)
+                        work(std::true_type(), std::integral_constant<int, 1>(), u, (u - u0) & 1, j);
+                pass(u);
+                ++u;
             }
         }
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (lost) {
+            l = __builtin_nanf("");
+            if (!tid)
+                atomicOr(b.flags, LORA_FLAG_CACHE_PAGE);
+        }
 
         l += __shfl_xor(l, 32);
         const bool whole = t.kept < 0 && u0 == 0 && u1 == t.units;
