@@ -751,9 +751,9 @@ __device__ __forceinline__ f32x16 scaled(f32x16 v, int r, f32x4 f)
 // ---------------------------------------------------------------------------
 // wide tiles: 128 rows, four waves on 32 rows each of a unit of 64 tokens
 
-// A unit's keys and values stand in LDS in the order of the cache, as bf16, twice: the waves read
-// one while the other is filled.  Token and dim operands are 32 lanes of 16 neighbouring bytes,
-// free of bank conflicts.
+// Blocks of 32 tokens stand in LDS in the order of the cache, as bf16, three of keys and three of
+// values in turn: the waves read one while the next are on their way.  Operands are 32 lanes of 16
+// neighbouring bytes, free of bank conflicts.
 template <int KIND, int DP>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(AttendArgs a)
 {
@@ -761,10 +761,10 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
     typedef Frag<T> F;
     constexpr int NS = DP / 16, ND = DP / 32;
     constexpr int kSide = kBlock * DP * 2;                   // bytes of a block's keys, and of its values
-    constexpr int kBuf = 4 * kSide;                          // keys of two blocks, values of two blocks
     constexpr bool CODED = KIND != kCacheNative;
-    __shared__ alignas(16) char lds[2 * kBuf];
-    __shared__ float scales[2][CODED ? 4 * kBlock : 1];      // of two blocks' keys, of their values
+    __shared__ alignas(16) char lds[6 * kSide];              // three blocks of keys, three of values
+    constexpr int kLoads = 2 * kSide / 1024 / 4;             // direct loads of a wave for a block's keys and another's values
+    __shared__ float scales[6][CODED ? kBlock : 1];
     const AttendBatch &b = a.b;
     const int w = worker_of_block();
     const AttendList list = scalar(&b.plan->list[1]);
@@ -817,84 +817,79 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
         const int see_wave = t.shared ? t.len : per + (t.row0 + (works ? wl : 0)) / b.group;
         const int see_min = t.shared ? t.len : per + t.row0 / b.group;
         const int see_max = t.shared ? t.len : per + (t.row0 + t.rows - 1) / b.group;
-        const int pre_units = units_for(t.pre_len, kWideUnit);
-        // units that every row sees whole: those before pre_full, and from pre_units on those before own_full
-        const int pre_full = t.pre_len / kWideUnit, own_full = pre_units + (see_min > 0 ? see_min / kWideUnit : 0);
+        // Blocks of 32 tokens, those of the prefix first: b0..b1-1 are the run's; every row sees whole
+        // those before pre_full, and from pre_end on those before own_full.
+        constexpr int kPer = kWideUnit / kBlock;
+        const int b0 = u0 * kPer, b1 = u1 * kPer, pre_end = units_for(t.pre_len, kWideUnit) * kPer;
+        const int pre_full = t.pre_len / kBlock, own_full = pre_end + (see_min > 0 ? see_min / kBlock : 0);
         const PageTable own_pages = (PageTable)(t.shared ? b.prefix_pages + (int64_t)t.seq * b.prefix_max_pages
                                                          : b.pages + (int64_t)t.seq * b.max_pages);
         const PageTable pre_pages = (PageTable)(b.prefix_pages + (t.pre_len ? (int64_t)t.pre_seq * b.prefix_max_pages : 0));
 
-        // The pages of a unit's two blocks, through the scalar cache: their wait is not the wait of the
-        // loads in flight.  Blocks that no row sees have the cache's first page.
-        auto pages_of = [&](int u, int (&page)[2]) __attribute__((always_inline)) {
-            const bool in_pre = u < pre_units;
-            const int tok0 = (in_pre ? u : u - pre_units) * kWideUnit, most = in_pre ? t.pre_len : see_max;
-            const PageTable pages = in_pre ? pre_pages : own_pages;
-            page[0] = page[1] = 0;
-            if (u < u1 && tok0 < most)
-                page[0] = pages[tok0 >> a.c.page_shift];
-            if (u < u1 && tok0 + kBlock < most)
-                page[1] = a.c.page_shift > 5 ? page[0] : pages[(tok0 + kBlock) >> a.c.page_shift];
+        // A block's page, through the scalar cache: its wait is not the wait of the loads in flight.
+        // Blocks past the run or that no row sees have the cache's first page.
+        auto page_of = [&](int k) __attribute__((always_inline)) {
+            const bool in_pre = k < pre_end;
+            const int tok0 = (in_pre ? k : k - pre_end) * kBlock, most = in_pre ? t.pre_len : see_max;
+            return k < b1 && tok0 < most ? (in_pre ? pre_pages : own_pages)[tok0 >> a.c.page_shift] : 0;
         };
         bool lost = false;                                   // a page was not one of the cache's
-        auto block_of = [&](int u, int j, int page) __attribute__((always_inline)) -> const char * {
+        auto block_of = [&](int k, int page) __attribute__((always_inline)) -> const char * {
             const bool good = (uint32_t)page < (uint32_t)a.c.pages;
             lost |= !good;
-            const int tok0 = (u < pre_units ? u : u - pre_units) * kWideUnit + j * kBlock;
-            const uint64_t p = (uint64_t)(a.c.base + cache_block(a.c, good ? page : 0, head, (tok0 >> 5) & in_page));
+            const uint64_t p = (uint64_t)(a.c.base + cache_block(a.c, good ? page : 0, head, (k < pre_end ? k : k - pre_end) & in_page));
             const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
             return (const char *)((uint64_t)hi << 32 | lo);
         };
-        constexpr int NC = CODED ? (kBlock * DP / 16 + 255) / 256 : 1;   // 16-byte pieces a thread takes of a side
-        uint4 held[2][2][NC];
-        float held_scale;
+        // Places of keys and values in LDS: three blocks each in turn.
         const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
-        // native: straight into LDS; codes: into registers, and from there as bf16
-        auto fetch = [&](int u, int buf, const int (&page)[2]) __attribute__((always_inline)) {
-            const char *blk[2] = {block_of(u, 0, page[0]), block_of(u, 1, page[1])};
+        auto place = [&](int side, int k) __attribute__((always_inline)) { return (3 * side + (k - b0 + 3) % 3) * kSide; };
+        // Keys of block k with the values of the block before it.  Native: straight into LDS, as many
+        // loads from every wave; codes: into registers, and from there as bf16 when they settle.
+        constexpr int NC = CODED ? (kBlock * DP / 16 + 255) / 256 : 1;   // 16-byte pieces a thread takes of a side
+        uint4 held[2][NC];
+        float held_scale[2];
+        auto fetch = [&](int k, int page_k, int page_v) __attribute__((always_inline)) {
+            const char *blk[2] = {block_of(k, page_k), block_of(k - 1, page_v)};
+            if constexpr (!CODED) {
+                constexpr int kPieces = kSide / 1024;
+                const int to[2] = {place(0, k), place(1, k - 1)};
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if constexpr (!CODED) {
-                    constexpr int kPieces = 2 * kSide / 1024;      // of keys and values, which follow each other
+                for (int i = 0; i < kLoads; ++i) {
+                    const int piece = wave + 4 * i, side = piece >= kPieces, at = (piece - side * kPieces) * 1024;
+                    dma16_off(side ? blk[1] : blk[0], (uint32_t)(side * kSide + at + lane * 16),
+                              lds_at + (side ? to[1] : to[0]) + at);
+                }
+            } else {
 #pragma unroll
-                    for (int i = 0; i < (kPieces + 3) / 4; ++i) {
-                        const int k = wave + 4 * i, side = k >= kPieces / 2;
-                        if (kPieces % 4 == 0 || k < kPieces)
-                            dma16_off(blk[j], (uint32_t)(k * 1024 + lane * 16),
-                                      lds_at + buf * kBuf + j * kSide + side * kSide + k * 1024);
-                    }
-                } else {
+                for (int side = 0; side < 2; ++side) {
 #pragma unroll
-                    for (int side = 0; side < 2; ++side)
-#pragma unroll
-                        for (int c = 0; c < NC; ++c)
-                            if (tid + 256 * c < kBlock * DP / 16)
-                                held[j][side][c] = *(const uint4 *)(blk[j] + side * kBlock * DP + (tid + 256 * c) * 16);
+                    for (int c = 0; c < NC; ++c)
+                        if (tid + 256 * c < kBlock * DP / 16)
+                            held[side][c] = *(const uint4 *)(blk[side] + side * kBlock * DP + (tid + 256 * c) * 16);
+                    if (wave == side && lane < kBlock)
+                        held_scale[side] = ((const float *)(blk[side] + 2 * kBlock * DP))[side * kBlock + lane];
                 }
             }
-            if constexpr (CODED)                             // a wave each: of a block's keys, of its values
-                if (lane < kBlock)
-                    held_scale = ((const float *)(blk[wave & 1] + 2 * kBlock * DP))[(wave >> 1) * kBlock + lane];
         };
-        auto settle = [&](int buf) __attribute__((always_inline)) {
-            if constexpr (CODED) {
+        auto settle = [&](int k) __attribute__((always_inline)) {
+            if constexpr (CODED)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int side = 0; side < 2; ++side) {
+                    const int at = place(side, k - side);
 #pragma unroll
-                    for (int side = 0; side < 2; ++side)
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) {
-                            if (tid + 256 * c >= kBlock * DP / 16)
-                                continue;
-                            const uint4 r = held[j][side][c];
-                            char *to = lds + buf * kBuf + (2 * side + j) * kSide + (tid + 256 * c) * 32;
-                            const Held<T, KIND> lo{make_uint2(r.x, r.y)}, hi{make_uint2(r.z, r.w)};
-                            *(bf16x8 *)to = frag_of(lo).v;
-                            *(bf16x8 *)(to + 16) = frag_of(hi).v;
-                        }
-                if (lane < kBlock)                           // keys' scales with that of q . k
-                    scales[buf][wave * kBlock + lane] = wave < 2 ? held_scale * a.scale : held_scale;
-            }
+                    for (int c = 0; c < NC; ++c) {
+                        if (tid + 256 * c >= kBlock * DP / 16)
+                            continue;
+                        const uint4 r = held[side][c];
+                        char *to = lds + at + (tid + 256 * c) * 32;
+                        const Held<T, CODED ? KIND : kCacheInt8> lo{make_uint2(r.x, r.y)}, hi{make_uint2(r.z, r.w)};
+                        *(bf16x8 *)to = frag_of(lo).v;
+                        *(bf16x8 *)(to + 16) = frag_of(hi).v;
+                    }
+                    if (wave == side && lane < kBlock)       // keys' scales with that of q . k
+                        scales[at / kSide][lane] = side ? held_scale[1] : held_scale[0] * a.scale;
+                }
         };
 
         f32x16 o[ND];
@@ -902,8 +897,12 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
         for (int d = 0; d < ND; ++d)
             o[d] = f32x16{};
         float m = kNone, l = 0;
-        // Raise the maximum to `top` of a lane's scores if it is passed by far.
-        auto raise = [&](float top) __attribute__((always_inline)) {
+        // Raise the maximum to a lane's highest score if it is passed by far.
+        auto raise = [&](const f32x16 &st) __attribute__((always_inline)) {
+            float top = kNone;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                top = __builtin_fmaxf(top, st[r]);
             top = __builtin_fmaxf(top, __shfl_xor(top, 32));
             if (!CODED)
                 top *= a.scale;
@@ -916,131 +915,163 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                 for (int d = 0; d < ND; ++d)
                     o[d] *= f;
             }
-            return m == kNone ? 0.f : -m;
         };
-        // NB blocks of a unit from block j0 on; MASKED: some rows do not see all of their tokens.
-        auto work = [&](auto masked, auto blocks, int u, int buf, int j0) __attribute__((always_inline)) {
-            constexpr bool MASKED = decltype(masked)::value;
-            constexpr int NB = decltype(blocks)::value;
-            const char *kb = lds + buf * kBuf + j0 * kSide, *vb = kb + 2 * kSide;
-            const float *sc = scales[buf] + (CODED ? j0 * kBlock : 0);
-            int here = 0, most = 0;                          // tokens from the block on that this row sees, that any of the wave does
-            if constexpr (MASKED) {
-                const bool in_pre = u < pre_units;
-                const int tok0 = (in_pre ? u : u - pre_units) * kWideUnit + j0 * kBlock;
-                here = (in_pre ? t.pre_len : see) - tok0;
-                most = (in_pre ? t.pre_len : see_wave) - tok0;
-                if (most <= 0)
-                    return;
-            }
-            f32x16 st[NB] = {};
+        // Scores of a block: in powers of two for codes (once rescaled), else over the scale.
+        auto scores = [&](int k) __attribute__((always_inline)) {
+            const char *kb = lds + place(0, k);
+            f32x16 st{};
 #pragma unroll
             for (int s = 0; s < NS; ++s)
-#pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    const F k{*(const bf16x8 *)(kb + j * kSide + ((2 * s + h) * kBlock + ktok) * 16)};
-                    st[j] = mma(k, q[s], st[j]);
-                }
-            float top = kNone;
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; r += 4) {
-                    if constexpr (CODED)
-                        st[j] = scaled(st[j], r, *(const f32x4 *)&sc[j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7)]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (MASKED && j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7) + i >= here)
-                            st[j][r + i] = kNone;
-                        top = __builtin_fmaxf(top, st[j][r + i]);
-                    }
-                }
-            const float off = raise(top);
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    st[j][r] = fexp2(CODED ? st[j][r] + off : fmaf(st[j][r], a.scale, off));
-                    l += st[j][r];
-                }
+                st = mma(F{*(const bf16x8 *)(kb + ((2 * s + h) * kBlock + ktok) * 16)}, q[s], st);
+            return st;
+        };
+        auto rescale = [&](f32x16 &st, int side, int k) __attribute__((always_inline)) {
             if constexpr (CODED) {
+                const float *sc = scales[place(side, k) / kSide];
 #pragma unroll
-                for (int j = 0; j < NB; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; r += 4) {
-                        st[j] = scaled(st[j], r, *(const f32x4 *)&sc[(2 + j) * kBlock + 16 * (r >> 3) + 8 * h + (r & 7)]);
-                        if constexpr (MASKED)                // a hidden token's scale may be NaN
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (j * kBlock + 16 * (r >> 3) + 8 * h + (r & 7) + i >= here)
-                                    st[j][r + i] = 0.f;
-                    }
+                for (int r = 0; r < 16; r += 4)
+                    st = scaled(st, r, *(const f32x4 *)&sc[16 * (r >> 3) + 8 * h + (r & 7)]);
             }
-            F p[2 * NB];
+        };
+        auto weights = [&](f32x16 &st) __attribute__((always_inline)) {
+            const float off = m == kNone ? 0.f : -m;
 #pragma unroll
-            for (int k = 0; k < 2 * NB; ++k) {
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = st[k >> 1][8 * (k & 1) + i];
-                p[k] = to_frag(v, T());
+            for (int r = 0; r < 16; ++r) {
+                st[r] = fexp2(CODED ? st[r] + off : fmaf(st[r], a.scale, off));
+                l += st[r];
             }
+        };
+        auto operand = [&](const f32x16 &st, int c) __attribute__((always_inline)) {
+            float v[8];
 #pragma unroll
-            for (int k = 0; k < 2 * NB; ++k) {
-                const int first = 16 * k + 8 * h;
+            for (int i = 0; i < 8; ++i)
+                v[i] = st[8 * c + i];
+            return to_frag(v, T());
+        };
+        auto value = [&](int k, int c, int d) __attribute__((always_inline)) {
+            return F{*(const bf16x8 *)(lds + place(1, k) + ((2 * c + h) * DP + 32 * d + n) * 16)};
+        };
+        auto add_values = [&](const f32x16 &st, int k) __attribute__((always_inline)) {
+            const F p[2] = {operand(st, 0), operand(st, 1)};
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+                    o[d] = mma(value(k, c, d), p[c], o[d]);
+        };
+        // A block of which some rows do not see all tokens.
+        auto edge = [&](int k) __attribute__((always_inline)) {
+            const bool in_pre = k < pre_end;
+            const int tok0 = (in_pre ? k : k - pre_end) * kBlock;
+            const int here = (in_pre ? t.pre_len : see) - tok0;          // tokens from the block on that this row sees
+            const int most = (in_pre ? t.pre_len : see_wave) - tok0;     // that any row of the wave does
+            if (most <= 0)
+                return;
+            f32x16 st = scores(k);
+            rescale(st, 0, k);
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (16 * (r >> 3) + 8 * h + (r & 7) >= here)
+                    st[r] = kNone;
+            raise(st);
+            weights(st);
+            rescale(st, 1, k);
+            if constexpr (CODED)                             // a hidden token's scale may be NaN
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (16 * (r >> 3) + 8 * h + (r & 7) >= here)
+                        st[r] = 0.f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int first = 16 * c + 8 * h;
+                const F p = operand(st, c);
                 F sees{};
-                if constexpr (MASKED && !CODED)
+                if constexpr (!CODED)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         sees.v[i] = first + i < here ? 1.f : 0.f;
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
-                    F v{*(const bf16x8 *)(vb + (k >> 1) * kSide + ((2 * (k & 1) + h) * DP + 32 * d + n) * 16)};
-                    if constexpr (MASKED) {                  // what no row sees may hold anything
-                        cut(v, most - first);
-                        if constexpr (!CODED)
-                            odd_values<T>(v, sees, o[d]);
-                    }
-                    o[d] = mma(v, p[k], o[d]);
+                    F v = value(k, c, d);
+                    cut(v, most - first);                    // what no row sees may hold anything
+                    if constexpr (!CODED)
+                        odd_values<T>(v, sees, o[d]);
+                    o[d] = mma(v, p, o[d]);
                 }
             }
         };
 
-        int next[2], after[2];
-        pages_of(u0, next);
-        fetch(u0, 0, next);
-        settle(0);
-        pages_of(u0 + 1, next);
-        auto turn = [&](int u) __attribute__((always_inline)) {          // unit u is there, u + 1 on its way
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            if (u + 1 < u1)
-                fetch(u + 1, (u - u0 + 1) & 1, next);
-            pages_of(u + 2, after);
+        // At the start of block k its keys (if not used yet) and values and the next one's keys are there,
+        // and one fetch is under way: keys are fetched three blocks ahead, values two.
+        auto wait = [&]() __attribute__((always_inline)) {
+            if constexpr (CODED)
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
         };
-        auto pass = [&](int u) __attribute__((always_inline)) {
-            if (u + 1 < u1)
-                settle((u - u0 + 1) & 1);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                next[j] = after[j];
+        int page2 = page_of(b0 + 2), page3 = page_of(b0 + 3);            // of the blocks two and three on
+        {
+            const int p0 = page_of(b0), p1 = page_of(b0 + 1);
+            fetch(b0, p0, p0);                               // the values are those of no block
+            settle(b0);
+            fetch(b0 + 1, p1, p0);
+            settle(b0 + 1);
+            fetch(b0 + 2, page2, p1);
+            settle(b0 + 2);
+        }
+        auto ahead = [&](int k) __attribute__((always_inline)) {
+            fetch(k + 3, page3, page2);
+            page2 = page3;
+            page3 = page_of(k + 4);
         };
-        for (int u = u0; u < u1;) {
-            const int full = u < pre_units ? pre_full : own_full;
-            const int stop = full < u1 ? full : u1;
-            for (; u < stop; ++u) {
-                turn(u);
+        // A block's weights and values go with the next one's scores, so that a wave has vector work of
+        // its own beside its matrix instructions.
+        auto step = [&](f32x16 &cur, f32x16 &nxt, int k) __attribute__((always_inline)) {
+            wait();                                          // all waves are done with block k's keys
+            ahead(k);
+            nxt = scores(k + 1);
+            weights(cur);
+            rescale(cur, 1, k);
+            rescale(nxt, 0, k + 1);
+            add_values(cur, k);
+            raise(nxt);
+            settle(k + 3);
+        };
+        auto last = [&](f32x16 &cur, int k) __attribute__((always_inline)) {
+            wait();
+            ahead(k);
+            weights(cur);
+            rescale(cur, 1, k);
+            add_values(cur, k);
+            settle(k + 3);
+        };
+        for (int k = b0; k < b1;) {
+            wait();
+            const int full = k < pre_end ? pre_full : own_full;
+            const int stop = full < b1 ? full : b1;
+            if (k < stop) {
+                f32x16 s0 = scores(k), s1;
+                rescale(s0, 0, k);
+                raise(s0);
+                for (;;) {
+                    if (k + 1 == stop) {
+                        last(s0, k++);
+                        break;
+                    }
+                    step(s0, s1, k++);
+                    if (k + 1 == stop) {
+                        last(s1, k++);
+                        break;
+                    }
+                    step(s1, s0, k++);
+                }
+            } else {
                 if (works)
-                    work(std::false_type(), std::integral_constant<int, 2>(), u, (u - u0) & 1, 0);
-                pass(u);
-            }
-            if (u < u1) {
-                turn(u);
-                if (works)
-#pragma unroll 1
-                    for (int j = 0; j < 2; ++j)
-                        work(std::true_type(), std::integral_constant<int, 1>(), u, (u - u0) & 1, j);
-                pass(u);
-                ++u;
+                    edge(k);
+                asm volatile("s_barrier" ::: "memory");      // its keys' place is free
+                ahead(k);
+                settle(k + 3);
+                ++k;
             }
         }
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
