@@ -764,7 +764,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
     constexpr bool CODED = KIND != kCacheNative;
     __shared__ alignas(16) char lds[6 * kSide];              // three blocks of keys, three of values
     constexpr int kLoads = 2 * kSide / 1024 / 4;             // direct loads of a wave for a block's keys and another's values
-    __shared__ float scales[6][CODED ? kBlock : 1];
+    __shared__ float scales[2][3][CODED ? kBlock : 1];
     const AttendBatch &b = a.b;
     const int w = worker_of_block();
     const AttendList list = scalar(&b.plan->list[1]);
@@ -822,73 +822,86 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
         constexpr int kPer = kWideUnit / kBlock;
         const int b0 = u0 * kPer, b1 = u1 * kPer, pre_end = units_for(t.pre_len, kWideUnit) * kPer;
         const int pre_full = t.pre_len / kBlock, own_full = pre_end + (see_min > 0 ? see_min / kBlock : 0);
-        const PageTable own_pages = (PageTable)(t.shared ? b.prefix_pages + (int64_t)t.seq * b.prefix_max_pages
-                                                         : b.pages + (int64_t)t.seq * b.max_pages);
-        const PageTable pre_pages = (PageTable)(b.prefix_pages + (t.pre_len ? (int64_t)t.pre_seq * b.prefix_max_pages : 0));
+        const int32_t *own_pages = t.shared ? b.prefix_pages + (int64_t)t.seq * b.prefix_max_pages
+                                            : b.pages + (int64_t)t.seq * b.max_pages;
+        const int32_t *pre_pages = b.prefix_pages + (t.pre_len ? (int64_t)t.pre_seq * b.prefix_max_pages : 0);
 
-        // A block's page, through the scalar cache: its wait is not the wait of the loads in flight.
-        // Blocks past the run or that no row sees have the cache's first page.
-        auto page_of = [&](int k) __attribute__((always_inline)) {
-            const bool in_pre = k < pre_end;
-            const int tok0 = (in_pre ? k : k - pre_end) * kBlock, most = in_pre ? t.pre_len : see_max;
-            return k < b1 && tok0 < most ? (in_pre ? pre_pages : own_pages)[tok0 >> a.c.page_shift] : 0;
-        };
+        // Where blocks are: each lane holds the address of one, 64 at a time, so that the loop has no
+        // address to form and no load to wait for.  Blocks past the run or that no row sees have the
+        // cache's first page.
         bool lost = false;                                   // a page was not one of the cache's
-        auto block_of = [&](int k, int page) __attribute__((always_inline)) -> const char * {
+        uint32_t far_lo = 0, far_hi = 0;
+        int far0 = 0;
+        auto look = [&](int k) __attribute__((always_inline)) {
+            far0 = k;
+            const int kk = k + lane;
+            const bool in_pre = kk < pre_end;
+            const int blk = in_pre ? kk : kk - pre_end, most = in_pre ? t.pre_len : see_max;
+            int page = 0;
+            if (kk < b1 && blk < units_for(most > 0 ? most : 0, kBlock))
+                page = (in_pre ? pre_pages : own_pages)[blk >> (a.c.page_shift - 5)];
             const bool good = (uint32_t)page < (uint32_t)a.c.pages;
-            lost |= !good;
-            const uint64_t p = (uint64_t)(a.c.base + cache_block(a.c, good ? page : 0, head, (k < pre_end ? k : k - pre_end) & in_page));
-            const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p), hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+            lost |= __any(!good);
+            const uint64_t p = (uint64_t)(a.c.base + cache_block(a.c, good ? page : 0, head, blk & in_page));
+            far_lo = (uint32_t)p;
+            far_hi = (uint32_t)(p >> 32);
+        };
+        auto block_of = [&](int k) __attribute__((always_inline)) -> const char * {
+            if (k - far0 >= 64)
+                look(k);
+            const uint32_t lo = __builtin_amdgcn_readlane(far_lo, k - far0), hi = __builtin_amdgcn_readlane(far_hi, k - far0);
             return (const char *)((uint64_t)hi << 32 | lo);
         };
-        // Places of keys and values in LDS: three blocks each in turn.
+        // Places of the blocks k, k + 1 and k + 2 in LDS, three in turn; the fourth takes the first's.
         const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
-        auto place = [&](int side, int k) __attribute__((always_inline)) { return (3 * side + (k - b0 + 3) % 3) * kSide; };
-        // Keys of block k with the values of the block before it.  Native: straight into LDS, as many
+        int at0 = 0, at1 = kSide, at2 = 2 * kSide;
+        constexpr int kValues = 3 * kSide;                   // values behind the keys
+        // Keys of a block with the values of the block before it.  Native: straight into LDS, as many
         // loads from every wave; codes: into registers, and from there as bf16 when they settle.
         constexpr int NC = CODED ? (kBlock * DP / 16 + 255) / 256 : 1;   // 16-byte pieces a thread takes of a side
         uint4 held[2][NC];
         float held_scale[2];
-        auto fetch = [&](int k, int page_k, int page_v) __attribute__((always_inline)) {
-            const char *blk[2] = {block_of(k, page_k), block_of(k - 1, page_v)};
+        auto fetch = [&](const char *keys, const char *values, int key_at, int value_at) __attribute__((always_inline)) {
             if constexpr (!CODED) {
                 constexpr int kPieces = kSide / 1024;
-                const int to[2] = {place(0, k), place(1, k - 1)};
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i) {
-                    const int piece = wave + 4 * i, side = piece >= kPieces, at = (piece - side * kPieces) * 1024;
-                    dma16_off(side ? blk[1] : blk[0], (uint32_t)(side * kSide + at + lane * 16),
-                              lds_at + (side ? to[1] : to[0]) + at);
+                    const int piece = wave + 4 * i;
+                    const int side = kPieces % 4 ? piece >= kPieces : 4 * i >= kPieces, at = (piece - side * kPieces) * 1024;
+                    dma16_off(side ? values : keys, (uint32_t)(side * kSide + at + lane * 16),
+                              lds_at + (side ? kValues + value_at : key_at) + at);
                 }
             } else {
 #pragma unroll
                 for (int side = 0; side < 2; ++side) {
+                    const char *blk = side ? values : keys;
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
                         if (tid + 256 * c < kBlock * DP / 16)
-                            held[side][c] = *(const uint4 *)(blk[side] + side * kBlock * DP + (tid + 256 * c) * 16);
+                            held[side][c] = *(const uint4 *)(blk + side * kBlock * DP + (tid + 256 * c) * 16);
                     if (wave == side && lane < kBlock)
-                        held_scale[side] = ((const float *)(blk[side] + 2 * kBlock * DP))[side * kBlock + lane];
+                        held_scale[side] = ((const float *)(blk + 2 * kBlock * DP))[side * kBlock + lane];
                 }
             }
         };
-        auto settle = [&](int k) __attribute__((always_inline)) {
+        auto settle = [&](int key_at, int value_at) __attribute__((always_inline)) {
             if constexpr (CODED)
 #pragma unroll
                 for (int side = 0; side < 2; ++side) {
-                    const int at = place(side, k - side);
+                    const int at = side ? value_at : key_at;
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         if (tid + 256 * c >= kBlock * DP / 16)
                             continue;
                         const uint4 r = held[side][c];
-                        char *to = lds + at + (tid + 256 * c) * 32;
+                        char *to = lds + side * kValues + at + (tid + 256 * c) * 32;
                         const Held<T, CODED ? KIND : kCacheInt8> lo{make_uint2(r.x, r.y)}, hi{make_uint2(r.z, r.w)};
                         *(bf16x8 *)to = frag_of(lo).v;
                         *(bf16x8 *)(to + 16) = frag_of(hi).v;
                     }
-                    if (wave == side && lane < kBlock)       // keys' scales with that of q . k
-                        scales[at / kSide][lane] = side ? held_scale[1] : held_scale[0] * a.scale;
+                    // keys' scales with that of q . k
+                    if (wave == side && lane < kBlock)
+                        scales[side][at / kSide][lane] = side ? held_scale[1] : held_scale[0] * a.scale;
                 }
         };
 
@@ -903,7 +916,8 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 top = __builtin_fmaxf(top, st[r]);
-            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+            const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+            top = __builtin_fmaxf(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
             if (!CODED)
                 top *= a.scale;
             if (__any(top > m + kRaise)) {
@@ -917,17 +931,17 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
             }
         };
         // Scores of a block: in powers of two for codes (once rescaled), else over the scale.
-        auto scores = [&](int k) __attribute__((always_inline)) {
-            const char *kb = lds + place(0, k);
+        auto scores = [&](int at) __attribute__((always_inline)) {
+            const char *kb = lds + at;
             f32x16 st{};
 #pragma unroll
             for (int s = 0; s < NS; ++s)
                 st = mma(F{*(const bf16x8 *)(kb + ((2 * s + h) * kBlock + ktok) * 16)}, q[s], st);
             return st;
         };
-        auto rescale = [&](f32x16 &st, int side, int k) __attribute__((always_inline)) {
+        auto rescale = [&](f32x16 &st, int side, int at) __attribute__((always_inline)) {
             if constexpr (CODED) {
-                const float *sc = scales[place(side, k) / kSide];
+                const float *sc = scales[side][at / kSide];
 #pragma unroll
                 for (int r = 0; r < 16; r += 4)
                     st = scaled(st, r, *(const f32x4 *)&sc[16 * (r >> 3) + 8 * h + (r & 7)]);
@@ -948,16 +962,57 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                 v[i] = st[8 * c + i];
             return to_frag(v, T());
         };
-        auto value = [&](int k, int c, int d) __attribute__((always_inline)) {
-            return F{*(const bf16x8 *)(lds + place(1, k) + ((2 * c + h) * DP + 32 * d + n) * 16)};
+        auto value = [&](int c, int d) __attribute__((always_inline)) {
+            return F{*(const bf16x8 *)(lds + kValues + at0 + ((2 * c + h) * DP + 32 * d + n) * 16)};
         };
-        auto add_values = [&](const f32x16 &st, int k) __attribute__((always_inline)) {
+        auto add_values = [&](const f32x16 &st) __attribute__((always_inline)) {
             const F p[2] = {operand(st, 0), operand(st, 1)};
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
-                    o[d] = mma(value(k, c, d), p[c], o[d]);
+                    o[d] = mma(value(c, d), p[c], o[d]);
+        };
+        // Block k's weights and values with block k + 1's scores, laid out by hand: a fourth of the operands
+        // ahead of the matrix instructions, and vector work behind each of those, which runs beside it.
+        auto both = [&](f32x16 &cur) __attribute__((always_inline)) {
+            constexpr int kAhead = 4;
+            const char *kb = lds + at1;
+            const float off = m == kNone ? 0.f : -m;
+            auto key = [&](int s) { return F{*(const bf16x8 *)(kb + ((2 * s + h) * kBlock + ktok) * 16)}; };
+            F x[kAhead];
+#pragma unroll
+            for (int s = 0; s < kAhead; ++s)
+                x[s] = key(s);
+            f32x16 nxt{};
+            F p[2];
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                __builtin_amdgcn_sched_barrier(0);
+                nxt = mma(x[s % kAhead], q[s], nxt);
+                x[s % kAhead] = s + kAhead < NS ? key(s + kAhead)
+                                                : value((s + kAhead - NS) / ND, (s + kAhead - NS) % ND);
+#pragma unroll
+                for (int r = 16 * s / NS; r < 16 * (s + 1) / NS; ++r) {
+                    cur[r] = fexp2(CODED ? cur[r] + off : fmaf(cur[r], a.scale, off));
+                    l += cur[r];
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            rescale(cur, 1, at0);
+            rescale(nxt, 0, at1);
+            p[0] = operand(cur, 0);
+            p[1] = operand(cur, 1);
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                const int at = (NS + i) % kAhead;
+                o[i % ND] = mma(x[at], p[i / ND], o[i % ND]);
+                if (i + kAhead < NS)
+                    x[at] = value((i + kAhead) / ND, (i + kAhead) % ND);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            return nxt;
         };
         // A block of which some rows do not see all tokens.
         auto edge = [&](int k) __attribute__((always_inline)) {
@@ -967,15 +1022,15 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
             const int most = (in_pre ? t.pre_len : see_wave) - tok0;     // that any row of the wave does
             if (most <= 0)
                 return;
-            f32x16 st = scores(k);
-            rescale(st, 0, k);
+            f32x16 st = scores(at0);
+            rescale(st, 0, at0);
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 if (16 * (r >> 3) + 8 * h + (r & 7) >= here)
                     st[r] = kNone;
             raise(st);
             weights(st);
-            rescale(st, 1, k);
+            rescale(st, 1, at0);
             if constexpr (CODED)                             // a hidden token's scale may be NaN
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
@@ -992,7 +1047,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                         sees.v[i] = first + i < here ? 1.f : 0.f;
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
-                    F v = value(k, c, d);
+                    F v = value(c, d);
                     cut(v, most - first);                    // what no row sees may hold anything
                     if constexpr (!CODED)
                         odd_values<T>(v, sees, o[d]);
@@ -1009,68 +1064,57 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
             else
                 asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
         };
-        int page2 = page_of(b0 + 2), page3 = page_of(b0 + 3);            // of the blocks two and three on
-        {
-            const int p0 = page_of(b0), p1 = page_of(b0 + 1);
-            fetch(b0, p0, p0);                               // the values are those of no block
-            settle(b0);
-            fetch(b0 + 1, p1, p0);
-            settle(b0 + 1);
-            fetch(b0 + 2, page2, p1);
-            settle(b0 + 2);
-        }
+        look(b0);
+        const char *before = block_of(b0), *behind;          // of the block two on
+        fetch(before, before, at0, at2);                     // the values are of no block
+        settle(at0, at2);
+        behind = block_of(b0 + 1);
+        fetch(behind, before, at1, at0);
+        settle(at1, at0);
+        before = behind;
+        behind = block_of(b0 + 2);
+        fetch(behind, before, at2, at1);
+        settle(at2, at1);
         auto ahead = [&](int k) __attribute__((always_inline)) {
-            fetch(k + 3, page3, page2);
-            page2 = page3;
-            page3 = page_of(k + 4);
+            before = behind;
+            behind = block_of(k + 3);
+            fetch(behind, before, at0, at2);
         };
-        // A block's weights and values go with the next one's scores, so that a wave has vector work of
-        // its own beside its matrix instructions.
-        auto step = [&](f32x16 &cur, f32x16 &nxt, int k) __attribute__((always_inline)) {
-            wait();                                          // all waves are done with block k's keys
-            ahead(k);
-            nxt = scores(k + 1);
-            weights(cur);
-            rescale(cur, 1, k);
-            rescale(nxt, 0, k + 1);
-            add_values(cur, k);
-            raise(nxt);
-            settle(k + 3);
-        };
-        auto last = [&](f32x16 &cur, int k) __attribute__((always_inline)) {
-            wait();
-            ahead(k);
-            weights(cur);
-            rescale(cur, 1, k);
-            add_values(cur, k);
-            settle(k + 3);
+        auto pass = [&]() __attribute__((always_inline)) {
+            settle(at0, at2);
+            const int first = at0;
+            at0 = at1;
+            at1 = at2;
+            at2 = first;
         };
         for (int k = b0; k < b1;) {
             wait();
             const int full = k < pre_end ? pre_full : own_full;
             const int stop = full < b1 ? full : b1;
             if (k < stop) {
-                f32x16 s0 = scores(k), s1;
-                rescale(s0, 0, k);
-                raise(s0);
-                for (;;) {
-                    if (k + 1 == stop) {
-                        last(s0, k++);
-                        break;
-                    }
-                    step(s0, s1, k++);
-                    if (k + 1 == stop) {
-                        last(s1, k++);
-                        break;
-                    }
-                    step(s1, s0, k++);
+                f32x16 cur = scores(at0);
+                rescale(cur, 0, at0);
+                raise(cur);
+                for (; k + 1 < stop; ++k) {
+                    wait();                                  // all waves are done with block k's keys
+                    ahead(k);
+                    cur = both(cur);
+                    raise(cur);
+                    pass();
                 }
+                wait();
+                ahead(k);
+                weights(cur);
+                rescale(cur, 1, at0);
+                add_values(cur);
+                pass();
+                ++k;
             } else {
                 if (works)
                     edge(k);
                 asm volatile("s_barrier" ::: "memory");      // its keys' place is free
                 ahead(k);
-                settle(k + 3);
+                pass();
                 ++k;
             }
         }
