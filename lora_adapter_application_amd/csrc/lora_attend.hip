@@ -479,6 +479,13 @@ __device__ __forceinline__ P scalar(const P *p)
     return r;
 }
 
+__device__ __forceinline__ const char *scalar_address(const char *p)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)(uint64_t)p);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)p >> 32));
+    return (const char *)((uint64_t)hi << 32 | lo);
+}
+
 // Workgroups of one XCD take neighbouring runs: tiles of one prefix or request, and so the pages
 // they read, stay in one L2.
 __device__ __forceinline__ int worker_of_block() { return (blockIdx.x & 7) * (kAttendWorkers / 8) + (blockIdx.x >> 3); }
@@ -762,9 +769,12 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
     constexpr int NS = DP / 16, ND = DP / 32;
     constexpr int kSide = kBlock * DP * 2;                   // bytes of a block's keys, and of its values
     constexpr bool CODED = KIND != kCacheNative;
-    __shared__ alignas(16) char lds[6 * kSide];              // three blocks of keys, three of values
-    constexpr int kLoads = 2 * kSide / 1024 / 4;             // direct loads of a wave for a block's keys and another's values
-    __shared__ float scales[2][3][CODED ? kBlock : 1];
+    constexpr int kCodes = CODED ? kBlock * DP : kSide;      // of them as the cache holds them
+    constexpr int kRaw = 6 * kSide, kScales = kRaw + (CODED ? 6 * kCodes : 0);
+    // three blocks of keys, three of values; three of their codes, the scales of eight
+    __shared__ alignas(16) char lds[kScales + (CODED ? 8 * 2 * kBlock * 4 : 0)];
+    // direct loads of a wave for a block's keys and another's values
+    constexpr int kLoads = (2 * kCodes / 1024 + 3) / 4 + (CODED ? 1 : 0);
     const AttendBatch &b = a.b;
     const int w = worker_of_block();
     const AttendList list = scalar(&b.plan->list[1]);
@@ -856,53 +866,53 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
         const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
         int at0 = 0, at1 = kSide, at2 = 2 * kSide;
         constexpr int kValues = 3 * kSide;                   // values behind the keys
-        // Keys of a block with the values of the block before it.  Native: straight into LDS, as many
-        // loads from every wave; codes: into registers, and from there as bf16 when they settle.
-        constexpr int NC = CODED ? (kBlock * DP / 16 + 255) / 256 : 1;   // 16-byte pieces a thread takes of a side
-        uint4 held[2][NC];
-        float held_scale[2];
-        auto fetch = [&](const char *keys, const char *values, int key_at, int value_at) __attribute__((always_inline)) {
-            if constexpr (!CODED) {
-                constexpr int kPieces = kSide / 1024;
+        // Keys of block k with the values of the block before it, straight into LDS, as many loads from
+        // every wave.  Codes go to a place of their own, three in turn too, with the scales of block k;
+        // they become bf16 two blocks later.
+        int raw0 = kRaw, raw1 = kRaw + 2 * kCodes, raw2 = kRaw + 4 * kCodes;
+        auto fetch = [&](int k, const char *keys, const char *values, int key_to, int value_to) __attribute__((always_inline)) {
+            constexpr int kPieces = kCodes / 1024;
+            keys = scalar_address(keys);
+            values = scalar_address(values);
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int piece = wave + 4 * i;
-                    const int side = kPieces % 4 ? piece >= kPieces : 4 * i >= kPieces, at = (piece - side * kPieces) * 1024;
-                    dma16_off(side ? values : keys, (uint32_t)(side * kSide + at + lane * 16),
-                              lds_at + (side ? kValues + value_at : key_at) + at);
-                }
-            } else {
-#pragma unroll
-                for (int side = 0; side < 2; ++side) {
-                    const char *blk = side ? values : keys;
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        if (tid + 256 * c < kBlock * DP / 16)
-                            held[side][c] = *(const uint4 *)(blk + side * kBlock * DP + (tid + 256 * c) * 16);
-                    if (wave == side && lane < kBlock)
-                        held_scale[side] = ((const float *)(blk + 2 * kBlock * DP))[side * kBlock + lane];
-                }
+            for (int i = 0; i < (2 * kPieces + 3) / 4; ++i) {
+                // a wave without a piece of its own fetches another's again
+                const int any = wave + 4 * i, piece = 2 * kPieces % 4 && any >= 2 * kPieces ? 2 * kPieces - 1 : any;
+                const int side = kPieces % 4 ? piece >= kPieces : 4 * i >= kPieces, at = (piece - side * kPieces) * 1024;
+                dma16_off(side ? values : keys, (uint32_t)(side * kCodes + at + lane * 16),
+                          lds_at + (side ? value_to : key_to) + at);
             }
+            if constexpr (CODED)
+                dma4_off(keys, (uint32_t)(2 * kCodes + lane * 4), lds_at + kScales + (k & 7) * 2 * kBlock * 4);
         };
-        auto settle = [&](int key_at, int value_at) __attribute__((always_inline)) {
+        // Codes at a place become keys and values in bf16.
+        constexpr int NC = (kBlock * DP / 16 + 255) / 256;   // 16-byte pieces a thread takes of a side
+        struct Held16 { uint4 r[2][NC]; };
+        auto pick = [&](int from) __attribute__((always_inline)) {
+            Held16 x;
             if constexpr (CODED)
 #pragma unroll
-                for (int side = 0; side < 2; ++side) {
-                    const int at = side ? value_at : key_at;
+                for (int side = 0; side < 2; ++side)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        if (NC * 256 == kBlock * DP / 16 || tid + 256 * c < kBlock * DP / 16)
+                            x.r[side][c] = *(const uint4 *)(lds + from + side * kCodes + (tid + 256 * c) * 16);
+            return x;
+        };
+        auto settle = [&](const Held16 &x, int key_to, int value_to) __attribute__((always_inline)) {
+            if constexpr (CODED)
+#pragma unroll
+                for (int side = 0; side < 2; ++side)
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        if (tid + 256 * c >= kBlock * DP / 16)
+                        if (NC * 256 != kBlock * DP / 16 && tid + 256 * c >= kBlock * DP / 16)
                             continue;
-                        const uint4 r = held[side][c];
-                        char *to = lds + side * kValues + at + (tid + 256 * c) * 32;
+                        const uint4 r = x.r[side][c];
+                        char *to = lds + (side ? value_to : key_to) + (tid + 256 * c) * 32;
                         const Held<T, CODED ? KIND : kCacheInt8> lo{make_uint2(r.x, r.y)}, hi{make_uint2(r.z, r.w)};
                         *(bf16x8 *)to = frag_of(lo).v;
                         *(bf16x8 *)(to + 16) = frag_of(hi).v;
                     }
-                    // keys' scales with that of q . k
-                    if (wave == side && lane < kBlock)
-                        scales[side][at / kSide][lane] = side ? held_scale[1] : held_scale[0] * a.scale;
-                }
         };
 
         f32x16 o[ND];
@@ -918,8 +928,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                 top = __builtin_fmaxf(top, st[r]);
             const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
             top = __builtin_fmaxf(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
-            if (!CODED)
-                top *= a.scale;
+            top *= a.scale;
             if (__any(top > m + kRaise)) {
                 const float up = __builtin_fmaxf(m, top);
                 const float f = up == kNone ? 1.f : fexp2(m - up);
@@ -930,7 +939,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                     o[d] *= f;
             }
         };
-        // Scores of a block: in powers of two for codes (once rescaled), else over the scale.
+        // Scores of a block, over the scale of q . k; of codes once rescaled.
         auto scores = [&](int at) __attribute__((always_inline)) {
             const char *kb = lds + at;
             f32x16 st{};
@@ -939,9 +948,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                 st = mma(F{*(const bf16x8 *)(kb + ((2 * s + h) * kBlock + ktok) * 16)}, q[s], st);
             return st;
         };
-        auto rescale = [&](f32x16 &st, int side, int at) __attribute__((always_inline)) {
+        auto rescale = [&](f32x16 &st, int side, int k) __attribute__((always_inline)) {
             if constexpr (CODED) {
-                const float *sc = scales[side][at / kSide];
+                const float *sc = (const float *)(lds + kScales) + ((k & 7) * 2 + side) * kBlock;
 #pragma unroll
                 for (int r = 0; r < 16; r += 4)
                     st = scaled(st, r, *(const f32x4 *)&sc[16 * (r >> 3) + 8 * h + (r & 7)]);
@@ -951,7 +960,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
             const float off = m == kNone ? 0.f : -m;
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                st[r] = fexp2(CODED ? st[r] + off : fmaf(st[r], a.scale, off));
+                st[r] = fexp2(fmaf(st[r], a.scale, off));
                 l += st[r];
             }
         };
@@ -975,7 +984,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
         };
         // Block k's weights and values with block k + 1's scores, laid out by hand: a fourth of the operands
         // ahead of the matrix instructions, and vector work behind each of those, which runs beside it.
-        auto both = [&](f32x16 &cur) __attribute__((always_inline)) {
+        auto both = [&](f32x16 &cur, int k) __attribute__((always_inline)) {
             constexpr int kAhead = 4;
             const char *kb = lds + at1;
             const float off = m == kNone ? 0.f : -m;
@@ -994,13 +1003,13 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                                                 : value((s + kAhead - NS) / ND, (s + kAhead - NS) % ND);
 #pragma unroll
                 for (int r = 16 * s / NS; r < 16 * (s + 1) / NS; ++r) {
-                    cur[r] = fexp2(CODED ? cur[r] + off : fmaf(cur[r], a.scale, off));
+                    cur[r] = fexp2(fmaf(cur[r], a.scale, off));
                     l += cur[r];
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
-            rescale(cur, 1, at0);
-            rescale(nxt, 0, at1);
+            rescale(cur, 1, k);
+            rescale(nxt, 0, k + 1);
             p[0] = operand(cur, 0);
             p[1] = operand(cur, 1);
 #pragma unroll
@@ -1023,14 +1032,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
             if (most <= 0)
                 return;
             f32x16 st = scores(at0);
-            rescale(st, 0, at0);
+            rescale(st, 0, k);
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 if (16 * (r >> 3) + 8 * h + (r & 7) >= here)
                     st[r] = kNone;
             raise(st);
             weights(st);
-            rescale(st, 1, at0);
+            rescale(st, 1, k);
             if constexpr (CODED)                             // a hidden token's scale may be NaN
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
@@ -1059,33 +1068,46 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
         // At the start of block k its keys (if not used yet) and values and the next one's keys are there,
         // and one fetch is under way: keys are fetched three blocks ahead, values two.
         auto wait = [&]() __attribute__((always_inline)) {
-            if constexpr (CODED)
-                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            else
-                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kLoads) : "memory");
         };
         look(b0);
-        const char *before = block_of(b0), *behind;          // of the block two on
-        fetch(before, before, at0, at2);                     // the values are of no block
-        settle(at0, at2);
-        behind = block_of(b0 + 1);
-        fetch(behind, before, at1, at0);
-        settle(at1, at0);
-        before = behind;
-        behind = block_of(b0 + 2);
-        fetch(behind, before, at2, at1);
-        settle(at2, at1);
-        auto ahead = [&](int k) __attribute__((always_inline)) {
+        const char *before = block_of(b0), *behind = before; // of the last two blocks fetched
+        auto next = [&](int k) __attribute__((always_inline)) {
             before = behind;
-            behind = block_of(k + 3);
-            fetch(behind, before, at0, at2);
+            behind = block_of(k);
         };
-        auto pass = [&]() __attribute__((always_inline)) {
-            settle(at0, at2);
-            const int first = at0;
+        fetch(b0, behind, before, CODED ? raw0 : at0, CODED ? raw0 + kCodes : kValues + at2);   // the values are of no block
+        next(b0 + 1);
+        fetch(b0 + 1, behind, before, CODED ? raw1 : at1, CODED ? raw1 + kCodes : kValues + at0);
+        next(b0 + 2);
+        fetch(b0 + 2, behind, before, CODED ? raw2 : at2, CODED ? raw2 + kCodes : kValues + at1);
+        if constexpr (CODED) {
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            settle(pick(raw0), at0, kValues + at2);
+            settle(pick(raw1), at1, kValues + at0);
+            settle(pick(raw2), at2, kValues + at1);
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            next(b0 + 3);
+            fetch(b0 + 3, behind, before, raw0, raw0 + kCodes);
+            next(b0 + 4);
+            fetch(b0 + 4, behind, before, raw1, raw1 + kCodes);
+        }
+        // Block k's place goes to block k + 3's keys, and codes two further.
+        auto ahead = [&](int k) __attribute__((always_inline)) {
+            next(k + (CODED ? 5 : 3));
+            fetch(k + 5, behind, before, CODED ? raw2 : at0, CODED ? raw2 + kCodes : kValues + at2);
+            return pick(raw0);
+        };
+        auto pass = [&](const Held16 &x) __attribute__((always_inline)) {
+            settle(x, at0, kValues + at2);
+            int first = at0;
             at0 = at1;
             at1 = at2;
             at2 = first;
+            first = raw0;
+            raw0 = raw1;
+            raw1 = raw2;
+            raw2 = first;
         };
         for (int k = b0; k < b1;) {
             wait();
@@ -1093,28 +1115,29 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
             const int stop = full < b1 ? full : b1;
             if (k < stop) {
                 f32x16 cur = scores(at0);
-                rescale(cur, 0, at0);
+                rescale(cur, 0, k);
                 raise(cur);
                 for (; k + 1 < stop; ++k) {
                     wait();                                  // all waves are done with block k's keys
-                    ahead(k);
-                    cur = both(cur);
+                    const Held16 x = ahead(k);
+                    __builtin_amdgcn_s_setprio(1);           // before the other workgroup's wave and its softmax
+                    cur = both(cur, k);
+                    __builtin_amdgcn_s_setprio(0);
                     raise(cur);
-                    pass();
+                    pass(x);
                 }
                 wait();
-                ahead(k);
+                const Held16 x = ahead(k);
                 weights(cur);
-                rescale(cur, 1, at0);
+                rescale(cur, 1, k);
                 add_values(cur);
-                pass();
+                pass(x);
                 ++k;
             } else {
                 if (works)
                     edge(k);
                 asm volatile("s_barrier" ::: "memory");      // its keys' place is free
-                ahead(k);
-                pass();
+                pass(ahead(k));
                 ++k;
             }
         }
