@@ -381,6 +381,8 @@ int do_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads, c
     b.kv_heads = v.kv_heads;
     b.page_shift = v.page_shift;
     b.wide = ctx->dtype == LORA_BF16;
+    b.workers[0] = kAttendCus * kAttendPerCu(ctx->elem, v.kind, v.dp);
+    b.workers[1] = kAttendCus * (v.dp <= 128 ? 2 : 1);
     b.flags = ctx->ws.plan.flags;
     if (b.n_tokens && b.n_seqs) {
         int64_t cap[2], kept[2];

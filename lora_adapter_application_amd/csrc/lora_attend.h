@@ -84,7 +84,13 @@ constexpr int kWideRows = 128, kWideUnit = 64;
 // A request of more rows than this (of one key-value head) goes by itself over its prefix:
 // its tiles are as wide as the shared ones, so sharing would save nothing and cost the parts.
 constexpr int kShareRows = 32;
-constexpr int kAttendWorkers = 512;      // two workgroups of 256 threads on each of 256 CUs
+// Workers are the workgroups of 256 threads that the chip's 256 CUs hold at once: as many of a
+// kernel on a CU as its registers and LDS leave room for.
+constexpr int kAttendCus = 256, kAttendWorkers = 4 * kAttendCus;   // at most
+constexpr int kAttendPerCu(int elem, int kind, int dp)             // narrow tiles
+{
+    return dp > 128 ? 1 : elem == 4 || (kind == 0 && dp > 64) ? 2 : 3;
+}
 
 struct AttendTile {
     int32_t seq;                 // request, or prefix if `shared`
@@ -126,12 +132,13 @@ struct AttendBatch {
     int32_t kv_heads;
     int32_t page_shift;
     int32_t wide;                // wide tiles may be used
+    int32_t workers[2];          // of the lists' kernels
     // workspace, all written by the plan
     AttendPlan *plan;
     AttendTile *tiles[2];
     int32_t cap[2];              // tiles a list can hold
     int32_t kept_cap[2];         // kept tiles a list can hold
-    int32_t *start[2];           // [kAttendWorkers] tile at which a worker starts
+    int32_t *start[2];           // [workers] tile at which a worker starts
     int32_t *list_before;        // [n_seqs + 1] listed tokens (of requests that share) before a request
     int32_t *listed;             // [n_tokens] those tokens
     PrefixTile *prefix_tile;     // [n_prefixes]

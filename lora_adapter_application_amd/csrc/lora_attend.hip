@@ -24,8 +24,6 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 
-typedef const __attribute__((address_space(4))) int32_t *PageTable;   // read through the scalar cache
-
 constexpr float kRaise = 8.f;        // a maximum is raised when a score passes it by 2^8
 #define kNone (-__builtin_inff())
 
@@ -64,7 +62,6 @@ __device__ __forceinline__ int32_t wave_scan(int32_t v)
     return v;
 }
 
-static_assert(2 * kAttendWorkers == kPlanThreads, "a thread finds a worker's start");
 // A barrier behind which the workgroup sees its writes to LDS; unlike __syncthreads it does not wait
 // for writes to memory, about 1 us each.
 __device__ __forceinline__ void lds_sync()
@@ -267,13 +264,15 @@ __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b
     const bool none = !attend_fits(b, sums[0], sums[1], sums[2], base);
     const int l = wave >= kPlanWaves / 2;                      // half of the threads for each list
     AttendList out{none ? 0 : l ? base[1] : base[0], none ? 0 : l ? base[5] : base[4], none ? 0 : l ? base[3] : base[2], 1};
-    const int64_t all = (int64_t)out.units * b.kv_heads, run = worker_run(all, kAttendWorkers);
+    const int workers = l ? b.workers[1] : b.workers[0];
+    const int64_t all = (int64_t)out.units * b.kv_heads, run = worker_run(all, workers);
     out.run = run < 1 ? 1 : (int32_t)run;
-    const int w = tid & (kAttendWorkers - 1);
-    if (!w)
+    if (tid == l * (kPlanThreads / 2))
         b.plan->list[l] = out;
-    const int64_t u = (int64_t)w * out.run;
-    if (u < all) {
+    for (int w = tid & (kPlanThreads / 2 - 1); w < workers; w += kPlanThreads / 2) {
+        const int64_t u = (int64_t)w * out.run;
+        if (u >= all)
+            break;
         const int32_t want = (int32_t)(u >> 32 ? u % out.units : (uint32_t)u % (uint32_t)out.units);
         int lo = 0, hi = out.tiles - 1;
         while (lo < hi) {
@@ -488,7 +487,7 @@ __device__ __forceinline__ const char *scalar_address(const char *p)
 
 // Workgroups of one XCD take neighbouring runs: tiles of one prefix or request, and so the pages
 // they read, stay in one L2.
-__device__ __forceinline__ int worker_of_block() { return (blockIdx.x & 7) * (kAttendWorkers / 8) + (blockIdx.x >> 3); }
+__device__ __forceinline__ int worker_of_block() { return (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3); }
 
 __device__ __forceinline__ float fexp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -529,7 +528,7 @@ __device__ __forceinline__ void odd_values(Frag<T> &v, const Frag<T> &sees, Acc 
 }
 
 template <typename T, int KIND, int DP>
-__global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
+__global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend_narrow_kernel(AttendArgs a)
 {
     constexpr int NS = DP / 32, ND = DP / 16, W = DP + 4;
     __shared__ float lds_o[4][kNarrowRows][W];
@@ -543,7 +542,7 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
     const int64_t end = at + list.run < total ? at + list.run : total;
     if (at >= end)
         return;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
     const int heads = b.group * b.kv_heads, hd = a.c.head_dim;
     const bool vec = (((uintptr_t)a.q | (uintptr_t)a.y) & 15) == 0;
     int head = __builtin_amdgcn_readfirstlane((int)(at / list.units)), x = first;
@@ -583,27 +582,48 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
                                             : b.pages + (int64_t)t.seq * b.max_pages;
         const int32_t *pre_pages = t.pre_len ? b.prefix_pages + (int64_t)t.pre_seq * b.prefix_max_pages : nullptr;
 
+        // Where the wave's blocks are: each lane holds the address of that of one unit, 64 at a time, so
+        // that no load of keys waits for one of a page.  Blocks that no row sees have the cache's first page.
+        bool lost = false;                                   // a page was not one of the cache's
+        uint32_t far_lo = 0, far_hi = 0;
+        int far0 = 0;
+        auto look = [&](int u) __attribute__((always_inline)) {
+            far0 = u;
+            const int uu = u + lane;
+            const bool in_pre = uu < pre_units;
+            const int tok0 = (in_pre ? uu : uu - pre_units) * kNarrowUnit + wave * kBlock;
+            int page = 0;
+            if (uu < u1 && tok0 < (in_pre ? t.pre_len : see_max))
+                page = (in_pre ? pre_pages : own_pages)[tok0 >> a.c.page_shift];
+            const bool good = (uint32_t)page < (uint32_t)a.c.pages;
+            lost |= __any(!good);
+            const uint64_t p = (uint64_t)(a.c.base + cache_block(a.c, good ? page : 0, head,
+                                                                 (tok0 >> 5) & ((1 << (a.c.page_shift - 5)) - 1)));
+            far_lo = (uint32_t)p;
+            far_hi = (uint32_t)(p >> 32);
+        };
+
         f32x4 o[ND];
 #pragma unroll
         for (int d = 0; d < ND; ++d)
             o[d] = f32x4{0, 0, 0, 0};
         float m = kNone, l = 0;
-
-        for (int u = u0; u < u1; ++u) {
-            const bool in_pre = u < pre_units;
-            const int tok0 = (in_pre ? u : u - pre_units) * kNarrowUnit + wave * kBlock;
-            int most = in_pre ? t.pre_len : see_max, least = in_pre ? t.pre_len : see_min;
-            int here = (in_pre ? t.pre_len : see) - tok0;    // tokens of the block this row sees
-            if (tok0 >= most)
-                continue;
-            const int page = (in_pre ? pre_pages : own_pages)[tok0 >> a.c.page_shift];
-            const bool good = (uint32_t)page < (uint32_t)a.c.pages;
-            if (!good) {                                     // rows that see it become NaN
-                l = __builtin_nanf("");
-                if (!lane)
-                    atomicOr(b.flags, LORA_FLAG_CACHE_PAGE);
+        // The wave's block of a unit; MASKED: some rows do not see all of its tokens.
+        auto work = [&](auto masked, int u) __attribute__((always_inline)) {
+            constexpr bool MASKED = decltype(masked)::value;
+            if (u - far0 >= 64)
+                look(u);
+            const uint32_t lo = __builtin_amdgcn_readlane(far_lo, u - far0), hi = __builtin_amdgcn_readlane(far_hi, u - far0);
+            const char *blk = (const char *)((uint64_t)hi << 32 | lo);
+            int here = 0, most = 0;                          // tokens of the block that this row sees, that any of the tile does
+            if constexpr (MASKED) {
+                const bool in_pre = u < pre_units;
+                const int tok0 = (in_pre ? u : u - pre_units) * kNarrowUnit + wave * kBlock;
+                here = (in_pre ? t.pre_len : see) - tok0;
+                most = (in_pre ? t.pre_len : see_max) - tok0;
+                if (most <= 0)
+                    return;
             }
-            const char *blk = a.c.base + cache_block(a.c, good ? page : 0, head, (tok0 >> 5) & ((1 << (a.c.page_shift - 5)) - 1));
             Held<T, KIND> kh[2][NS], vh[ND];
             const int km = 8 * (n >> 2) + (n & 3);
 #pragma unroll
@@ -611,18 +631,16 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     kh[c][s] = held_load<T, KIND>(blk, (4 * s + g) * kBlock + km + 4 * c);
+            f32x4 ks[2], vs[2];                              // of codes: of tokens 8 g + 4 c + i
+            if constexpr (KIND != kCacheNative)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    ks[c] = *(const f32x4 *)(blk + 2 * a.c.half + (8 * g + 4 * c) * 4);
+                    vs[c] = *(const f32x4 *)(blk + 2 * a.c.half + (kBlock + 8 * g + 4 * c) * 4);
+                }
 #pragma unroll
             for (int d = 0; d < ND; ++d)
                 vh[d] = held_load<T, KIND>(blk + a.c.half, g * DP + 16 * d + n);
-            f32x4 ks[2], vs[2];
-            if constexpr (KIND != kCacheNative) {
-                const float *sc = (const float *)(blk + 2 * a.c.half);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    ks[c] = *(const f32x4 *)(sc + 8 * g + 4 * c);
-                    vs[c] = *(const f32x4 *)(sc + kBlock + 8 * g + 4 * c);
-                }
-            }
             f32x4 st[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
             for (int s = 0; s < NS; ++s)
@@ -632,7 +650,6 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
             // scores in powers of two; token 8 g + 4 c + i of the block
             float p[8];
             float top = kNone;
-            const bool part = tok0 + kBlock > least;
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -640,7 +657,7 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
                     float v = st[c][i] * a.scale;
                     if constexpr (KIND != kCacheNative)
                         v *= ks[c][i];
-                    if (part && 8 * g + 4 * c + i >= here)
+                    if (MASKED && 8 * g + 4 * c + i >= here)
                         v = kNone;
                     p[4 * c + i] = v;
                     top = __builtin_fmaxf(top, v);
@@ -661,32 +678,41 @@ __global__ __launch_bounds__(256) void attend_narrow_kernel(AttendArgs a)
             for (int j = 0; j < 8; ++j) {
                 p[j] = fexp2(p[j] - off);
                 l += p[j];
-                if constexpr (KIND != kCacheNative)
-                    p[j] = part && 8 * g + j >= here ? 0.f : p[j] * vs[j >> 2][j & 3];
+                if constexpr (KIND != kCacheNative)          // a hidden token's scale may be NaN
+                    p[j] = MASKED && 8 * g + j >= here ? 0.f : p[j] * vs[j >> 2][j & 3];
             }
             const Frag<T> pf = to_frag(p, T());
-            if (!part) {
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-                    o[d] = mma(frag_of(vh[d]), pf, o[d]);
-            } else {
-                // what no row sees may hold anything
-                const int keep = most - tok0 - 8 * g;
-                float sees[8];
+            Frag<T> sees{};
+            if constexpr (MASKED && KIND == kCacheNative)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    sees[j] = 8 * g + j < here ? 1.f : 0.f;
-                const Frag<T> sf = to_frag(sees, T());
+                    sees.v[j] = 8 * g + j < here ? 1.f : 0.f;
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    Frag<T> v = frag_of(vh[d]);
-                    cut(v, keep);
+            for (int d = 0; d < ND; ++d) {
+                Frag<T> v = frag_of(vh[d]);
+                if constexpr (MASKED) {                      // what no row sees may hold anything
+                    cut(v, most - 8 * g);
                     if constexpr (KIND == kCacheNative)
-                        if (least < most)
-                            odd_values<T>(v, sf, o[d]);
-                    o[d] = mma(v, pf, o[d]);
+                        odd_values<T>(v, sees, o[d]);
                 }
+                o[d] = mma(v, pf, o[d]);
             }
+        };
+        look(u0);
+        const int pre_full = (t.pre_len - (wave + 1) * kBlock + kNarrowUnit) / kNarrowUnit;
+        const int own_full = pre_units + (see_min - (wave + 1) * kBlock + kNarrowUnit) / kNarrowUnit;
+        for (int u = u0; u < u1;) {
+            const int full = u < pre_units ? pre_full : own_full;
+            const int stop = full < u1 ? full : u1;
+            for (; u < stop; ++u)
+                work(std::false_type(), u);
+            if (u < u1)
+                work(std::true_type(), u++);
+        }
+        if (lost) {
+            l = __builtin_nanf("");
+            if (!lane)
+                atomicOr(b.flags, LORA_FLAG_CACHE_PAGE);
         }
 
         // join the waves
@@ -1320,10 +1346,10 @@ template <typename T, int KIND>
 hipError_t launch_narrow(const AttendArgs &a, hipStream_t st)
 {
     switch (a.c.dp) {
-    case 64: attend_narrow_kernel<T, KIND, 64><<<kAttendWorkers, 256, 0, st>>>(a); break;
-    case 96: attend_narrow_kernel<T, KIND, 96><<<kAttendWorkers, 256, 0, st>>>(a); break;
-    case 128: attend_narrow_kernel<T, KIND, 128><<<kAttendWorkers, 256, 0, st>>>(a); break;
-    default: attend_narrow_kernel<T, KIND, 256><<<kAttendWorkers, 256, 0, st>>>(a); break;
+    case 64: attend_narrow_kernel<T, KIND, 64><<<a.b.workers[0], 256, 0, st>>>(a); break;
+    case 96: attend_narrow_kernel<T, KIND, 96><<<a.b.workers[0], 256, 0, st>>>(a); break;
+    case 128: attend_narrow_kernel<T, KIND, 128><<<a.b.workers[0], 256, 0, st>>>(a); break;
+    default: attend_narrow_kernel<T, KIND, 256><<<a.b.workers[0], 256, 0, st>>>(a); break;
     }
     return hipGetLastError();
 }
@@ -1332,10 +1358,10 @@ template <int KIND>
 hipError_t launch_wide(const AttendArgs &a, hipStream_t st)
 {
     switch (a.c.dp) {
-    case 64: attend_wide_kernel<KIND, 64><<<kAttendWorkers, 256, 0, st>>>(a); break;
-    case 96: attend_wide_kernel<KIND, 96><<<kAttendWorkers, 256, 0, st>>>(a); break;
-    case 128: attend_wide_kernel<KIND, 128><<<kAttendWorkers, 256, 0, st>>>(a); break;
-    default: attend_wide_kernel<KIND, 256><<<kAttendWorkers, 256, 0, st>>>(a); break;
+    case 64: attend_wide_kernel<KIND, 64><<<a.b.workers[1], 256, 0, st>>>(a); break;
+    case 96: attend_wide_kernel<KIND, 96><<<a.b.workers[1], 256, 0, st>>>(a); break;
+    case 128: attend_wide_kernel<KIND, 128><<<a.b.workers[1], 256, 0, st>>>(a); break;
+    default: attend_wide_kernel<KIND, 256><<<a.b.workers[1], 256, 0, st>>>(a); break;
     }
     return hipGetLastError();
 }

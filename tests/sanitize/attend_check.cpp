@@ -151,7 +151,7 @@ static void check_plan(const Batch &in, bool ordered)
         }
         CHECK(units <= 1 << 30);
         lists[l] = {(int32_t)all[l].size(), (int32_t)units, (int32_t)kept[l],
-                    (int32_t)std::max<int64_t>(1, worker_run(units * b.kv_heads, kAttendWorkers))};
+                    (int32_t)std::max<int64_t>(1, worker_run(units * b.kv_heads, b.workers[l]))};
     }
     for (int l = 0; l < 2; ++l) {
         const AttendList &L = lists[l];
@@ -161,7 +161,7 @@ static void check_plan(const Batch &in, bool ordered)
         for (int h = 0; h < b.kv_heads; ++h)
             for (const AttendTile &t : all[l]) {
                 const int w0 = first_worker(L, h, t), w1 = last_worker(L, h, t);
-                CHECK(w0 >= 0 && w0 <= w1 && w1 < kAttendWorkers);
+                CHECK(w0 >= 0 && w0 <= w1 && w1 < b.workers[l]);
                 const int64_t at = (int64_t)h * L.units + t.unit0;
                 for (int w = w0; w <= w1; ++w) {
                     const int64_t a = std::max(at, (int64_t)w * L.run), e = std::min(at + t.units, (int64_t)(w + 1) * L.run);
@@ -223,6 +223,8 @@ static void plans()
         b.kv_heads = pick(1, 9);
         b.page_shift = pick(5, 8);
         b.wide = pick(0, 1);
+        for (int &w : b.workers)
+            w = kAttendCus * pick(1, kAttendWorkers / kAttendCus);
         b.n_seqs = pick(1, round % 7 ? 40 : 700);
         b.n_prefixes = pick(0, 2) ? pick(0, 6) : 0;
         b.max_pages = pick(0, 12);
