@@ -89,7 +89,8 @@ constexpr int kShareRows = 32;
 constexpr int kAttendCus = 256, kAttendWorkers = 4 * kAttendCus;   // at most
 constexpr int kAttendPerCu(int elem, int kind, int dp)             // narrow tiles
 {
-    return dp > 128 ? 1 : elem == 4 || (kind == 0 && dp > 64) ? 2 : 3;
+    return dp > 128 ? (elem == 4 && kind == 0 ? 1 : 2) : dp > 96 ? (elem == 4 && kind == 0 ? 2 : 3)
+         : dp > 64 && kind == 0 ? 3 : 4;
 }
 
 struct AttendTile {
@@ -133,6 +134,7 @@ struct AttendBatch {
     int32_t page_shift;
     int32_t wide;                // wide tiles may be used
     int32_t workers[2];          // of the lists' kernels
+    int32_t simple;              // planned by each launch for itself (simple_batch)
     // workspace, all written by the plan
     AttendPlan *plan;
     AttendTile *tiles[2];
@@ -245,6 +247,26 @@ __host__ __device__ inline AttendEntity prefix_of_batch(const AttendBatch &b, in
     t.keeps = 1;
     t.list = b.wide && t.rows > kShareRows;
     t.tiles = units_for(t.rows, list_rows(t.list));
+    return t;
+}
+
+// Batches that need no plan kernel: one new token a request, no prefixes, and requests whose rows
+// are one narrow tile each, so few that a workgroup sums their units itself.
+constexpr int kSimpleSeqs = 256;
+inline bool simple_batch(const AttendBatch &b)
+{
+    return !b.q_start && !b.n_prefixes && b.n_seqs <= kSimpleSeqs && b.group <= kNarrowRows;
+}
+__host__ __device__ inline AttendTile simple_tile(int seq, int len, int group, int unit0)
+{
+    AttendTile t{};
+    t.seq = t.token0 = seq;
+    t.rows = group;
+    t.len = len;
+    t.q_len = 1;
+    t.unit0 = unit0;
+    t.units = len > 0 ? units_for(len, kNarrowUnit) : 1;
+    t.kept = t.prefix = t.pre_seq = -1;
     return t;
 }
 

@@ -12,6 +12,7 @@
 // as that of the rounded result); the sum is that of the unrounded ones.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "lora_attend.h"
@@ -491,6 +492,56 @@ __device__ __forceinline__ int worker_of_block() { return (blockIdx.x & 7) * (gr
 
 __device__ __forceinline__ float fexp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// at / units: a key-value head.
+__device__ __forceinline__ int div_small(int64_t at, int32_t units)
+{
+    return at >> 32 ? (int)(at / units) : (int)((uint32_t)at / (uint32_t)units);
+}
+
+// ---------------------------------------------------------------------------
+// simple batches: a workgroup sums the requests' units itself, one a thread
+
+struct SimplePlan {
+    int32_t len[kSimpleSeqs], unit0[kSimpleSeqs], sum[4];
+};
+__device__ __forceinline__ AttendList plan_simple(const AttendBatch &b, SimplePlan &p)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    bool bad = false;
+    const int len = tid < b.n_seqs ? held_of(b.lengths[tid], b.max_pages, b.page_shift, &bad) : 0;
+    if (bad && !blockIdx.x && !blockIdx.y)
+        atomicOr(b.flags, LORA_FLAG_ATTEND_BATCH);
+    const int units = tid < b.n_seqs ? simple_tile(tid, len, b.group, 0).units : 0;
+    const int incl = wave_scan(units);
+    if (lane == 63)
+        p.sum[wave] = incl;
+    lds_sync();
+    int before = incl - units, all = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        before += k < wave ? p.sum[k] : 0;
+        all += p.sum[k];
+    }
+    p.len[tid] = len;
+    p.unit0[tid] = before;
+    lds_sync();
+    all = __builtin_amdgcn_readfirstlane(all);
+    return {b.n_seqs, all, 0, (int32_t)worker_run((int64_t)all * b.kv_heads, b.workers[0])};
+}
+// The tile with unit u.
+__device__ __forceinline__ int find_simple(const SimplePlan &p, int u, int tiles)
+{
+    int lo = 0, hi = tiles - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__builtin_amdgcn_readfirstlane(p.unit0[mid]) <= u)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
 // ---------------------------------------------------------------------------
 // narrow tiles: 16 rows, four waves on 32 tokens each of a unit of 128
 
@@ -533,11 +584,19 @@ __global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend
     constexpr int NS = DP / 32, ND = DP / 16, W = DP + 4;
     __shared__ float lds_o[4][kNarrowRows][W];
     __shared__ float lds_m[4][kNarrowRows], lds_l[4][kNarrowRows];
+    __shared__ SimplePlan own;
     const AttendBatch &b = a.b;
     const int w = worker_of_block();
-    const AttendList list = scalar(&b.plan->list[0]);
-    const int first = scalar(b.start[0] + w);                // stale if the worker has no work
-    const int64_t total = scalar(&b.plan->bad) ? 0 : (int64_t)list.units * b.kv_heads;
+    AttendList list;
+    int first = 0, bad = 0;
+    if (b.simple) {
+        list = plan_simple(b, own);
+    } else {
+        list = scalar(&b.plan->list[0]);
+        first = scalar(b.start[0] + w);                      // stale if the worker has no work
+        bad = scalar(&b.plan->bad);
+    }
+    const int64_t total = bad ? 0 : (int64_t)list.units * b.kv_heads;
     int64_t at = (int64_t)w * list.run;
     const int64_t end = at + list.run < total ? at + list.run : total;
     if (at >= end)
@@ -545,14 +604,19 @@ __global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
     const int heads = b.group * b.kv_heads, hd = a.c.head_dim;
     const bool vec = (((uintptr_t)a.q | (uintptr_t)a.y) & 15) == 0;
-    int head = __builtin_amdgcn_readfirstlane((int)(at / list.units)), x = first;
+    int head = __builtin_amdgcn_readfirstlane(div_small(at, list.units));
+    int x = b.simple ? find_simple(own, (int)(at - (int64_t)head * list.units), list.tiles) : first;
 
     for (; at < end; ++x) {
         if (x == list.tiles) {
             x = 0;
             ++head;
         }
-        const AttendTile t = scalar(b.tiles[0] + x);
+        AttendTile t;
+        if (b.simple)
+            t = simple_tile(x, __builtin_amdgcn_readfirstlane(own.len[x]), b.group, __builtin_amdgcn_readfirstlane(own.unit0[x]));
+        else
+            t = scalar(b.tiles[0] + x);
         const int64_t base = (int64_t)head * list.units + t.unit0;
         const int u0 = (int)(at - base);
         const int u1 = (int)((end < base + t.units ? end : base + t.units) - base);
@@ -818,7 +882,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
     // row r of a result holds token 16 (r / 16) + 8 h + 0..7 in its registers when the rows of
     // the operand take the tokens with bits 2 and 3 of their number exchanged
     const int ktok = (n & 19) | (n & 4) << 1 | (n & 8) >> 1;
-    int head = __builtin_amdgcn_readfirstlane((int)(at / list.units)), x = first;
+    int head = __builtin_amdgcn_readfirstlane(div_small(at, list.units)), x = first;
 
     for (; at < end; ++x) {
         if (x == list.tiles) {
@@ -1215,24 +1279,77 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
 // ---------------------------------------------------------------------------
 // joining parts
 
-// One workgroup a tile and key-value head, four dims a lane.  A group of lanes takes a row, or a
-// share of its parts where rows are few: each lane fetches the maximum and sum of one part, the
-// weights follow from them, and no load of a part waits for another.
+// A workgroup takes a narrow tile of a key-value head, or 16 rows of a wide one, four dims a lane.
+// A group of lanes takes a row, or a share of its parts where rows are few: each lane fetches the
+// maximum and sum of one part, the weights follow from them, and no load of a part waits for
+// another.  Wide tiles whose parts are kept only where workers part are found by those borders,
+// which are far fewer than the tiles.
+// Where there are many narrow tiles of few rows, a workgroup takes several key-value heads of one.
+struct JoinGrid {
+    int32_t narrow, kept, borders;       // workgroups: narrow tiles, wide ones whose parts are kept, borders
+    int32_t heads, each;                 // of a narrow tile: workgroups, and key-value heads a workgroup
+};
+constexpr int kJoinRows = 16, kJoinChunks = kWideRows / kJoinRows;
+
 template <typename T, int DP>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, JoinGrid grid)
 {
     constexpr int NL = DP <= 64 ? 16 : DP <= 128 ? 32 : 64, NG = 256 / NL;
     __shared__ f32x4 lds_o[NG][NL];
     __shared__ float lds_m[NG], lds_l[NG];
+    __shared__ SimplePlan own;
     const AttendBatch &b = a.b;
-    const int l = (int)blockIdx.x >= b.cap[0];
-    const int x = l ? blockIdx.x - b.cap[0] : blockIdx.x, head = blockIdx.y;
-    const AttendList list = b.plan->list[l], other = b.plan->list[!l];
-    const AttendTile t = b.tiles[l][x];                      // stale where x is past the list
-    if (x >= list.tiles)
+    const int l = (int)blockIdx.x >= grid.narrow;
+    AttendList list, other{};
+    AttendTile t;
+    int head, chunk = 0, w0, w1;
+    if (b.simple) {
+        list = plan_simple(b, own);
+        const int x = blockIdx.x / grid.heads;
+        head = blockIdx.x % grid.heads;
+        t = simple_tile(x, own.len[x], b.group, own.unit0[x]);
+    } else if (!l) {
+        list = b.plan->list[0];
+        other = b.plan->list[1];
+        const int x = blockIdx.x / grid.heads;
+        head = blockIdx.x % grid.heads;
+        t = b.tiles[0][x];                                   // stale where x is past the list
+        if (x >= list.tiles)
+            return;
+    } else {
+        list = b.plan->list[1];
+        other = b.plan->list[0];
+        const int i = blockIdx.x - grid.narrow, kept = i < grid.kept;
+        chunk = (kept ? i : i - grid.kept) % kJoinChunks;
+        const int k = (kept ? i : i - grid.kept) / kJoinChunks;
+        if (kept) {
+            const int x = k / b.kv_heads;
+            head = k % b.kv_heads;
+            t = b.tiles[1][x];
+            if (x >= list.tiles || t.kept < 0)
+                return;
+        } else {                                             // the first border inside of a tile
+            const int64_t at = (int64_t)(k + 1) * list.run;
+            if (at >= (int64_t)list.units * b.kv_heads)
+                return;
+            head = div_small(at, list.units);
+            t = b.tiles[1][b.start[1][k + 1]];
+            if (t.kept >= 0 || first_worker(list, head, t) != k)
+                return;
+        }
+        if (chunk * kJoinRows >= t.rows)
+            return;
+    }
+    if (t.shared)
         return;
-    const int w0 = first_worker(list, head, t), w1 = last_worker(list, head, t);
-    if (t.shared || (t.kept < 0 && w0 == w1))
+    const int each = l ? 1 : grid.each, per_head = NG / each;            // heads, and groups of one
+    const int grp = threadIdx.x / NL % per_head;
+    head = head * each + threadIdx.x / NL / per_head;
+    const bool has = head < b.kv_heads;
+    w0 = has ? first_worker(list, head, t) : 0;
+    w1 = has ? last_worker(list, head, t) : 0;
+    const bool joins = has && (t.kept >= 0 || w0 != w1);
+    if (each == 1 && !joins)
         return;
     const int R = list_rows(l), hd = a.c.head_dim, heads = b.group * b.kv_heads;
     PrefixTile pre{0, 0};
@@ -1246,14 +1363,16 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
     const int PR = list_rows(pre.list);
     const bool vec = ((uintptr_t)a.y & 15) == 0;
     int split = 1;                                           // groups of a row
-    while (split < 8 && t.rows * split * 2 <= NG)
+    const int row_end = l && t.rows > (chunk + 1) * kJoinRows ? (chunk + 1) * kJoinRows : t.rows;
+    const int row0 = chunk * kJoinRows;
+    while (split < 8 && (row_end - row0) * split * 2 <= per_head)
         split *= 2;
-    const int grp = threadIdx.x / NL, lane = threadIdx.x % NL, sub = grp % split, d = lane * 4;
+    const int lane = threadIdx.x % NL, sub = grp % split, d = lane * 4;
     const int n_own = w1 - w0 + 1;
     const int64_t own_at = part_slot(list, head, t, w0);
-    for (int r0 = 0; r0 < t.rows; r0 += NG / split) {
+    for (int r0 = row0; r0 < row_end; r0 += per_head / split) {
         const int r = r0 + grp / split;
-        const bool live = r < t.rows;
+        const bool live = joins && r < row_end;
         float top = kNone, sum = 0;
         f32x4 v = {0, 0, 0, 0};
         if (live) {
@@ -1309,23 +1428,24 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a)
             }
         }
         if (split > 1) {
-            lds_o[grp][lane] = v;
+            const int me = threadIdx.x / NL;
+            lds_o[me][lane] = v;
             if (!lane) {
-                lds_m[grp] = top;
-                lds_l[grp] = sum;
+                lds_m[me] = top;
+                lds_l[me] = sum;
             }
             __syncthreads();
             if (live && !sub) {
                 float up = top;
                 for (int k = 1; k < split; ++k)
-                    up = __builtin_fmaxf(up, lds_m[grp + k]);
+                    up = __builtin_fmaxf(up, lds_m[me + k]);
                 float f = top == kNone ? 1.f : fexp2(top - up);
                 v *= f;
                 sum *= f;
                 for (int k = 1; k < split; ++k) {
-                    f = lds_m[grp + k] == kNone ? 1.f : fexp2(lds_m[grp + k] - up);
-                    v += lds_o[grp + k][lane] * f;
-                    sum += lds_l[grp + k] * f;
+                    f = lds_m[me + k] == kNone ? 1.f : fexp2(lds_m[me + k] - up);
+                    v += lds_o[me + k][lane] * f;
+                    sum += lds_l[me + k] * f;
                 }
             }
         }
@@ -1381,12 +1501,23 @@ hipError_t launch_all(const AttendArgs &a, hipStream_t st)
                                          : launch_narrow<T, kCacheInt8>(a, st);
     if (e != hipSuccess)
         return e;
-    const dim3 grid(a.b.cap[0] + a.b.cap[1], a.b.kv_heads);
+    JoinGrid grid;
+    // a workgroup has 1024 / dp groups of lanes (4, 8 or 16), a row each; a tile of one row for one head
+    // costs as much as one that fills them
+    const int groups = a.c.dp <= 64 ? 16 : a.c.dp <= 128 ? 8 : 4, rows = std::min(a.b.max_queries * a.b.group, kNarrowRows);
+    grid.each = 1;
+    while (a.b.cap[0] * a.b.kv_heads > 1024 * grid.each && grid.each * 2 <= a.b.kv_heads && grid.each * 2 * rows <= groups)
+        grid.each *= 2;
+    grid.heads = (a.b.kv_heads + grid.each - 1) / grid.each;
+    grid.narrow = a.b.cap[0] * grid.heads;
+    grid.kept = a.b.n_prefixes && a.b.group > kShareRows ? a.b.cap[1] * a.b.kv_heads * kJoinChunks : 0;
+    grid.borders = a.b.cap[1] ? (a.b.workers[1] - 1) * kJoinChunks : 0;
+    const int all = grid.narrow + grid.kept + grid.borders;
     switch (a.c.dp) {
-    case 64: attend_join_kernel<T, 64><<<grid, 256, 0, st>>>(a); break;
-    case 96: attend_join_kernel<T, 96><<<grid, 256, 0, st>>>(a); break;
-    case 128: attend_join_kernel<T, 128><<<grid, 256, 0, st>>>(a); break;
-    default: attend_join_kernel<T, 256><<<grid, 256, 0, st>>>(a); break;
+    case 64: attend_join_kernel<T, 64><<<all, 256, 0, st>>>(a, grid); break;
+    case 96: attend_join_kernel<T, 96><<<all, 256, 0, st>>>(a, grid); break;
+    case 128: attend_join_kernel<T, 128><<<all, 256, 0, st>>>(a, grid); break;
+    default: attend_join_kernel<T, 256><<<all, 256, 0, st>>>(a, grid); break;
     }
     return hipGetLastError();
 }

@@ -85,6 +85,9 @@ CASES = [
     ("bf16", "native", 8, 1, 256, 32, [100, 3], [200, 30], [(0, 2, 100)]),
     ("bf16", "native", 8, 1, 128, 64, [700], [1500], [(0, 1, 900)]),
     ("bf16", "int8", 8, 1, 128, 32, [200], [1500], [(0, 1, 900)]),
+    # many tiles of few rows: several key-value heads are joined together
+    ("bf16", "native", 5, 5, 64, 32, [1] * 300, [i % 70 for i in range(300)], [(3, 290, 140)]),
+    ("bf16", "fp8", 6, 3, 128, 32, [1] * 400, [i % 50 for i in range(400)], [(0, 400, 300)]),
     # more work than workers
     ("bf16", "native", 32, 32, 64, 32, [1] * 70, [5 * i + 1 for i in range(70)], [(10, 60, 200)]),
 ]
@@ -104,10 +107,34 @@ def test_rows_of_no_request_stay():
     check_rows(r, y, scale, before, "lead and tail")
 
 
-def test_no_starts():
-    r = Requests(4, "bf16", "native", 4, 2, 64, 32, [1] * 7, [40, 3, 9, 0, 100, 7, 7], q_start=False)
+@pytest.mark.parametrize("dtype,heads,kv_heads,lengths", [
+    ("bf16", 4, 2, [40, 3, 9, 0, 100, 7, 7]),
+    ("bf16", 16, 1, [5000]),
+    ("fp32", 3, 3, [0]),
+    ("bf16", 8, 8, [11 * i % 400 for i in range(255)]),
+    ("fp32", 5, 5, [7 * i % 90 for i in range(256)]),
+    ("bf16", 2, 1, [7 * i % 90 for i in range(257)]),        # more than a launch plans by itself
+    ("bf16", 17, 1, [40, 300]),                              # rows of more than one tile
+])
+def test_one_token_a_request_without_starts(dtype, heads, kv_heads, lengths):
+    r = Requests(4, dtype, "native", heads, kv_heads, 64, 32, [1] * len(lengths), lengths, q_start=False, tail=2)
     y, before, scale = attended(r)
     check_rows(r, y, scale, before, "no q_start")
+
+
+def test_lengths_out_of_range_without_starts():
+    r = Requests(18, "bf16", "native", 4, 2, 64, 32, [1] * 6, [40, 3, 64, 9, 100, 7], q_start=False)
+    S, cache = r.make()
+    q, b = r.q.cuda(), r.batch()
+    y, good = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+    S.attend_prepare(cache, r.heads, b)
+    S.attend(cache, q, good)
+    assert S.flags() == 0
+    for value in (2 ** 31 - 1, -2 ** 31):
+        b.lengths[1] = value
+        S.attend(cache, q, y)
+        assert S.flags() == binding.LORA_FLAG_ATTEND_BATCH
+        assert torch.equal(y[[0, 2, 3, 4, 5]], good[[0, 2, 3, 4, 5]])
 
 
 @pytest.mark.parametrize("kind", ["native", "fp8", "int8"])
