@@ -377,7 +377,7 @@ int do_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads, c
     b.max_pages = batch->max_pages;
     b.prefix_max_pages = batch->prefix_max_pages;
     b.max_queries = std::min(batch->max_queries, std::max(batch->n_tokens, 1));
-    b.group = q_heads / v.kv_heads;
+    set_group(b, q_heads / v.kv_heads);
     b.kv_heads = v.kv_heads;
     b.page_shift = v.page_shift;
     b.wide = ctx->dtype == LORA_BF16;
@@ -394,6 +394,9 @@ int do_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads, c
             b.cap[l] = (int32_t)cap[l];
             b.kept_cap[l] = (int32_t)kept[l];
         }
+        // most tiles times most units of one
+        const double most = ((double)b.max_pages + b.prefix_max_pages) * (1 << v.page_shift) / kWideUnit + 2;
+        b.units_fit = (double)(cap[0] + cap[1]) * most < (double)(1 << 30);
         AttendState cut;
         const size_t bytes = cut_workspace(nullptr, b, cut, v.dp);
         DeviceGuard guard(ctx->device);

@@ -93,7 +93,7 @@ constexpr int kAttendPerCu(int elem, int kind, int dp)             // narrow til
          : dp > 64 && kind == 0 ? 3 : 4;
 }
 
-struct AttendTile {
+struct alignas(16) AttendTile {
     int32_t seq;                 // request, or prefix if `shared`
     int32_t shared;              // rows come from the list of the prefix's tokens
     int32_t token0;              // first new token of the request, or of the prefix in its list
@@ -134,6 +134,8 @@ struct AttendBatch {
     int32_t page_shift;
     int32_t wide;                // wide tiles may be used
     int32_t workers[2];          // of the lists' kernels
+    int32_t units_fit;           // no batch of these sizes has more than 2^30 units
+    uint32_t group_mul, group_shift;   // x / group is (x + the high word of x group_mul) >> group_shift
     int32_t simple;              // planned by each launch for itself (simple_batch)
     // workspace, all written by the plan
     AttendPlan *plan;
@@ -270,8 +272,22 @@ __host__ __device__ inline AttendTile simple_tile(int seq, int len, int group, i
     return t;
 }
 
+// x / group for 0 <= x < 2^31, and the numbers that it takes.
+__host__ __device__ inline int32_t over_group(const AttendBatch &b, int32_t x)
+{
+    return (int32_t)(((uint32_t)(((uint64_t)(uint32_t)x * b.group_mul) >> 32) + (uint32_t)x) >> b.group_shift);
+}
+inline void set_group(AttendBatch &b, int32_t group)
+{
+    b.group = group;
+    b.group_shift = 0;
+    while ((1u << b.group_shift) < (uint32_t)group)
+        ++b.group_shift;
+    b.group_mul = (uint32_t)((((1ull << b.group_shift) - group) << 32) / group + 1);
+}
+
 // Tile j of an entity; `list0`: where the list of tokens that share has the request's first.
-__host__ __device__ inline AttendTile tile_of(const AttendEntity &e, int j, int group, int list0)
+__host__ __device__ inline AttendTile tile_of(const AttendBatch &b, const AttendEntity &e, int j, int list0)
 {
     const int R = list_rows(e.list), unit = list_unit(e.list);
     AttendTile t{};
@@ -285,13 +301,13 @@ __host__ __device__ inline AttendTile tile_of(const AttendEntity &e, int j, int 
     t.pre_len = e.pre_len;
     t.pre_seq = e.pre_seq;
     t.prefix = e.prefix;
-    t.pre_row = e.prefix >= 0 ? list0 * group + t.row0 : 0;
+    t.pre_row = e.prefix >= 0 ? list0 * b.group + t.row0 : 0;
     if (e.shared) {
         t.units = units_for(e.len, unit);
     } else {
         // its prefix where it reads that by itself, and its own tokens up to the last one
         // that its last row sees
-        const int last = (t.row0 + t.rows - 1) / group;
+        const int last = over_group(b, t.row0 + t.rows - 1);
         const int seen = e.len - e.q_len + last + 1;
         t.units = units_for(e.pre_len, unit) + units_for(seen < 0 ? 0 : seen, unit);
         if (t.units < 1)

@@ -39,7 +39,7 @@ constexpr int kPlanEach = 4;         // tiles a thread writes by itself; a wave 
 
 // What an entity adds to the lists.  Where requests, or prefixes, claim more tokens than there are
 // these sums may wrap; such a batch is found by sums of 64 bits and gets no work.
-struct PlanCount { int32_t v[7]; };  // tiles, kept tiles, units of the two lists, listed tokens
+struct PlanCount { int32_t v[6]; };  // tiles, kept tiles, units of the two lists
 
 // Inclusive sums over the lanes of a wave, and over each 16 of them.
 template <int CTRL, int ROWS>
@@ -88,6 +88,7 @@ __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b
     if (tid < b.n_seqs)
         words = request_words(b, tid);
     const bool small = b.n_seqs <= kPlanSeqs;
+    const int entities = b.n_seqs + b.n_prefixes;
     const int32_t *before = small ? listed_before : b.list_before;
     if (tid < 3)
         sums[tid] = 0;
@@ -105,164 +106,184 @@ __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b
         c.prefix_lengths = pre_len;
     }
     lds_sync();
-    int32_t base[7] = {};
     bool bad = false;
-    unsigned long long sum[3] = {};
+    AttendEntity e{};
+    // sum over the workgroup of one value a thread: those before the thread's, and all
+    auto sum_before = [&](int k, int32_t v, int32_t &all) {
+        const int32_t incl = row_scan((lane & 15) < waves ? wave_sum[k][lane & 15] : 0);
+        all = __builtin_amdgcn_readlane(incl, 15);
+        return (wave ? __builtin_amdgcn_readlane(incl, wave - 1) : 0) + v;
+    };
 
-    // requests, then prefixes, which need the requests' list
-    for (int part = 0; part < 2; ++part) {
-        const int first = part ? b.n_seqs : 0, end = part ? b.n_seqs + b.n_prefixes : b.n_seqs;
-        if (part) {
-            if (!tid) {
-                if (small)
-                    listed_before[b.n_seqs] = base[6];
-                else
-                    b.list_before[b.n_seqs] = base[6];
-            }
-            if (small)
-                lds_sync();
-            else
-                __syncthreads();
-        }
-        for (int from = first; from < end; from += threads) {
+    // the tokens of requests that share a prefix, request by request
+    int32_t n_listed = 0;
+    if (b.n_prefixes) {
+        for (int from = 0; from < b.n_seqs; from += threads) {
             const int i = from + tid;
-            AttendEntity e{};
-            PlanCount n{};
-            if (i < end) {
-                if (!part) {
-                    e = request_of(c, i, words, &bad);
-                    if (i + threads < end)
-                        words = request_words(b, i + threads);
-                } else {
-                    const int p = i - b.n_seqs, s0 = c.prefix_seqs[p], s1 = c.prefix_seqs[p + 1];
-                    bad |= s0 < 0 || s1 < s0 || s1 > b.n_seqs;
-                    const int lo = clamp_to(s0, 0, b.n_seqs), hi = clamp_to(s1, lo, b.n_seqs);
-                    const int l0 = before[lo];
-                    e = prefix_of_batch(c, p, l0, before[hi] - l0, &bad);
+            int32_t own = 0;
+            if (from + wave * 64 < b.n_seqs) {                 // waves without requests only keep the barriers
+                if (i < b.n_seqs) {
+                    e = request_of(c, i, from ? request_words(b, i) : words, &bad);
+                    own = e.listed;
                 }
-                unsigned long long units = 0;
-                for (int j = 0; j < e.tiles; ++j)
-                    units += tile_of(e, j, b.group, 0).units;
-                sum[0] += part ? 0 : e.q_len;
-                sum[1] += part ? e.rows / b.group : 0;
-                sum[2] += units;
-#pragma unroll
-                for (int l = 0; l < 2; ++l) {
-                    n.v[l] = e.list == l ? e.tiles : 0;
-                    n.v[2 + l] = e.list == l && e.keeps ? e.tiles : 0;
-                    n.v[4 + l] = e.list == l ? (int32_t)units : 0;
-                }
-                n.v[6] = e.listed;
-            }
-            PlanCount at{};
-            const bool any = from + wave * 64 < end;           // waves without entities only keep the barriers
-            if (!any) {
-                if (lane < 7)
-                    wave_sum[lane][wave] = 0;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 7; ++k) {
-                    const int32_t incl = wave_scan(n.v[k]);
-                    if (lane == 63)
-                        wave_sum[k][wave] = incl;
-                    at.v[k] = base[k] + incl - n.v[k];
-                }
+                own = wave_scan(own);
+                if (lane == 63)
+                    wave_sum[0][wave] = own;
+            } else if (!lane) {
+                wave_sum[0][wave] = 0;
             }
             lds_sync();
-#pragma unroll
-            for (int k = 0; k < 7; ++k) {
-                const int32_t incl = row_scan((lane & 15) < waves ? wave_sum[k][lane & 15] : 0);
-                at.v[k] += wave ? __builtin_amdgcn_readlane(incl, wave - 1) : 0;
-                base[k] += __builtin_amdgcn_readlane(incl, 15);
+            int32_t all;
+            const int32_t at = n_listed + sum_before(0, own, all) - e.listed;
+            if (i < b.n_seqs) {
+                b.list_before[i] = at;
+                if (small)
+                    listed_before[i] = at;
+                for (int j = 0; j < e.listed; ++j)
+                    if ((uint32_t)(at + j) < (uint32_t)b.n_tokens)
+                        b.listed[at + j] = e.token0 + j;
             }
-            if (i < end) {
-                const int l = e.list, tile = l ? at.v[1] : at.v[0];
-                const int kept = l ? at.v[3] : at.v[2], u0 = l ? at.v[5] : at.v[4];
-                int list0 = 0;
-                if (part) {
-                    b.prefix_tile[i - b.n_seqs] = PrefixTile{l, tile};
-                } else {
-                    b.list_before[i] = at.v[6];
-                    if (small)
-                        listed_before[i] = at.v[6];
-                    for (int j = 0; j < e.listed; ++j)
-                        if ((uint32_t)(at.v[6] + j) < (uint32_t)b.n_tokens)
-                            b.listed[at.v[6] + j] = e.token0 + j;
-                    list0 = at.v[6];
-                }
-                if (e.tiles > kPlanEach) {
-                    const int k = atomicAdd(&n_large, 1);      // their order changes no place
-                    large[k] = i;
-                    large_at[k][0] = tile;
-                    large_at[k][1] = kept;
-                    large_at[k][2] = u0;
-                    large_at[k][3] = list0;
-                } else {
-                    int u = u0;
-                    for (int j = 0; j < e.tiles && (uint32_t)(tile + j) < (uint32_t)b.cap[l]; ++j) {
-                        AttendTile t = tile_of(e, j, b.group, list0);
-                        t.kept = e.keeps ? kept + j : -1;
-                        t.unit0 = u;
-                        u += t.units;
-                        b.tiles[l][tile + j] = t;
-                        if (tile + j < kPlanUnits)
-                            unit0[l][tile + j] = t.unit0;
-                    }
-                }
-            }
+            n_listed += all;
             lds_sync();
-            const int count = n_large;
-            for (int k = wave; k < count; k += waves) {
-                const int id = large[k], tile = large_at[k][0], kept = large_at[k][1];
-                bool again = false;
-                int list0 = 0;
-                AttendEntity g;
-                if (!part) {
-                    g = request_of(c, id, request_words(b, id), &again);
-                    list0 = large_at[k][3];
-                } else {
-                    const int p = id - b.n_seqs;
-                    const int lo = clamp_to(c.prefix_seqs[p], 0, b.n_seqs), hi = clamp_to(c.prefix_seqs[p + 1], lo, b.n_seqs);
-                    const int l0 = before[lo];
-                    g = prefix_of_batch(c, p, l0, before[hi] - l0, &again);
-                }
-                int u = large_at[k][2];
-                for (int j0 = 0; j0 < g.tiles; j0 += 64) {
-                    const int j = j0 + lane;
-                    AttendTile t{};
-                    if (j < g.tiles)
-                        t = tile_of(g, j, b.group, list0);
-                    const int32_t incl = wave_scan(t.units);
-                    t.kept = g.keeps ? kept + j : -1;
-                    t.unit0 = u + incl - t.units;
-                    u += __builtin_amdgcn_readlane(incl, 63);
-                    if (j < g.tiles && (uint32_t)(tile + j) < (uint32_t)b.cap[g.list]) {
-                        b.tiles[g.list][tile + j] = t;
-                        if (tile + j < kPlanUnits)
-                            unit0[g.list][tile + j] = t.unit0;
-                    }
-                }
-            }
-            lds_sync();
-            if (!tid)
-                n_large = 0;
         }
+        if (!tid) {
+            if (small)
+                listed_before[b.n_seqs] = n_listed;
+            else
+                b.list_before[b.n_seqs] = n_listed;
+        }
+        if (small)
+            lds_sync();
+        else
+            __syncthreads();
+    }
+
+    // the tiles of requests and of prefixes
+    auto entity_of = [&](int i, const Request &r, bool *flag) {
+        if (i < b.n_seqs)
+            return request_of(c, i, r, flag);
+        const int p = i - b.n_seqs, s0 = c.prefix_seqs[p], s1 = c.prefix_seqs[p + 1];
+        *flag |= s0 < 0 || s1 < s0 || s1 > b.n_seqs;
+        const int lo = clamp_to(s0, 0, b.n_seqs), hi = clamp_to(s1, lo, b.n_seqs);
+        const int l0 = before[lo];
+        return prefix_of_batch(c, p, l0, before[hi] - l0, flag);
+    };
+    int32_t base[6] = {};
+    unsigned long long sum[3] = {};
+    for (int from = 0; from < entities; from += threads) {
+        const int i = from + tid;
+        PlanCount n{}, at{};
+        const bool any = from + wave * 64 < entities;
+        if (any) {
+            if (i >= entities)
+                e = AttendEntity{};
+            else if (from || i >= b.n_seqs || !b.n_prefixes || b.n_seqs > threads)   // else as found above
+                e = entity_of(i, from && i < b.n_seqs ? request_words(b, i) : words, &bad);
+            unsigned long long units = 0;
+            for (int j = 0; j < e.tiles; ++j)
+                units += tile_of(b, e, j, 0).units;
+            sum[0] += e.shared ? 0 : e.q_len;
+            sum[1] += e.shared ? over_group(b, e.rows) : 0;
+            sum[2] += units;
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {
+                n.v[l] = e.list == l ? e.tiles : 0;
+                n.v[2 + l] = e.list == l && e.keeps ? e.tiles : 0;
+                n.v[4 + l] = e.list == l ? (int32_t)units : 0;
+            }
+#pragma unroll
+            for (int k = 0; k < 6; ++k) {
+                const int32_t incl = wave_scan(n.v[k]);
+                if (lane == 63)
+                    wave_sum[k][wave] = incl;
+                at.v[k] = base[k] + incl - n.v[k];
+            }
+        } else if (lane < 6) {
+            wave_sum[lane][wave] = 0;
+        }
+        lds_sync();
+#pragma unroll
+        for (int k = 0; k < 6; ++k) {
+            int32_t all;
+            at.v[k] = sum_before(k, at.v[k], all);
+            base[k] += all;
+        }
+        if (any && i < entities) {
+            const int l = e.list, tile = l ? at.v[1] : at.v[0];
+            const int kept = l ? at.v[3] : at.v[2], u0 = l ? at.v[5] : at.v[4];
+            const int list0 = e.prefix >= 0 ? before[i] : 0;
+            if (i >= b.n_seqs)
+                b.prefix_tile[i - b.n_seqs] = PrefixTile{l, tile};
+            if (e.tiles > kPlanEach) {
+                const int k = atomicAdd(&n_large, 1);          // their order changes no place
+                large[k] = i;
+                large_at[k][0] = tile;
+                large_at[k][1] = kept;
+                large_at[k][2] = u0;
+                large_at[k][3] = list0;
+            } else {
+                int u = u0;
+                for (int j = 0; j < e.tiles && (uint32_t)(tile + j) < (uint32_t)b.cap[l]; ++j) {
+                    AttendTile t = tile_of(b, e, j, list0);
+                    t.kept = e.keeps ? kept + j : -1;
+                    t.unit0 = u;
+                    u += t.units;
+                    b.tiles[l][tile + j] = t;
+                    if (tile + j < kPlanUnits)
+                        unit0[l][tile + j] = t.unit0;
+                }
+            }
+        }
+        lds_sync();
+        const int count = n_large;
+        if (!count)
+            continue;
+        for (int k = wave; k < count; k += waves) {
+            const int id = large[k], tile = large_at[k][0], kept = large_at[k][1];
+            bool again = false;
+            const AttendEntity g = entity_of(id, id < b.n_seqs ? request_words(b, id) : Request{}, &again);
+            int u = large_at[k][2];
+            for (int j0 = 0; j0 < g.tiles; j0 += 64) {
+                const int j = j0 + lane;
+                AttendTile t{};
+                if (j < g.tiles)
+                    t = tile_of(b, g, j, large_at[k][3]);
+                const int32_t incl = wave_scan(t.units);
+                t.kept = g.keeps ? kept + j : -1;
+                t.unit0 = u + incl - t.units;
+                u += __builtin_amdgcn_readlane(incl, 63);
+                if (j < g.tiles && (uint32_t)(tile + j) < (uint32_t)b.cap[g.list]) {
+                    b.tiles[g.list][tile + j] = t;
+                    if (tile + j < kPlanUnits)
+                        unit0[g.list][tile + j] = t.unit0;
+                }
+            }
+        }
+        lds_sync();
+        if (!tid)
+            n_large = 0;
+        lds_sync();
     }
     if (bad)
         bad_any = 1;
-#pragma unroll 1
-    for (int k = 0; k < 3; ++k) {                              // whole numbers: their order changes nothing
-        const unsigned long long v = k == 0 ? sum[0] : k == 1 ? sum[1] : sum[2];
-        const uint32_t lo = wave_scan((int32_t)(v & 0xffffff)), hi = wave_scan((int32_t)(v >> 24));
-        if (lane == 63 && (lo | hi))
-            atomicAdd(&sums[k], ((unsigned long long)hi << 24) + lo);
-    }
-    lds_sync();
     if (base[0] > kPlanUnits || base[1] > kPlanUnits)
         __syncthreads();                                       // first units that the search reads from memory
-    // a batch that claims tokens twice gets no work; one that is only out of order, the work that
-    // its clamped values name
-    const bool none = !attend_fits(b, sums[0], sums[1], sums[2], base);
+    else
+        lds_sync();
+    // A batch that claims tokens twice gets no work; one that is only out of order, the work that its
+    // clamped values name.  Arrays in order claim none twice, and what they name fits.
+    bool none = false;
+    if (bad_any || !b.units_fit) {
+#pragma unroll 1
+        for (int k = 0; k < 3; ++k) {                          // whole numbers: their order changes nothing
+            const unsigned long long v = k == 0 ? sum[0] : k == 1 ? sum[1] : sum[2];
+            const uint32_t lo = wave_scan((int32_t)(v & 0xffffff)), hi = wave_scan((int32_t)(v >> 24));
+            if (lane == 63 && (lo | hi))
+                atomicAdd(&sums[k], ((unsigned long long)hi << 24) + lo);
+        }
+        lds_sync();
+        none = !attend_fits(b, sums[0], sums[1], sums[2], base);
+    }
     const int l = wave >= kPlanWaves / 2;                      // half of the threads for each list
     AttendList out{none ? 0 : l ? base[1] : base[0], none ? 0 : l ? base[5] : base[4], none ? 0 : l ? base[3] : base[2], 1};
     const int workers = l ? b.workers[1] : b.workers[0];
@@ -462,7 +483,7 @@ __device__ __forceinline__ Frag<T> q_frag(const T *q, bool vec)
 
 __device__ __forceinline__ int row_token(const AttendBatch &b, const AttendTile &t, int r)
 {
-    const int at = t.token0 + r / b.group;
+    const int at = t.token0 + over_group(b, r);
     return t.shared ? b.listed[at] : at;
 }
 
@@ -627,7 +648,7 @@ __global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend
         {
             const int r = mine ? row : t.row0;
             const int token = row_token(b, t, r);
-            const T *p = (const T *)a.q + ((int64_t)token * heads + head * b.group + r % b.group) * hd;
+            const T *p = (const T *)a.q + ((int64_t)token * heads + head * b.group + (r - over_group(b, r) * b.group)) * hd;
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
                 const int d = 32 * s + 8 * g;
@@ -638,9 +659,9 @@ __global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend
         }
         // tokens of the request's own pages that this lane's row sees, the fewest and the most of the tile
         const int per = t.shared ? 0 : t.len - t.q_len + 1;
-        const int see = t.shared ? t.len : per + (mine ? row : t.row0 + t.rows - 1) / b.group;
-        const int see_min = t.shared ? t.len : per + t.row0 / b.group;
-        const int see_max = t.shared ? t.len : per + (t.row0 + t.rows - 1) / b.group;
+        const int see = t.shared ? t.len : per + over_group(b, mine ? row : t.row0 + t.rows - 1);
+        const int see_min = t.shared ? t.len : per + over_group(b, t.row0);
+        const int see_max = t.shared ? t.len : per + over_group(b, t.row0 + t.rows - 1);
         const int pre_units = units_for(t.pre_len, kNarrowUnit);
         const int32_t *own_pages = t.shared ? b.prefix_pages + (int64_t)t.seq * b.prefix_max_pages
                                             : b.pages + (int64_t)t.seq * b.max_pages;
@@ -814,14 +835,14 @@ __global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend
             if (whole) {
                 if (d < hd) {
                     const int rr = t.row0 + r;
-                    const int sees = t.shared ? t.len : per + rr / b.group;
+                    const int sees = t.shared ? t.len : per + over_group(b, rr);
                     const bool empty = sees <= 0 && !t.pre_len;
                     float out[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         out[k] = empty ? 0.f : v[k] / sum;
                     const int64_t token = row_token(b, t, rr);
-                    put4((T *)a.y + (token * heads + head * b.group + rr % b.group) * hd + d, out, vec);
+                    put4((T *)a.y + (token * heads + head * b.group + (rr - over_group(b, rr) * b.group)) * hd + d, out, vec);
                 }
             } else {
                 *(f32x4 *)(a.parts[0] + (slot * kNarrowRows + r) * DP + d) = v;
@@ -902,7 +923,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
         F q[NS];
         {
             const int token = row_token(b, t, row);
-            const T *p = (const T *)a.q + ((int64_t)token * heads + head * b.group + row % b.group) * hd;
+            const T *p = (const T *)a.q + ((int64_t)token * heads + head * b.group + (row - over_group(b, row) * b.group)) * hd;
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
                 const int d = 16 * s + 8 * h;
@@ -913,10 +934,10 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
         }
         // own tokens that this lane's row sees, the most of the wave's rows, the fewest and the most of the tile's
         const int per = t.shared ? 0 : t.len - t.q_len + 1;
-        const int see = t.shared ? t.len : per + row / b.group;
-        const int see_wave = t.shared ? t.len : per + (t.row0 + (works ? wl : 0)) / b.group;
-        const int see_min = t.shared ? t.len : per + t.row0 / b.group;
-        const int see_max = t.shared ? t.len : per + (t.row0 + t.rows - 1) / b.group;
+        const int see = t.shared ? t.len : per + over_group(b, row);
+        const int see_wave = t.shared ? t.len : per + over_group(b, t.row0 + (works ? wl : 0));
+        const int see_min = t.shared ? t.len : per + over_group(b, t.row0);
+        const int see_max = t.shared ? t.len : per + over_group(b, t.row0 + t.rows - 1);
         // Blocks of 32 tokens, those of the prefix first: b0..b1-1 are the run's; every row sees whole
         // those before pre_full, and from pre_end on those before own_full.
         constexpr int kPer = kWideUnit / kBlock;
@@ -1245,7 +1266,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                 const bool empty = see <= 0 && !t.pre_len;
                 const float by = empty ? 0.f : 1.f / l;
                 const int64_t token = row_token(b, t, row);
-                T *y = (T *)a.y + (token * heads + head * b.group + row % b.group) * hd;
+                T *y = (T *)a.y + (token * heads + head * b.group + (row - over_group(b, row) * b.group)) * hd;
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -1451,12 +1472,12 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, JoinGrid
         }
         if (live && !sub && d < hd) {
             const int rr = t.row0 + r;
-            const bool empty = t.len - t.q_len + 1 + rr / b.group <= 0 && !t.pre_len && t.prefix < 0;
+            const bool empty = t.len - t.q_len + 1 + over_group(b, rr) <= 0 && !t.pre_len && t.prefix < 0;
             float out[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 out[k] = empty ? 0.f : v[k] / sum;
-            put4((T *)a.y + ((int64_t)(t.token0 + rr / b.group) * heads + head * b.group + rr % b.group) * hd + d,
+            put4((T *)a.y + ((int64_t)(t.token0 + over_group(b, rr)) * heads + head * b.group + (rr - over_group(b, rr) * b.group)) * hd + d,
                  out, vec);
         }
     }

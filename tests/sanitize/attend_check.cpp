@@ -115,7 +115,7 @@ static void check_plan(const Batch &in, bool ordered)
     for (int i = 0; i < N; ++i) {
         (i < b.n_seqs ? claimed : shared) += ent[i].rows / b.group;
         for (int j = 0; j < ent[i].tiles; ++j)
-            all_units += tile_of(ent[i], j, b.group, 0).units;
+            all_units += tile_of(b, ent[i], j, 0).units;
     }
     const int32_t count[4] = {(int32_t)tiles[0], (int32_t)tiles[1], (int32_t)kept[0], (int32_t)kept[1]};
     const bool fits = attend_fits(b, claimed, shared, all_units, count);
@@ -140,7 +140,7 @@ static void check_plan(const Batch &in, bool ordered)
             if (i < b.n_seqs && ent[i].prefix >= 0)
                 list0 = (int)list_before[i];
             for (int j = 0; j < ent[i].tiles; ++j) {
-                AttendTile t = tile_of(ent[i], j, b.group, list0);
+                AttendTile t = tile_of(b, ent[i], j, list0);
                 CHECK((int64_t)all[l].size() == tiles_before[l][i] + j);
                 t.kept = ent[i].keeps ? (int32_t)kept_before[l][i] + j : -1;
                 CHECK(t.rows >= 1 && t.rows <= list_rows(l) && t.units >= 1);
@@ -219,7 +219,7 @@ static void plans()
         current = "plan";
         Batch x;
         AttendBatch &b = x.b;
-        b.group = groups[pick(0, 10)];
+        set_group(b, groups[pick(0, 10)]);
         b.kv_heads = pick(1, 9);
         b.page_shift = pick(5, 8);
         b.wide = pick(0, 1);
@@ -257,6 +257,23 @@ static void plans()
                     e = wild[pick(0, 10)];
         y.link(start);
         check_plan(y, false);
+    }
+}
+
+static void division()
+{
+    current = "division by the heads of a key-value head";
+    AttendBatch b{};
+    std::mt19937 rng(3);
+    for (int g = 1; g <= 1024; ++g) {
+        set_group(b, g);
+        for (int k = 0; k < 2000; ++k) {
+            const int32_t x = k < 1000 ? k : k < 1500 ? (int32_t)(rng() >> 1) : (int32_t)(rng() >> 1) / g * g - k % 2;
+            if (x >= 0)
+                CHECK(over_group(b, x) == x / g);
+        }
+        for (int64_t x : {2147483647ll, 2147483646ll, 2147483647ll / g * g, 2147483647ll / g * g - 1})
+            CHECK(over_group(b, (int32_t)x) == x / g);
     }
 }
 
@@ -309,6 +326,7 @@ static void expect(int got, int want, const char *what)
 int main()
 {
     plans();
+    division();
     layout();
     const int bad = LORA_ERR_INVALID_ARGUMENT;
     lora_rotary rot;
