@@ -649,8 +649,9 @@ int lora_cache_store(lora_ctx *ctx, lora_cache *cache, const void *k, const void
 int lora_cache_load(lora_ctx *ctx, const lora_cache *cache, const int32_t *slots, void *k,
                     void *v, int32_t n_tokens, void *stream);
 
-/* Limit of the requests, and of the prefixes, of one batch. */
+/* Limits of the requests and of the prefixes of one batch. */
 #define LORA_ATTEND_MAX_SEQS (1 << 20)
+#define LORA_ATTEND_MAX_PREFIXES 1024
 
 /*
  * The requests of one batch and what each attends to.  Arrays are int32 device memory of the

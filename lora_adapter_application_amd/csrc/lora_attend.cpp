@@ -348,8 +348,9 @@ int do_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads, c
                     batch->n_tokens, q_heads);
     if (batch->n_seqs < 0 || batch->n_prefixes < 0 || batch->max_pages < 0 || batch->prefix_max_pages < 0)
         return fail(ctx, LORA_ERR_INVALID_ARGUMENT, "a size of the batch is negative");
-    if (batch->n_seqs > LORA_ATTEND_MAX_SEQS || batch->n_prefixes > LORA_ATTEND_MAX_SEQS)
-        return fail(ctx, LORA_ERR_INVALID_ARGUMENT, "%d requests or %d prefixes exceed LORA_ATTEND_MAX_SEQS",
+    if (batch->n_seqs > LORA_ATTEND_MAX_SEQS || batch->n_prefixes > LORA_ATTEND_MAX_PREFIXES)
+        return fail(ctx, LORA_ERR_INVALID_ARGUMENT,
+                    "%d requests or %d prefixes exceed LORA_ATTEND_MAX_SEQS or LORA_ATTEND_MAX_PREFIXES",
                     batch->n_seqs, batch->n_prefixes);
     if (batch->max_queries < 1)
         return fail(ctx, LORA_ERR_INVALID_ARGUMENT, "max_queries %d < 1", batch->max_queries);
@@ -396,7 +397,7 @@ int do_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads, c
         }
         // most tiles times most units of one
         const double most = ((double)b.max_pages + b.prefix_max_pages) * (1 << v.page_shift) / kWideUnit + 2;
-        b.units_fit = (double)(cap[0] + cap[1]) * most < (double)(1 << 30);
+        b.units_fit = (double)(cap[0] + cap[1]) * most < (double)(1 << 29);
         AttendState cut;
         const size_t bytes = cut_workspace(nullptr, b, cut, v.dp);
         DeviceGuard guard(ctx->device);

@@ -134,7 +134,7 @@ struct AttendBatch {
     int32_t page_shift;
     int32_t wide;                // wide tiles may be used
     int32_t workers[2];          // of the lists' kernels
-    int32_t units_fit;           // no batch of these sizes has more than 2^30 units
+    int32_t units_fit;           // no batch of these sizes has more than 2^29 units
     uint32_t group_mul, group_shift;   // x / group is (x + the high word of x group_mul) >> group_shift
     int32_t simple;              // planned by each launch for itself (simple_batch)
     // workspace, all written by the plan
@@ -203,7 +203,12 @@ struct AttendEntity {
 };
 
 __host__ __device__ inline int units_for(int64_t tokens, int unit) { return (int)((tokens + unit - 1) / unit); }
-__host__ __device__ inline int64_t worker_run(int64_t total, int workers) { return (total + workers - 1) / workers; }
+// total / workers rounded up, for workers a multiple of 256 and total below 2^39, by a division of 32 bits
+__host__ __device__ inline int32_t worker_run(int64_t total, int workers)
+{
+    const uint32_t k = (uint32_t)workers >> 8;
+    return (int32_t)(((uint32_t)((total + 255) >> 8) + k - 1) / k);
+}
 __host__ __device__ inline int list_rows(int l) { return l ? kWideRows : kNarrowRows; }
 __host__ __device__ inline int list_unit(int l) { return l ? kWideUnit : kNarrowUnit; }
 __host__ __device__ inline int share_rows(int group) { return group > kShareRows ? group : kShareRows; }
@@ -317,12 +322,12 @@ __host__ __device__ inline AttendTile tile_of(const AttendBatch &b, const Attend
 }
 
 // Whether a batch may be worked on: no token claimed twice, by requests (`tokens` new ones in all) or by
-// prefixes (`listed`), no more than 2^30 units, and then, as the capacities are made, every list
+// prefixes (`listed`), no more than 2^29 units, and then, as the capacities are made, every list
 // within its own (count: tiles of the lists, kept tiles, ...).
 __host__ __device__ inline bool attend_fits(const AttendBatch &b, unsigned long long tokens, unsigned long long listed,
                                             unsigned long long units, const int32_t *count)
 {
-    return tokens <= (unsigned long long)b.n_tokens && listed <= (unsigned long long)b.n_tokens && units <= 1ull << 30 &&
+    return tokens <= (unsigned long long)b.n_tokens && listed <= (unsigned long long)b.n_tokens && units <= 1ull << 29 &&
            count[0] <= b.cap[0] && count[1] <= b.cap[1] && count[2] <= b.kept_cap[0] && count[3] <= b.kept_cap[1];
 }
 

@@ -33,7 +33,6 @@ constexpr float kRaise = 8.f;        // a maximum is raised when a score passes 
 
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanUnits = 2048;     // tiles of a list whose first units stand in LDS for the workers' search
-constexpr int kPlanPrefixes = 512;   // prefixes whose bounds and lengths stand in LDS
 constexpr int kPlanSeqs = 2048;      // requests whose listed tokens stand in LDS
 constexpr int kPlanEach = 4;         // tiles a thread writes by itself; a wave writes those of larger entities
 
@@ -77,8 +76,10 @@ __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b
     constexpr int threads = kPlanThreads, waves = kPlanWaves;
     __shared__ int32_t wave_sum[7][kPlanWaves];
     __shared__ int32_t unit0[2][kPlanUnits];
-    __shared__ int32_t bounds[kPlanPrefixes + 1], pre_len[kPlanPrefixes];
-    __shared__ int32_t large[kPlanThreads], large_at[kPlanThreads][4], n_large;
+    __shared__ int32_t bounds[LORA_ATTEND_MAX_PREFIXES + 1], pre_len[LORA_ATTEND_MAX_PREFIXES];
+    __shared__ AttendEntity large[kPlanThreads];
+    __shared__ unsigned long long large_units[kPlanThreads];
+    __shared__ int32_t large_at[kPlanThreads][4], n_large;
     __shared__ int32_t listed_before[kPlanSeqs + 1];
     __shared__ unsigned long long sums[3];   // new tokens, tokens listed for prefixes, units
     __shared__ int bad_any;
@@ -89,21 +90,26 @@ __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b
         words = request_words(b, tid);
     const bool small = b.n_seqs <= kPlanSeqs;
     const int entities = b.n_seqs + b.n_prefixes;
-    const int32_t *before = small ? listed_before : b.list_before;
+    // (no pointer to either: a read through that would wait for every write under way)
+    auto before = [&](int i) {
+        if (small)
+            return listed_before[i];
+        return b.list_before[i];
+    };
     if (tid < 3)
         sums[tid] = 0;
     if (!tid) {
         bad_any = 0;
         n_large = 0;
     }
-    AttendBatch c = b;                   // with the prefixes' bounds and lengths from LDS, if they fit
-    if (b.n_prefixes && b.n_prefixes <= kPlanPrefixes) {
+    AttendBatch c = b;                   // with the prefixes' bounds and lengths from LDS
+    c.prefix_seqs = bounds;
+    c.prefix_lengths = pre_len;
+    if (b.n_prefixes) {
         for (int i = tid; i <= b.n_prefixes; i += threads)
             bounds[i] = b.prefix_seqs[i];
         for (int i = tid; i < b.n_prefixes; i += threads)
             pre_len[i] = b.prefix_lengths[i];
-        c.prefix_seqs = bounds;
-        c.prefix_lengths = pre_len;
     }
     lds_sync();
     bool bad = false;
@@ -165,8 +171,8 @@ __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b
         const int p = i - b.n_seqs, s0 = c.prefix_seqs[p], s1 = c.prefix_seqs[p + 1];
         *flag |= s0 < 0 || s1 < s0 || s1 > b.n_seqs;
         const int lo = clamp_to(s0, 0, b.n_seqs), hi = clamp_to(s1, lo, b.n_seqs);
-        const int l0 = before[lo];
-        return prefix_of_batch(c, p, l0, before[hi] - l0, flag);
+        const int l0 = before(lo);
+        return prefix_of_batch(c, p, l0, before(hi) - l0, flag);
     };
     int32_t base[6] = {};
     unsigned long long sum[3] = {};
@@ -174,14 +180,38 @@ __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b
         const int i = from + tid;
         PlanCount n{}, at{};
         const bool any = from + wave * 64 < entities;
+        int mine = -1;                                         // the thread's number among the large
         if (any) {
             if (i >= entities)
                 e = AttendEntity{};
             else if (from || i >= b.n_seqs || !b.n_prefixes || b.n_seqs > threads)   // else as found above
                 e = entity_of(i, from && i < b.n_seqs ? request_words(b, i) : words, &bad);
+            if (e.tiles > kPlanEach) {
+                mine = atomicAdd(&n_large, 1);                 // their order changes no place
+                large[mine] = e;
+            }
+        }
+        lds_sync();
+        const int count = n_large;
+        if (count) {                                           // their units, a wave each
+            for (int k = wave; k < count; k += waves) {
+                unsigned long long units = 0;
+                for (int j = lane; j < large[k].tiles; j += 64)
+                    units += tile_of(b, large[k], j, 0).units;
+                for (int d = 1; d < 64; d <<= 1)
+                    units += __shfl_xor(units, d);
+                if (!lane)
+                    large_units[k] = units;
+            }
+            lds_sync();
+        }
+        if (any) {
             unsigned long long units = 0;
-            for (int j = 0; j < e.tiles; ++j)
-                units += tile_of(b, e, j, 0).units;
+            if (mine >= 0)
+                units = large_units[mine];
+            else
+                for (int j = 0; j < e.tiles; ++j)
+                    units += tile_of(b, e, j, 0).units;
             sum[0] += e.shared ? 0 : e.q_len;
             sum[1] += e.shared ? over_group(b, e.rows) : 0;
             sum[2] += units;
@@ -211,16 +241,14 @@ __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b
         if (any && i < entities) {
             const int l = e.list, tile = l ? at.v[1] : at.v[0];
             const int kept = l ? at.v[3] : at.v[2], u0 = l ? at.v[5] : at.v[4];
-            const int list0 = e.prefix >= 0 ? before[i] : 0;
+            const int list0 = e.prefix >= 0 ? before(i) : 0;
             if (i >= b.n_seqs)
                 b.prefix_tile[i - b.n_seqs] = PrefixTile{l, tile};
-            if (e.tiles > kPlanEach) {
-                const int k = atomicAdd(&n_large, 1);          // their order changes no place
-                large[k] = i;
-                large_at[k][0] = tile;
-                large_at[k][1] = kept;
-                large_at[k][2] = u0;
-                large_at[k][3] = list0;
+            if (mine >= 0) {
+                large_at[mine][0] = tile;
+                large_at[mine][1] = kept;
+                large_at[mine][2] = u0;
+                large_at[mine][3] = list0;
             } else {
                 int u = u0;
                 for (int j = 0; j < e.tiles && (uint32_t)(tile + j) < (uint32_t)b.cap[l]; ++j) {
@@ -234,14 +262,12 @@ __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b
                 }
             }
         }
-        lds_sync();
-        const int count = n_large;
         if (!count)
             continue;
+        lds_sync();
         for (int k = wave; k < count; k += waves) {
-            const int id = large[k], tile = large_at[k][0], kept = large_at[k][1];
-            bool again = false;
-            const AttendEntity g = entity_of(id, id < b.n_seqs ? request_words(b, id) : Request{}, &again);
+            const int tile = large_at[k][0], kept = large_at[k][1];
+            const AttendEntity g = large[k];
             int u = large_at[k][2];
             for (int j0 = 0; j0 < g.tiles; j0 += 64) {
                 const int j = j0 + lane;
@@ -287,8 +313,8 @@ __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b
     const int l = wave >= kPlanWaves / 2;                      // half of the threads for each list
     AttendList out{none ? 0 : l ? base[1] : base[0], none ? 0 : l ? base[5] : base[4], none ? 0 : l ? base[3] : base[2], 1};
     const int workers = l ? b.workers[1] : b.workers[0];
-    const int64_t all = (int64_t)out.units * b.kv_heads, run = worker_run(all, workers);
-    out.run = run < 1 ? 1 : (int32_t)run;
+    const int64_t all = (int64_t)out.units * b.kv_heads;
+    out.run = all ? worker_run(all, workers) : 1;
     if (tid == l * (kPlanThreads / 2))
         b.plan->list[l] = out;
     for (int w = tid & (kPlanThreads / 2 - 1); w < workers; w += kPlanThreads / 2) {
@@ -297,14 +323,19 @@ __global__ __launch_bounds__(kPlanThreads) void attend_plan_kernel(AttendBatch b
             break;
         const int32_t want = (int32_t)(u >> 32 ? u % out.units : (uint32_t)u % (uint32_t)out.units);
         int lo = 0, hi = out.tiles - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            const int32_t v = mid < kPlanUnits ? unit0[l][mid] : b.tiles[l][mid].unit0;
-            if (v <= want)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
+        auto search = [&](auto &&first_unit) {
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (first_unit(mid) <= want)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+        };
+        if (out.tiles <= kPlanUnits)
+            search([&](int k) { return unit0[l][k]; });
+        else
+            search([&](int k) { return b.tiles[l][k].unit0; });
         b.start[l][w] = lo;
     }
     if (!tid) {
@@ -547,7 +578,7 @@ __device__ __forceinline__ AttendList plan_simple(const AttendBatch &b, SimplePl
     p.unit0[tid] = before;
     lds_sync();
     all = __builtin_amdgcn_readfirstlane(all);
-    return {b.n_seqs, all, 0, (int32_t)worker_run((int64_t)all * b.kv_heads, b.workers[0])};
+    return {b.n_seqs, all, 0, worker_run((int64_t)all * b.kv_heads, b.workers[0])};
 }
 // The tile with unit u.
 __device__ __forceinline__ int find_simple(const SimplePlan &p, int u, int tiles)

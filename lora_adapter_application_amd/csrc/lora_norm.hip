@@ -204,8 +204,10 @@ hipError_t launch(const NormArgs &a, hipStream_t st)
         lanes *= 2;
     const int each = (items + lanes - 1) / lanes;        // at most 8: head_dim is at most 512
     const int passes = (a.rot.total_heads + 256 / lanes - 1) / (256 / lanes);
-    // enough workgroups for the chip when tokens are few
-    const int split = a.rot.T >= 2048 ? 1 : passes < 2048 / a.rot.T ? passes : 2048 / a.rot.T;
+    // where tokens are few, as many workgroups as the chip's 256 CUs hold at once, so that none waits for
+    // a second round: 5 each of the kernel with most registers, else 8
+    const int hold = 256 * (sizeof(T) == 2 && half ? 5 : 8);
+    const int split = passes < hold / a.rot.T ? passes : hold / a.rot.T;
     const dim3 grid(a.rot.T, split < 1 ? 1 : split);
 #define LORA_NORM(NI) half ? launch_items<T, true, V, NI>(a, lanes, grid, st) : launch_items<T, false, V, NI>(a, lanes, grid, st)
     if (each == 1)

@@ -125,7 +125,7 @@ static void check_plan(const Batch &in, bool ordered)
     } else if (!fits) {
         // nothing but tokens claimed twice and units without end is refused
         CHECK(bad);
-        CHECK(claimed > (unsigned long long)b.n_tokens || shared > (unsigned long long)b.n_tokens || all_units > 1ull << 30);
+        CHECK(claimed > (unsigned long long)b.n_tokens || shared > (unsigned long long)b.n_tokens || all_units > 1ull << 29);
         return;
     }
     std::vector<int> rows_done((size_t)b.n_tokens * b.group, 0);
@@ -149,9 +149,9 @@ static void check_plan(const Batch &in, bool ordered)
                 all[l].push_back(t);
             }
         }
-        CHECK(units <= 1 << 30);
+        CHECK(units <= 1 << 29);
         lists[l] = {(int32_t)all[l].size(), (int32_t)units, (int32_t)kept[l],
-                    (int32_t)std::max<int64_t>(1, worker_run(units * b.kv_heads, b.workers[l]))};
+                    std::max(1, worker_run(units * b.kv_heads, b.workers[l]))};
     }
     for (int l = 0; l < 2; ++l) {
         const AttendList &L = lists[l];
@@ -262,6 +262,13 @@ static void plans()
 
 static void division()
 {
+    current = "a worker's run";
+    std::mt19937_64 big(5);
+    for (int k = 0; k < 20000; ++k) {
+        const int64_t total = (int64_t)(big() >> (25 + k % 39));
+        const int workers = kAttendCus * (1 + k % 4);
+        CHECK(worker_run(total, workers) == (total + workers - 1) / workers);
+    }
     current = "division by the heads of a key-value head";
     AttendBatch b{};
     std::mt19937 rng(3);
