@@ -7,9 +7,10 @@
 // result layout of the first is the operand layout of the second (a lane keeps 8 tokens of one
 // row), so weights go from product to product in registers, and the cache's order makes every
 // operand one contiguous read.  The running maximum m is raised only when a score passes it by
-// 2^8, which keeps weights far inside fp32 and skips most rescalings; sums are fp32.  Weights are
-// rounded to bf16 for the second product of a bf16 ctx, by 2^-8 of a weight at most (as large an error
-// as that of the rounded result); the sum is that of the unrounded ones.
+// 2^8, which keeps weights far inside fp32 and skips most rescalings; sums are fp32.  The second
+// product of a bf16 ctx takes bf16 weights, off by 2^-8 of a weight at most (as large an error as that of
+// the rounded result) in wide tiles, which the matrix cores bound, and by 2^-16 in narrow ones, which
+// the loads bound; the sum is that of the unrounded ones.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -797,7 +798,17 @@ __global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend
                 if constexpr (KIND != kCacheNative)          // a hidden token's scale may be NaN
                     p[j] = MASKED && 8 * g + j >= here ? 0.f : p[j] * vs[j >> 2][j & 3];
             }
+            // of bf16, the weight and what its rounding leaves, 16 bits in all: loads bound this kernel and
+            // the second product costs it under 1%
             const Frag<T> pf = to_frag(p, T());
+            Frag<T> rest{};
+            if constexpr (sizeof(T) == 2) {
+                float r[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    r[j] = p[j] - (float)pf.v[j];
+                rest = to_frag(r, T());
+            }
             Frag<T> sees{};
             if constexpr (MASKED && KIND == kCacheNative)
 #pragma unroll
@@ -812,6 +823,8 @@ __global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend
                         odd_values<T>(v, sees, o[d]);
                 }
                 o[d] = mma(v, pf, o[d]);
+                if constexpr (sizeof(T) == 2)
+                    o[d] = mma(v, rest, o[d]);
             }
         };
         look(u0);
