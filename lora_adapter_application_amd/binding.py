@@ -697,7 +697,8 @@ def lora_profile_end(ctx) -> dict:
 # convenience owners of a ctx and of a cache
 
 class Cache:
-    """A paged cache of a slot pool (Slots.cache)."""
+    """A paged cache of a slot pool (Slots.cache), freed with this object: keep it while a graph
+    that uses it may be replayed."""
 
     def __init__(self, slots, kv_heads, head_dim, pages, page_size, kind):
         self.slots, self.kv_heads, self.head_dim = slots, int(kv_heads), int(head_dim)
@@ -893,9 +894,13 @@ class Slots:
 
     def attend_prepare(self, cache, q_heads, batch, n_tokens=None, stream=None):
         """lora_attend_prepare; n_tokens: the rows of q (default: those of the batch, or one
-        a request)."""
+        a request where it has no q_start)."""
         if n_tokens is None:
-            n_tokens = batch.n_seqs if batch.n_tokens is None else batch.n_tokens
+            n_tokens = batch.n_tokens
+        if n_tokens is None:
+            if batch.q_start is not None:
+                raise ValueError("a batch with q_start needs n_tokens, the rows of q")
+            n_tokens = batch.n_seqs
         self._check_batch(batch)
         lora_attend_prepare(self.ctx, cache.handle, q_heads, batch, n_tokens, stream)
         self._attended = (batch, int(n_tokens), int(q_heads))

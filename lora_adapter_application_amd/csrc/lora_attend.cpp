@@ -319,7 +319,7 @@ size_t cut_workspace(char *base, AttendBatch &b, AttendState &st, int dp)
     c.take(b.listed, b.n_tokens);
     c.take(b.prefix_tile, b.n_prefixes);
     for (int l = 0; l < 2; ++l) {
-        const int64_t rows = b.cap[l] ? part_slots(b.kept_cap[l], b.kv_heads) * list_rows(l) : 0;
+        const int64_t rows = b.cap[l] ? part_slots(b.workers[l], b.kept_cap[l], b.kv_heads) * list_rows(l) : 0;
         c.take(st.sums[l], rows * 2);
         c.take(st.parts[l], rows * dp);
     }
@@ -408,7 +408,8 @@ int do_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads, c
                             "the workspace must grow to %zu bytes: prepare a batch of these sizes once before "
                             "the capture", bytes);
             void *p = nullptr;
-            const size_t more = bytes + bytes / 4;           // not at every batch that is a little larger
+            // not at every batch that is a little larger; all that came before stay below this one
+            const size_t more = std::max(bytes + bytes / 4, 2 * st.bytes);
             if ((rc = device_alloc(ctx, &p, more, "attention workspace")))
                 return rc;
             st.base = (char *)p;

@@ -334,16 +334,16 @@ __host__ __device__ inline bool attend_fits(const AttendBatch &b, unsigned long 
 // Where worker w keeps its part of a tile of key-value head `head`: a kept tile's parts follow
 // those of the tiles before it; of the others a worker has at most two, the one that starts
 // before its run and the one that ends behind it.
-__host__ __device__ inline int64_t part_slot(const AttendList &l, int head, const AttendTile &t, int w)
+__host__ __device__ inline int64_t part_slot(const AttendList &l, int workers, int head, const AttendTile &t, int w)
 {
     if (t.kept >= 0)
-        return 2ll * kAttendWorkers + (int64_t)head * l.kept + t.kept + w;
+        return 2ll * workers + (int64_t)head * l.kept + t.kept + w;
     const int64_t at = (int64_t)head * l.units + t.unit0;
     return 2ll * w + (at < (int64_t)w * l.run ? 0 : 1);
 }
-__host__ __device__ inline int64_t part_slots(int kept_cap, int kv_heads)
+__host__ __device__ inline int64_t part_slots(int workers, int kept_cap, int kv_heads)
 {
-    return 3ll * kAttendWorkers + (int64_t)kept_cap * kv_heads;
+    return 3ll * workers + (int64_t)kept_cap * kv_heads;
 }
 __host__ __device__ inline int first_worker(const AttendList &l, int head, const AttendTile &t)
 {

@@ -9,8 +9,7 @@
 // operand one contiguous read.  The running maximum m is raised only when a score passes it by
 // 2^8, which keeps weights far inside fp32 and skips most rescalings; sums are fp32.  The second
 // product of a bf16 ctx takes bf16 weights, off by 2^-8 of a weight at most (as large an error as that of
-// the rounded result) in wide tiles, which the matrix cores bound, and by 2^-16 in narrow ones, which
-// the loads bound; the sum is that of the unrounded ones.
+// the rounded result), in narrow tiles of 8-bit values by 2^-16; the sum is that of the unrounded ones.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -798,11 +797,13 @@ __global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend
                 if constexpr (KIND != kCacheNative)          // a hidden token's scale may be NaN
                     p[j] = MASKED && 8 * g + j >= here ? 0.f : p[j] * vs[j >> 2][j & 3];
             }
-            // of bf16, the weight and what its rounding leaves, 16 bits in all: loads bound this kernel and
-            // the second product costs it under 1%
+            // Of codes, which are finite, also what the weight's rounding leaves, 16 bits in all: loads bound
+            // this kernel and the second product costs it under 1%.  (Times an infinity it would be of
+            // any sign, or 0.)
+            constexpr bool FINE = sizeof(T) == 2 && KIND != kCacheNative;
             const Frag<T> pf = to_frag(p, T());
             Frag<T> rest{};
-            if constexpr (sizeof(T) == 2) {
+            if constexpr (FINE) {
                 float r[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -823,7 +824,7 @@ __global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend
                         odd_values<T>(v, sees, o[d]);
                 }
                 o[d] = mma(v, pf, o[d]);
-                if constexpr (sizeof(T) == 2)
+                if constexpr (FINE)
                     o[d] = mma(v, rest, o[d]);
             }
         };
@@ -862,7 +863,7 @@ __global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend
         }
         __syncthreads();
         const bool whole = t.kept < 0 && u0 == 0 && u1 == t.units;
-        const int64_t slot = part_slot(list, head, t, w);
+        const int64_t slot = part_slot(list, b.workers[0], head, t, w);
         for (int i = threadIdx.x; i < t.rows * (DP / 4); i += 256) {
             const int r = i / (DP / 4), d = i % (DP / 4) * 4;
             float top = kNone, sum = 0;
@@ -1324,7 +1325,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                             put4(y + dim, out, vec);
                     }
             } else {
-                const int64_t slot = part_slot(list, head, t, w) * kWideRows + wr + n;
+                const int64_t slot = part_slot(list, b.workers[1], head, t, w) * kWideRows + wr + n;
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -1372,6 +1373,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, JoinGrid
         list = plan_simple(b, own);
         const int x = blockIdx.x / grid.heads;
         head = blockIdx.x % grid.heads;
+        if (x >= list.tiles)
+            return;
         t = simple_tile(x, own.len[x], b.group, own.unit0[x]);
     } else if (!l) {
         list = b.plan->list[0];
@@ -1434,7 +1437,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, JoinGrid
         split *= 2;
     const int lane = threadIdx.x % NL, sub = grp % split, d = lane * 4;
     const int n_own = w1 - w0 + 1;
-    const int64_t own_at = part_slot(list, head, t, w0);
+    const int64_t own_at = part_slot(list, b.workers[l], head, t, w0);
     for (int r0 = row0; r0 < row_end; r0 += per_head / split) {
         const int r = r0 + grp / split;
         const bool live = joins && r < row_end;
@@ -1449,7 +1452,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, JoinGrid
                 const AttendTile s = b.tiles[pre.list][pre.tile + pr / PR];
                 const int s0 = first_worker(shared, head, s);
                 n += last_worker(shared, head, s) - s0 + 1;
-                pre_at = part_slot(shared, head, s, s0);
+                pre_at = part_slot(shared, b.workers[pre.list], head, s, s0);
                 pr %= PR;
             }
             for (int k0 = 0; k0 < n; k0 += NL * split) {

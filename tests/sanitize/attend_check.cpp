@@ -156,7 +156,7 @@ static void check_plan(const Batch &in, bool ordered)
     for (int l = 0; l < 2; ++l) {
         const AttendList &L = lists[l];
         std::set<int64_t> used;
-        const int64_t slots = part_slots(b.kept_cap[l], b.kv_heads);
+        const int64_t slots = part_slots(b.workers[l], b.kept_cap[l], b.kv_heads);
         int64_t total = 0;
         for (int h = 0; h < b.kv_heads; ++h)
             for (const AttendTile &t : all[l]) {
@@ -169,7 +169,7 @@ static void check_plan(const Batch &in, bool ordered)
                     total += e - a;
                     if (t.kept < 0 && w0 == w1)
                         continue;                            // written whole
-                    const int64_t s = part_slot(L, h, t, w);
+                    const int64_t s = part_slot(L, b.workers[l], h, t, w);
                     CHECK(s >= 0 && s < slots);
                     CHECK(used.insert(s).second);
                 }

@@ -88,6 +88,9 @@ CASES = [
     # many tiles of few rows: several key-value heads are joined together
     ("bf16", "native", 5, 5, 64, 32, [1] * 300, [i % 70 for i in range(300)], [(3, 290, 140)]),
     ("bf16", "fp8", 6, 3, 128, 32, [1] * 400, [i % 50 for i in range(400)], [(0, 400, 300)]),
+    # more requests than a workgroup has threads, than the plan keeps in LDS
+    ("bf16", "native", 2, 1, 64, 32, [1] * 1300, [1 + i % 9 for i in range(1300)], [(0, 700, 40), (700, 1290, 33)]),
+    ("bf16", "int8", 2, 1, 64, 32, [1, 0, 2] * 900, [2 + i % 9 for i in range(2700)], [(0, 1200, 40), (1200, 2600, 33)]),
     # more work than workers
     ("bf16", "native", 32, 32, 64, 32, [1] * 70, [5 * i + 1 for i in range(70)], [(10, 60, 200)]),
 ]
@@ -196,6 +199,26 @@ def test_infinities_and_nans_stay_with_the_rows_that_see_them():
                         "value nan": torch.isnan(hot)}[what].all(), (what, n)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("queries,length,pre", [([1], 300, 0), ([2], 200, 70), ([40], 300, 0), ([90], 200, 70)])
+def test_infinite_values_that_every_row_sees(dtype, queries, length, pre):
+    """In blocks without hidden tokens: an infinity makes its dim that of every row, both signs and a
+    NaN make it NaN, no other dim changes."""
+    r = Requests(19, dtype, "native", 4, 2, 64, 32, queries, [length], [(0, 1, pre)] if pre else [])
+    clean, _, _ = attended(r)
+    at = r.slots_of(r.prefix_table[0], pre) if pre else r.slots_of(r.table[0], 64)
+    r.v[at[3], 0, 5], r.v[at[9], 0, 6] = math.inf, -math.inf
+    r.v[at[3], 0, 7], r.v[at[40], 0, 7] = math.inf, -math.inf
+    r.v[at[50], 0, 8] = math.nan
+    y, _, _ = attended(r)
+    got, ok = y.cpu().view(-1, 2, 2, 64).float(), clean.cpu().view(-1, 2, 2, 64).float()
+    assert torch.equal(got[:, 1], ok[:, 1])
+    rest = [d for d in range(64) if d not in (5, 6, 7, 8)]
+    assert torch.equal(got[:, 0][..., rest], ok[:, 0][..., rest])
+    assert (got[:, 0, :, 5] == math.inf).all() and (got[:, 0, :, 6] == -math.inf).all()
+    assert torch.isnan(got[:, 0, :, 7:9]).all()
+
+
 @pytest.mark.parametrize("kind", ["fp8", "int8"])
 def test_a_coded_head_with_a_nan(kind):
     r = Requests(9, "bf16", kind, 4, 2, 64, 32, [40], [70])
@@ -282,6 +305,9 @@ def test_arrays_out_of_range_are_clamped_and_flagged():
             (lambda b: b.lengths.__setitem__(1, big), binding.LORA_FLAG_ATTEND_BATCH, [0, 2, 3, 4, 5]),
             (lambda b: b.lengths.__setitem__(1, low), binding.LORA_FLAG_ATTEND_BATCH, [0, 2, 3, 4, 5]),
             (lambda b: b.q_start.__setitem__(6, big), binding.LORA_FLAG_ATTEND_BATCH, [0, 1, 2, 3, 4, 5]),
+            (lambda b: b.q_start.__setitem__(6, low), binding.LORA_FLAG_ATTEND_BATCH, [0, 1, 2, 3, 4]),
+            (lambda b: b.q_start.__setitem__(3, 4), binding.LORA_FLAG_ATTEND_BATCH, [0, 1, 2, 4, 5]),   # two of at most one
+            (lambda b: b.q_start.__setitem__(1, 6), binding.LORA_FLAG_ATTEND_BATCH, [0, 2, 3, 4, 5]),
             (lambda b: b.prefix_seqs.__setitem__(1, 1000), binding.LORA_FLAG_ATTEND_BATCH, [0, 1, 2]),
             (lambda b: b.prefix_lengths.__setitem__(0, big), binding.LORA_FLAG_ATTEND_BATCH, [3, 4, 5]),
             (lambda b: b.pages.__setitem__((4, 1), r.pages), binding.LORA_FLAG_CACHE_PAGE, [0, 1, 2, 3, 5]),
