@@ -564,6 +564,12 @@ int lora_rotary_group(lora_ctx *ctx, const lora_rotary *rotary, int32_t n,
                       const int32_t *modules, const void *const *x, void *const *y,
                       const int32_t *positions, int32_t n_tokens, void *stream);
 
+/*
+ * Between a layer's projections: head norms with rotary positions, a paged cache of keys and
+ * values, and attention over it.  These calls use no slot and no plan of tokens by slot, and
+ * neither lora_stats nor lora_profile counts them.
+ */
+
 /* Limit of head_dim for lora_norm_rotary_group. */
 #define LORA_NORM_MAX_DIM 512
 

@@ -1,5 +1,6 @@
 """MI355X (gfx950) multi-adapter LoRA apply path, and the frozen part of a layer around it:
-4-bit base products, the gated feed-forward on them, and rotary positions.
+4-bit base products, the gated feed-forward on them, rotary positions with or without norms of
+the heads, a paged cache of keys and values, and attention over it.
 
 The product is the C-ABI library ``liblora_mi355x.so`` (``include/lora_mi355x.h``),
 built from ``csrc/`` by ``build.py``.  ``binding`` is its ctypes binding;

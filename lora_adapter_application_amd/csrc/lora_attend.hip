@@ -30,6 +30,11 @@ constexpr float kRaise = 8.f;        // a maximum is raised when a score passes 
 
 // ---------------------------------------------------------------------------
 // plan: one workgroup turns the batch's lengths into the two lists of tiles
+//
+// 256 to 512 requests take 9 to 11 us, latency throughout: lengths, counts, sums over the workgroup,
+// tiles, the search for each worker's first tile, a barrier between each.  One workgroup, because
+// several would have to wait for each other's sums, about a launch each; sums in LDS and registers,
+// because a barrier that also waits for memory costs 1 us.
 
 constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanUnits = 2048;     // tiles of a list whose first units stand in LDS for the workers' search
@@ -552,6 +557,8 @@ __device__ __forceinline__ int div_small(int64_t at, int32_t units)
 
 // ---------------------------------------------------------------------------
 // simple batches: a workgroup sums the requests' units itself, one a thread
+//
+// Saves the plan's launch, 9 us of what is 18 for a single token over 2047 others without it.
 
 struct SimplePlan {
     int32_t len[kSimpleSeqs], unit0[kSimpleSeqs], sum[4];
@@ -596,6 +603,16 @@ __device__ __forceinline__ int find_simple(const SimplePlan &p, int u, int tiles
 
 // ---------------------------------------------------------------------------
 // narrow tiles: 16 rows, four waves on 32 tokens each of a unit of 128
+//
+// For rows so few that reading the cache is the work: 16 is the least that a matrix instruction takes,
+// and the waves split the tokens, since all of them need the same few rows.  Operands go from memory
+// to registers, no LDS between; the four waves' results meet in LDS once a tile.  Bytes bound it where
+// there are enough: 256 requests of up to 2048 and 8 prefixes, fp8, 440 us (5.1 TB/s); one token over 2047,
+// 12 us, one or two units a worker: the chain page, keys, scores, values, sums, part.  With heads in
+// groups of 8 half of the 16 rows carry nothing and conversions of codes count too (512 requests,
+// int8, 271 thousand tokens of 8 heads, 146 us, 3.9 TB/s).  Not kept: fetching the next block's keys ahead within the wave costs the
+// registers of the other workgroups on the CU (494 to 620 us when it was tried), as do four
+// workgroups a CU at 128 dims of codes (spills, +14%).
 
 // The contribution of values that are infinite or NaN, for blocks of which rows see different
 // tokens: a hidden token's weight is 0, and 0 times those is NaN.  Their places are taken out of
@@ -913,10 +930,20 @@ __device__ __forceinline__ f32x16 scaled(f32x16 v, int r, f32x4 f)
 
 // ---------------------------------------------------------------------------
 // wide tiles: 128 rows, four waves on 32 rows each of a unit of 64 tokens
-
-// Blocks of 32 tokens stand in LDS in the order of the cache, as bf16, three of keys and three of
-// values in turn: the waves read one while the next are on their way.  Operands are 32 lanes of 16
-// neighbouring bytes, free of bank conflicts.
+//
+// For rows enough that the products are the work.  Blocks of 32 tokens stand in LDS in the order of
+// the cache, as bf16, three of keys and three of values in turn: the waves read one while the next
+// are on their way.  Operands are 32 lanes of 16 neighbouring bytes, free of bank conflicts.  Codes
+// land in LDS as they are, two blocks further ahead, and the waves turn them into bf16 there, each
+// code once for all 128 rows (through registers instead: 437 to 510 us against 324).
+//
+// Two workgroups a CU, so a SIMD has two waves: the scores of one block are formed beside the weights
+// of the block before it, and one wave's exponentials beside the other's products.  Prompts of 64
+// heads over 4096 shared and up to 1024 own tokens: 1215 us (970 TFLOP/s of what rows see; matrix
+// cores busy 0.48 of the time, vector instructions issued 0.50, together what a SIMD issues); 16
+// prefixes of 16,384 in int8 under 512 requests: 325 us (850 TFLOP/s).  Not kept: units of 64 tokens
+// at once (spills, 1700 us and more), two chains of sums for the scores (+1%), operands six
+// instructions ahead (none).
 template <int KIND, int DP>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(AttendArgs a)
 {
@@ -1349,7 +1376,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
 // A group of lanes takes a row, or a share of its parts where rows are few: each lane fetches the
 // maximum and sum of one part, the weights follow from them, and no load of a part waits for
 // another.  Wide tiles whose parts are kept only where workers part are found by those borders,
-// which are far fewer than the tiles.
+// which are far fewer than the tiles.  The chain tile, borders, maxima, values bounds it: 6 to 11 us
+// where a worker's border parts a tile here and there, 31 us for 512 requests with prefixes and 38 us
+// for 16 long prompts, which have some 67 MB of parts to read each.
 // Where there are many narrow tiles of few rows, a workgroup takes several key-value heads of one.
 struct JoinGrid {
     int32_t narrow, kept, borders;       // workgroups: narrow tiles, wide ones whose parts are kept, borders
