@@ -935,13 +935,13 @@ __device__ __forceinline__ f32x16 scaled(f32x16 v, int r, f32x4 f)
 // the cache, as bf16, three of keys and three of values in turn: the waves read one while the next
 // are on their way.  Operands are 32 lanes of 16 neighbouring bytes, free of bank conflicts.  Codes
 // land in LDS as they are, two blocks further ahead, and the waves turn them into bf16 there, each
-// code once for all 128 rows (through registers instead: 437 to 510 us against 324).
+// code once for all 128 rows (through registers instead: 437 to 510 us against 312).
 //
 // Two workgroups a CU, so a SIMD has two waves: the scores of one block are formed beside the weights
 // of the block before it, and one wave's exponentials beside the other's products.  Prompts of 64
 // heads over 4096 shared and up to 1024 own tokens: 1215 us (970 TFLOP/s of what rows see; matrix
 // cores busy 0.48 of the time, vector instructions issued 0.50, together what a SIMD issues); 16
-// prefixes of 16,384 in int8 under 512 requests: 325 us (850 TFLOP/s).  Not kept: units of 64 tokens
+// prefixes of 16,384 in int8 under 512 requests: 312 us (880 TFLOP/s).  Not kept: units of 64 tokens
 // at once (spills, 1700 us and more), two chains of sums for the scores (+1%), operands six
 // instructions ahead (none).
 template <int KIND, int DP>
@@ -1068,33 +1068,31 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
             if constexpr (CODED)
                 dma4_off(keys, (uint32_t)(2 * kCodes + lane * 4), lds_at + kScales + (k & 7) * 2 * kBlock * 4);
         };
-        // Codes at a place become keys and values in bf16.
-        constexpr int NC = (kBlock * DP / 16 + 255) / 256;   // 16-byte pieces a thread takes of a side
-        struct Held16 { uint4 r[2][NC]; };
+        // Codes at a place become keys and values in bf16, eight at a time: a thread's 8 bytes become
+        // neighbouring 16 (16 and 32 would put every two lanes of a write on the same banks).
+        constexpr int kEights = kBlock * DP / 8, NC = (kEights + 255) / 256;   // of a side; a thread's
+        struct Codes { uint2 r[2][NC]; };
         auto pick = [&](int from) __attribute__((always_inline)) {
-            Held16 x;
+            Codes x;
             if constexpr (CODED)
 #pragma unroll
                 for (int side = 0; side < 2; ++side)
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
-                        if (NC * 256 == kBlock * DP / 16 || tid + 256 * c < kBlock * DP / 16)
-                            x.r[side][c] = *(const uint4 *)(lds + from + side * kCodes + (tid + 256 * c) * 16);
+                        if (NC * 256 == kEights || tid + 256 * c < kEights)
+                            x.r[side][c] = *(const uint2 *)(lds + from + side * kCodes + (tid + 256 * c) * 8);
             return x;
         };
-        auto settle = [&](const Held16 &x, int key_to, int value_to) __attribute__((always_inline)) {
+        auto settle = [&](const Codes &x, int key_to, int value_to) __attribute__((always_inline)) {
             if constexpr (CODED)
 #pragma unroll
                 for (int side = 0; side < 2; ++side)
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        if (NC * 256 != kBlock * DP / 16 && tid + 256 * c >= kBlock * DP / 16)
+                        if (NC * 256 != kEights && tid + 256 * c >= kEights)
                             continue;
-                        const uint4 r = x.r[side][c];
-                        char *to = lds + (side ? value_to : key_to) + (tid + 256 * c) * 32;
-                        const Held<T, CODED ? KIND : kCacheInt8> lo{make_uint2(r.x, r.y)}, hi{make_uint2(r.z, r.w)};
-                        *(bf16x8 *)to = frag_of(lo).v;
-                        *(bf16x8 *)(to + 16) = frag_of(hi).v;
+                        const Held<T, CODED ? KIND : kCacheInt8> eight{x.r[side][c]};
+                        *(bf16x8 *)(lds + (side ? value_to : key_to) + (tid + 256 * c) * 16) = frag_of(eight).v;
                     }
         };
 
@@ -1281,7 +1279,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
             fetch(k + 5, behind, before, CODED ? raw2 : at0, CODED ? raw2 + kCodes : kValues + at2);
             return pick(raw0);
         };
-        auto pass = [&](const Held16 &x) __attribute__((always_inline)) {
+        auto pass = [&](const Codes &x) __attribute__((always_inline)) {
             settle(x, at0, kValues + at2);
             int first = at0;
             at0 = at1;
@@ -1302,7 +1300,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                 raise(cur);
                 for (; k + 1 < stop; ++k) {
                     wait();                                  // all waves are done with block k's keys
-                    const Held16 x = ahead(k);
+                    const Codes x = ahead(k);
                     __builtin_amdgcn_s_setprio(1);           // before the other workgroup's wave and its softmax
                     cur = both(cur, k);
                     __builtin_amdgcn_s_setprio(0);
@@ -1310,7 +1308,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
                     pass(x);
                 }
                 wait();
-                const Held16 x = ahead(k);
+                const Codes x = ahead(k);
                 weights(cur);
                 rescale(cur, 1, k);
                 add_values(cur);
@@ -1372,19 +1370,20 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attend_wide_kernel(Att
 // ---------------------------------------------------------------------------
 // joining parts
 
-// A workgroup takes a narrow tile of a key-value head, or 16 rows of a wide one, four dims a lane.
+// A workgroup takes a narrow tile of a key-value head, or 32 rows of a wide one, four dims a lane
+// (starting workgroups counts: 16 long prompts take 34 us of joining, 39 with 16 rows each, and more with 8).
 // A group of lanes takes a row, or a share of its parts where rows are few: each lane fetches the
 // maximum and sum of one part, the weights follow from them, and no load of a part waits for
 // another.  Wide tiles whose parts are kept only where workers part are found by those borders,
 // which are far fewer than the tiles.  The chain tile, borders, maxima, values bounds it: 6 to 11 us
-// where a worker's border parts a tile here and there, 31 us for 512 requests with prefixes and 38 us
+// where a worker's border parts a tile here and there, 30 us for 512 requests with prefixes and 34 us
 // for 16 long prompts, which have some 67 MB of parts to read each.
 // Where there are many narrow tiles of few rows, a workgroup takes several key-value heads of one.
 struct JoinGrid {
     int32_t narrow, kept, borders;       // workgroups: narrow tiles, wide ones whose parts are kept, borders
     int32_t heads, each;                 // of a narrow tile: workgroups, and key-value heads a workgroup
 };
-constexpr int kJoinRows = 16, kJoinChunks = kWideRows / kJoinRows;
+constexpr int kJoinRows = 32, kJoinChunks = kWideRows / kJoinRows;
 
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, JoinGrid grid)
