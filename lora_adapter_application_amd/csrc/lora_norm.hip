@@ -10,7 +10,7 @@
 // the chain position, sine and cosine, barrier, load, shuffles, store.
 //
 // 64 heads of 128, bf16: 32,556 tokens take 224 us (4.77 TB/s, 0.98 of a copy); 72 heads, 512 tokens
-// 7.3 us; one token 4.5 us, of which the host's call is 3.4.  A lane fetches its next head before the
+// 7.4 us; one token 4.5 us, of which the host's call is 3.4.  A lane fetches its next head before the
 // sums of this one; the registers for that leave four waves a SIMD, and more waves spill (bounds of
 // six 546 us, of eight 899).
 #include <hip/hip_runtime.h>
