@@ -997,10 +997,18 @@ class Slots:
         ctx, handle, qp, yp = self.ctx, cache.handle, _ptr(q), _ptr(y)
         factor = float(cache.head_dim ** -0.5 if scale is None else scale)
         refs = (cache, q, y, batch, s)
+        mine = (batch, n_tok, int(q_heads))
 
         def call():
             _ = refs
-            rc = lib.lora_attend_prepare(ctx, handle, q_heads, ctypes.byref(s), st) if prepare else 0
+            rc = 0
+            if prepare:
+                rc = lib.lora_attend_prepare(ctx, handle, q_heads, ctypes.byref(s), st)
+                if not rc:
+                    self._attended = mine
+            elif self._attended is not None and self._attended[1:] != mine[1:]:
+                raise ValueError("the batch prepared last has %d tokens of %d heads, q %d of %d"
+                                 % (*self._attended[1:], *mine[1:]))
             rc = rc or lib.lora_attend(ctx, handle, qp, yp, factor, st)
             if rc:
                 _check(rc, ctx)

@@ -1393,29 +1393,32 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, JoinGrid
     __shared__ float lds_m[NG], lds_l[NG];
     __shared__ SimplePlan own;
     const AttendBatch &b = a.b;
-    const int l = (int)blockIdx.x >= grid.narrow;
+    const int block = blockIdx.y * gridDim.x + blockIdx.x;   // rows of a grid: one holds 2^32 threads at most
+    if (block >= grid.narrow + grid.kept + grid.borders)
+        return;
+    const int l = block >= grid.narrow;
     AttendList list, other{};
     AttendTile t;
     int head, chunk = 0, w0, w1;
     if (b.simple) {
         list = plan_simple(b, own);
-        const int x = blockIdx.x / grid.heads;
-        head = blockIdx.x % grid.heads;
+        const int x = block / grid.heads;
+        head = block % grid.heads;
         if (x >= list.tiles)
             return;
         t = simple_tile(x, own.len[x], b.group, own.unit0[x]);
     } else if (!l) {
         list = b.plan->list[0];
         other = b.plan->list[1];
-        const int x = blockIdx.x / grid.heads;
-        head = blockIdx.x % grid.heads;
+        const int x = block / grid.heads;
+        head = block % grid.heads;
         t = b.tiles[0][x];                                   // stale where x is past the list
         if (x >= list.tiles)
             return;
     } else {
         list = b.plan->list[1];
         other = b.plan->list[0];
-        const int i = blockIdx.x - grid.narrow, kept = i < grid.kept;
+        const int i = block - grid.narrow, kept = i < grid.kept;
         chunk = (kept ? i : i - grid.kept) % kJoinChunks;
         const int k = (kept ? i : i - grid.kept) / kJoinChunks;
         if (kept) {
@@ -1608,7 +1611,8 @@ hipError_t launch_all(const AttendArgs &a, hipStream_t st)
     grid.narrow = a.b.cap[0] * grid.heads;
     grid.kept = a.b.n_prefixes && a.b.group > kShareRows ? a.b.cap[1] * a.b.kv_heads * kJoinChunks : 0;
     grid.borders = a.b.cap[1] ? (a.b.workers[1] - 1) * kJoinChunks : 0;
-    const int all = grid.narrow + grid.kept + grid.borders;
+    const int blocks = grid.narrow + grid.kept + grid.borders, across = std::min(blocks, 1 << 22);
+    const dim3 all(across, (blocks + across - 1) / across);
     switch (a.c.dp) {
     case 64: attend_join_kernel<T, 64><<<all, 256, 0, st>>>(a, grid); break;
     case 96: attend_join_kernel<T, 96><<<all, 256, 0, st>>>(a, grid); break;

@@ -400,3 +400,61 @@ def test_empty_batches():
     S.attend(cache, q, y)
     torch.cuda.synchronize()
     assert bool((y == 7).all())
+
+
+def test_more_workgroups_than_a_row_of_a_grid_holds():
+    """2^19 requests of one token and a long last one, on 33 key-value heads: the last tiles' parts
+    are joined by workgroups past 2^24.  Two pages hold the tokens of all requests."""
+    n, kv_heads, group, dim, page, pages = (1 << 19) + 1, 33, 9, 8, 32768, 32
+    heads = kv_heads * group
+    S = binding.Slots(1, 1, [(64, 64)], "bf16", n)
+    cache = S.cache(kv_heads, dim, 2, page)
+    gen = torch.Generator().manual_seed(5)
+    k = torch.zeros(4096, kv_heads * dim, dtype=torch.bfloat16).cuda()
+    total = torch.zeros(kv_heads * dim, dtype=torch.float64)
+    first = None
+    for at in range(0, 2 * page, 4096):                      # a page around 1, the other around 5
+        v = (torch.randn(4096, kv_heads * dim, generator=gen) + (1 if at < page else 5)).bfloat16()
+        total += v.double().sum(0)
+        first = v[0] if first is None else first
+        S.cache_store(cache, k, v.cuda(), torch.arange(at, at + 4096, dtype=torch.int32).cuda())
+    lengths = torch.ones(n, dtype=torch.int32)
+    lengths[-1] = page * pages
+    table = torch.zeros(n, pages, dtype=torch.int32, device="cuda")
+    table[:, pages // 2:] = 1
+    q = torch.zeros(n, heads * dim, dtype=torch.bfloat16, device="cuda")
+    y = torch.full_like(q, 7.0)
+    S.attend_prepare(cache, heads, binding.AttendBatch(lengths.cuda(), table))
+    S.attend(cache, q, y)
+    torch.cuda.synchronize()
+    assert S.flags() == 0
+    spread = first.view(kv_heads, 1, dim).expand(-1, group, -1).reshape(-1).cuda()
+    assert torch.equal(y[:-1], spread.expand(n - 1, -1))
+    # Equal weights, so the mean of the pages.  The weights are 1 and their sum is exact.  A wave adds
+    # 2^18 of the values with a rounding each, of 2^-24 of the sum of their sizes at most (3.1 on
+    # average): 2^-6 x 3.1 < 2^-4 of the mean, which is then rounded to bf16.
+    want = (total / (2 * page)).view(kv_heads, 1, dim).expand(-1, group, -1).reshape(-1)
+    bound = 2.0 ** -8 * want.abs() + 2.0 ** -4
+    assert ((y[-1].double().cpu() - want).abs() <= bound).all()
+    cache.close()
+    S.close()
+
+
+def test_a_bound_call_without_a_plan_of_its_own():
+    r = Requests(31, "bf16", "native", 4, 2, 64, 64, [1] * 5, [100, 1, 257, 60, 5], [])
+    S, cache = r.make()
+    batch, q = r.batch(), r.q.cuda()
+    y, z = torch.empty_like(q), torch.empty_like(q)
+    first = S.bind_attend(cache, 4, q, y, batch)
+    second = S.bind_attend(cache, 4, q, z, batch, prepare=False)
+    fewer = S.bind_attend(cache, 4, q[:2], z[:2], batch, prepare=False)
+    first()
+    second()
+    torch.cuda.synchronize()
+    assert torch.equal(y, z)
+    with pytest.raises(ValueError):
+        fewer()
+    with pytest.raises(ValueError):
+        S.attend(cache, q[:2], z[:2])
+    cache.close()
+    S.close()
