@@ -676,7 +676,7 @@ int lora_cache_load(lora_ctx *ctx, const lora_cache *cache, const int32_t *slots
 typedef struct {
     int32_t n_tokens;               /* rows of q and y */
     int32_t n_seqs;                 /* requests */
-    int32_t max_queries;            /* most new tokens of one request, >= 1 */
+    int32_t max_queries;            /* most new tokens of one request, >= 1 (without q_start it is 1) */
     int32_t max_pages;              /* columns of pages */
     const int32_t *q_start;         /* [n_seqs + 1], ascending, or NULL: request i has token i */
     const int32_t *lengths;         /* [n_seqs], 0..max_pages * page_size */

@@ -386,18 +386,8 @@ int do_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads, c
     b.workers[1] = kAttendCus * (v.dp <= 128 ? 2 : 1);
     b.flags = ctx->ws.plan.flags;
     if (b.n_tokens && b.n_seqs) {
-        b.simple = simple_batch(b);
-        int64_t cap[2], kept[2];
-        attend_capacity(b.n_tokens, b.n_seqs, b.n_prefixes, b.max_queries, b.group, b.wide != 0, cap, kept);
-        for (int l = 0; l < 2; ++l) {
-            if (cap[l] * v.kv_heads * 8 > INT32_MAX / 2 || kept[l] > INT32_MAX / 2)
-                return fail(ctx, LORA_ERR_TOO_MANY_TOKENS, "the batch needs more than 2^27 tiles");
-            b.cap[l] = (int32_t)cap[l];
-            b.kept_cap[l] = (int32_t)kept[l];
-        }
-        // most tiles times most units of one
-        const double most = ((double)b.max_pages + b.prefix_max_pages) * (1 << v.page_shift) / kWideUnit + 2;
-        b.units_fit = (double)(cap[0] + cap[1]) * most < (double)(1 << 29);
+        if (!size_batch(b))
+            return fail(ctx, LORA_ERR_TOO_MANY_TOKENS, "the batch needs more than 2^27 tiles");
         AttendState cut;
         const size_t bytes = cut_workspace(nullptr, b, cut, v.dp);
         DeviceGuard guard(ctx->device);

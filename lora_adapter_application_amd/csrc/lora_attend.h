@@ -385,6 +385,27 @@ inline void attend_capacity(int64_t n_tokens, int64_t n_seqs, int64_t n_prefixes
     }
 }
 
+// What follows from the sizes that the host knows: what the lists can hold, and how the batch is
+// planned.  False: more tiles than are numbered.
+inline bool size_batch(AttendBatch &b)
+{
+    if (!b.q_start)                      // one new token a request, whatever the caller says of the most
+        b.max_queries = 1;
+    b.simple = simple_batch(b);
+    int64_t cap[2], kept[2];
+    attend_capacity(b.n_tokens, b.n_seqs, b.n_prefixes, b.max_queries, b.group, b.wide != 0, cap, kept);
+    for (int l = 0; l < 2; ++l) {
+        if (cap[l] * b.kv_heads * 8 > INT32_MAX / 2 || kept[l] > INT32_MAX / 2)
+            return false;
+        b.cap[l] = (int32_t)cap[l];
+        b.kept_cap[l] = (int32_t)kept[l];
+    }
+    // most tiles times most units of one
+    const double most = ((double)b.max_pages + b.prefix_max_pages) * (1 << b.page_shift) / kWideUnit + 2;
+    b.units_fit = (double)(cap[0] + cap[1]) * most < (double)(1 << 29);
+    return true;
+}
+
 struct AttendArgs {
     AttendBatch b;
     CacheView c;

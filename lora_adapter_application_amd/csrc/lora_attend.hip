@@ -1589,7 +1589,7 @@ template <typename T>
 hipError_t launch_all(const AttendArgs &a, hipStream_t st)
 {
     hipError_t e = hipSuccess;
-    if (a.b.cap[1])
+    if (a.b.cap[1] && !a.b.simple)                           // of a simple batch nobody writes a list of wide tiles
         e = a.c.kind == kCacheNative ? launch_wide<kCacheNative>(a, st)
           : a.c.kind == kCacheFp8 ? launch_wide<kCacheFp8>(a, st)
                                   : launch_wide<kCacheInt8>(a, st);
