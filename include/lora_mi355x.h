@@ -701,7 +701,8 @@ typedef struct {
  * new tokens pad it).  Graphs and eager calls share the workspace and must be ordered, as
  * every other use of the ctx.
  * Values in the arrays that are out of range or out of order are clamped and set
- * LORA_FLAG_ATTEND_BATCH; a batch whose requests claim the same tokens may get no work at all.
+ * LORA_FLAG_ATTEND_BATCH; a batch whose requests claim the same tokens, or of more than 2^35 tokens
+ * to attend to, may get no work at all.
  * Errors: a handle that is no cache of the ctx, sizes out of range, NULL arrays, a workspace
  * too small under capture -> LORA_ERR_INVALID_ARGUMENT; n_tokens > max_tokens or n_tokens *
  * q_heads >= 2^31 -> LORA_ERR_TOO_MANY_TOKENS; LORA_ERR_OUT_OF_MEMORY.

@@ -391,7 +391,6 @@ inline bool size_batch(AttendBatch &b)
 {
     if (!b.q_start)                      // one new token a request, whatever the caller says of the most
         b.max_queries = 1;
-    b.simple = simple_batch(b);
     int64_t cap[2], kept[2];
     attend_capacity(b.n_tokens, b.n_seqs, b.n_prefixes, b.max_queries, b.group, b.wide != 0, cap, kept);
     for (int l = 0; l < 2; ++l) {
@@ -403,6 +402,7 @@ inline bool size_batch(AttendBatch &b)
     // most tiles times most units of one
     const double most = ((double)b.max_pages + b.prefix_max_pages) * (1 << b.page_shift) / kWideUnit + 2;
     b.units_fit = (double)(cap[0] + cap[1]) * most < (double)(1 << 29);
+    b.simple = simple_batch(b) && b.units_fit;               // their sum takes 32 bits
     return true;
 }
 

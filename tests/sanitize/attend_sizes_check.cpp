@@ -61,9 +61,29 @@ static void one_token_each()
                     }
 }
 
+// A launch that plans a batch for itself sums its units in 32 bits: only where no lengths that the
+// table can name have more.
+static void units_of_simple_batches()
+{
+    for (int seqs : {1, 31, 32, 200, 256})
+        for (int page_shift : {5, 10, 20, 30})
+            for (int pages : {1, 8, 2048, 1 << 21, 1 << 26}) {
+                const AttendBatch b = sized(seqs, seqs, 1, 1, true, false, 0, pages, page_shift);
+                const int64_t most = (int64_t)pages << page_shift;
+                bool bad = false;
+                const int held = held_of(INT32_MAX, pages, page_shift, &bad);
+                CHECK(held == (most < INT32_MAX ? most : INT32_MAX), " %d", held);
+                if (b.simple)
+                    CHECK(seqs * (int64_t)simple_tile(0, held, 1, 0).units <= 1 << 29, " %d requests of %d tokens", seqs, held);
+                if (most < (1ll << 33) / seqs)
+                    CHECK(b.simple, " %d requests of %lld tokens", seqs, (long long)most);
+            }
+}
+
 int main()
 {
     one_token_each();
+    units_of_simple_batches();
     std::printf("failures: %d\n", failures);
     return failures != 0;
 }

@@ -47,3 +47,19 @@ def test_single_tokens_without_starts_whatever_the_most_new_tokens(requests, hea
     assert S.flags() == 0
     log(f"  worst error / bound {check_rows(r, y, 64 ** -0.5, before, 'single tokens'):.3f}")
     S.close()
+
+
+def test_more_tokens_than_a_plan_counts():
+    """256 requests that name one page over and over, 2^39 tokens in all: no work, and the flag."""
+    n, page, pages = 256, 32768, 65536
+    S = binding.Slots(1, 1, [(64, 64)], "bf16", 4096)
+    cache = S.cache(1, 8, 1, page, "fp8")
+    table = torch.zeros(n, pages, dtype=torch.int32, device="cuda")
+    q = torch.ones(n, 8, dtype=torch.bfloat16, device="cuda")
+    y = torch.full_like(q, 7.0)
+    S.attend_prepare(cache, 1, binding.AttendBatch(torch.full((n,), 2 ** 31 - 1, dtype=torch.int32, device="cuda"), table))
+    S.attend(cache, q, y)
+    torch.cuda.synchronize()
+    assert S.flags() == binding.LORA_FLAG_ATTEND_BATCH
+    assert bool((y == 7).all())
+    S.close()
