@@ -846,8 +846,10 @@ __global__ __launch_bounds__(256, kAttendPerCu(sizeof(T), KIND, DP)) void attend
             }
         };
         look(u0);
-        const int pre_full = (t.pre_len - (wave + 1) * kBlock + kNarrowUnit) / kNarrowUnit;
-        const int own_full = pre_units + (see_min - (wave + 1) * kBlock + kNarrowUnit) / kNarrowUnit;
+        // units before these have whole blocks of the wave's; rounded down, also below zero
+        static_assert(kNarrowUnit == 128, "");
+        const int pre_full = ((t.pre_len - (wave + 1) * kBlock) >> 7) + 1;
+        const int own_full = pre_units + ((see_min - (wave + 1) * kBlock) >> 7) + 1;
         for (int u = u0; u < u1;) {
             const int full = u < pre_units ? pre_full : own_full;
             const int stop = full < u1 ? full : u1;

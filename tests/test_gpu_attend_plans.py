@@ -63,3 +63,30 @@ def test_more_tokens_than_a_plan_counts():
     assert S.flags() == binding.LORA_FLAG_ATTEND_BATCH
     assert bool((y == 7).all())
     S.close()
+
+
+def test_the_longest_request():
+    """2^31 - 1 tokens, a page over and over: whole blocks are counted up to there.  Equal weights, so
+    the mean of the page, whose last token is counted once less."""
+    page, pages = 32768, 65536
+    S = binding.Slots(1, 1, [(64, 64)], "bf16", page)
+    cache = S.cache(1, 8, 1, page, "fp8")
+    gen = torch.Generator().manual_seed(6)
+    v = torch.randint(1, 8, (page, 8), generator=gen)
+    v[:, 0] = 7                                               # a scale of 2^-6 throughout
+    S.cache_store(cache, torch.zeros(page, 8).bfloat16().cuda(), v.bfloat16().cuda(),
+                  torch.arange(page, dtype=torch.int32).cuda())
+    table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+    q = torch.ones(1, 8, dtype=torch.bfloat16, device="cuda")
+    y = torch.full_like(q, 7.0)
+    S.attend_prepare(cache, 1, binding.AttendBatch(torch.full((1,), 2 ** 31 - 1, dtype=torch.int32, device="cuda"), table))
+    S.attend(cache, q, y)
+    torch.cuda.synchronize()
+    assert S.flags() == 0
+    # The codes of 1..7 in units of 2^-6 are whole numbers, exact.  A wave has 2^31 / 4096 = 2^19 tokens
+    # at most of sums up to 7 times that, a lane a fourth of the tokens: both exact in fp32.  The parts'
+    # sums are rounded about a thousand times, 2^-24 each.
+    want = v.double().mean(0)
+    bound = want * (2.0 ** -8 + 2 * 2.0 ** -14 + 2.0 ** -30)
+    assert ((y[0].double().cpu() - want).abs() <= bound).all(), (y, want)
+    S.close()
