@@ -693,13 +693,14 @@ typedef struct {
  * with q_heads query heads and caches of `cache`'s kv_heads, head_dim and page_size (of any
  * kind): once a step for all layers.  q_heads is a multiple of kv_heads; query head h reads
  * key-value head h / (q_heads / kv_heads).
- * The plan stays valid until the next lora_attend_prepare.  It and the parts of lora_attend
+ * The plan stays valid until the next call of lora_attend_prepare.  It and the parts of lora_attend
  * are kept in the ctx's attention workspace, which grows with the batches prepared.  Under
  * graph capture it cannot grow: prepare a batch of the same sizes once before.  A captured
  * lora_attend needs its lora_attend_prepare in the same capture; the replayed graph reads the
  * batch's arrays as they are then, so it serves every batch of these sizes (requests without
- * new tokens pad it).  Graphs and eager calls share the workspace and must be ordered, as
- * every other use of the ctx.
+ * new tokens pad it).  A replay leaves the plan of a call outside of captures as it is: those of
+ * graphs have a place of their own.  Graphs and eager calls share the rest of the workspace and
+ * must be ordered, as every other use of the ctx.
  * Values in the arrays that are out of range or out of order are clamped and set
  * LORA_FLAG_ATTEND_BATCH; a batch whose requests claim the same tokens, or of more than 2^35 tokens
  * to attend to, may get no work at all.

@@ -3,8 +3,8 @@
 // cache (lora_cache_*) and attention over it (lora_attend_*).
 //
 // A cache is device memory of its ctx, cut in pages whose order and lengths the caller keeps; its
-// calls read and write what their arguments name and keep nothing else.  The attention's plan and
-// parts live in one workspace of the ctx that grows with the batches prepared; a workspace that a
+// calls read and write what their arguments name and keep nothing else.  The attention's plans and
+// parts live in a workspace of the ctx that grows with the batches prepared; memory that a
 // captured graph may use stays allocated until lora_slots_destroy.
 #include <hip/hip_runtime.h>
 
@@ -295,7 +295,7 @@ int do_cache_move(bool store, lora_ctx *ctx, const lora_cache *cache, const void
     return LORA_OK;
 }
 
-// The workspace of one batch, cut from one allocation.
+// What one batch needs, cut from an allocation.
 struct Cut {
     char *base;
     size_t used = 0;
@@ -307,7 +307,7 @@ struct Cut {
     }
 };
 
-size_t cut_workspace(char *base, AttendBatch &b, AttendState &st, int dp)
+size_t cut_plan(char *base, AttendBatch &b)
 {
     Cut c{base};
     c.take(b.plan, 1);
@@ -318,13 +318,22 @@ size_t cut_workspace(char *base, AttendBatch &b, AttendState &st, int dp)
     c.take(b.list_before, (int64_t)b.n_seqs + 1);
     c.take(b.listed, b.n_tokens);
     c.take(b.prefix_tile, b.n_prefixes);
+    return c.used;
+}
+
+size_t cut_parts(char *base, const AttendBatch &b, int dp, float *parts[2], float *sums[2])
+{
+    Cut c{base};
     for (int l = 0; l < 2; ++l) {
         const int64_t rows = b.cap[l] ? part_slots(b.workers[l], b.kept_cap[l], b.kv_heads) * list_rows(l) : 0;
-        c.take(st.sums[l], rows * 2);
-        c.take(st.parts[l], rows * dp);
+        c.take(sums[l], rows * 2);
+        c.take(parts[l], rows * dp);
     }
     return c.used;
 }
+
+// Not at every batch that is a little larger; all that came before stay below this one.
+size_t grown(size_t need, size_t have) { return (std::max(need + need / 4, 2 * have) + 255) / 256 * 256; }
 
 int do_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads, const lora_attend_batch *batch,
                       void *stream)
@@ -388,32 +397,39 @@ int do_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads, c
     if (b.n_tokens && b.n_seqs) {
         if (!size_batch(b))
             return fail(ctx, LORA_ERR_TOO_MANY_TOKENS, "the batch needs more than 2^27 tiles");
-        AttendState cut;
-        const size_t bytes = cut_workspace(nullptr, b, cut, v.dp);
+        float *parts[2], *sums[2];
+        const size_t plan = cut_plan(nullptr, b), rest = cut_parts(nullptr, b, v.dp, parts, sums);
         DeviceGuard guard(ctx->device);
         hipStream_t s = (hipStream_t)stream;
-        if (bytes > st.bytes) {
-            if (any_capture(ctx, s))
-                return fail(ctx, LORA_ERR_INVALID_ARGUMENT,
-                            "the workspace must grow to %zu bytes: prepare a batch of these sizes once before "
-                            "the capture", bytes);
-            void *p = nullptr;
-            // not at every batch that is a little larger; all that came before stay below this one
-            const size_t more = std::max(bytes + bytes / 4, 2 * st.bytes);
-            if ((rc = device_alloc(ctx, &p, more, "attention workspace")))
+        if ((plan > st.plan_bytes || rest > st.parts_bytes) && any_capture(ctx, s))
+            return fail(ctx, LORA_ERR_INVALID_ARGUMENT,
+                        "the workspace must grow to %zu bytes: prepare a batch of these sizes once before "
+                        "the capture", 2 * plan + rest);
+        void *p = nullptr;
+        if (plan > st.plan_bytes) {
+            const size_t more = grown(plan, st.plan_bytes);
+            if ((rc = device_alloc(ctx, &p, 2 * more, "attention plans")))
                 return rc;
-            st.base = (char *)p;
-            st.bytes = more;
+            st.plans = (char *)p;
+            st.plan_bytes = more;
         }
-        cut_workspace(st.base, b, cut, v.dp);
+        if (rest > st.parts_bytes) {
+            const size_t more = grown(rest, st.parts_bytes);
+            if ((rc = device_alloc(ctx, &p, more, "attention parts")))
+                return rc;
+            st.parts_base = (char *)p;
+            st.parts_bytes = more;
+        }
+        cut_plan(st.plans + (capture_of(s) ? st.plan_bytes : 0), b);
+        cut_parts(st.parts_base, b, v.dp, parts, sums);
         if ((rc = before_launch(ctx, s)))
             return rc;
         st.prepared = false;
         if (!b.simple)
             HIP_TRY(ctx, launch_attend_plan(b, s));
         for (int l = 0; l < 2; ++l) {
-            st.parts[l] = cut.parts[l];
-            st.sums[l] = cut.sums[l];
+            st.parts[l] = parts[l];
+            st.sums[l] = sums[l];
         }
     }
     st.capture = capture_of((hipStream_t)stream);

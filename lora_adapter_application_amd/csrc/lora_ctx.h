@@ -70,14 +70,17 @@ struct BatchState {
     const void *last_x[kMaxGroup] = {};   // inputs of the last shrink (saved modules read them)
 };
 
-// The prepared batch of lora_attend and the workspace that its plan and parts are cut from.
+// The prepared batch of lora_attend and the workspace that its plan and parts are cut from.  Plans of
+// captured prepares have a place of their own: a graph that is replayed writes its plan again, and an
+// eager one has to stay.  Parts are of one lora_attend call, and all calls share their place.
 struct AttendState {
     bool prepared = false;
     AttendBatch batch{};
     int head_dim = 0;
     unsigned long long capture = 0;      // the capture its plan was prepared in, or 0
-    char *base = nullptr;
-    size_t bytes = 0;
+    char *plans = nullptr;               // [2][plan_bytes]: eager, captured
+    char *parts_base = nullptr;
+    size_t plan_bytes = 0, parts_bytes = 0;
     float *parts[2] = {}, *sums[2] = {};
 };
 

@@ -90,3 +90,43 @@ def test_the_longest_request():
     bound = want * (2.0 ** -8 + 2 * 2.0 ** -14 + 2.0 ** -30)
     assert ((y[0].double().cpu() - want).abs() <= bound).all(), (y, want)
     S.close()
+
+
+def test_a_replayed_graph_leaves_the_eager_plan():
+    """prepare, replays of graphs with prepares of other batches, then the layers of the eager step."""
+    shapes = [([1] * 40 + [70], list(range(1, 41)) + [90], [(0, 17, 1000), (17, 30, 65)]),
+              ([100, 1, 3], [150, 9, 40], [(0, 2, 300)]),
+              ([1] * 300, [7 * i % 90 for i in range(300)], [(5, 200, 130)])]
+    batches = [Requests(51 + k, "bf16", "fp8", 16, 2, 128, 64, *shape) for k, shape in enumerate(shapes)]
+    S = binding.Slots(1, 1, [(64, 64)], "bf16", 4096)
+    caches = [cache_of(S, r) for r in batches]
+    given = [r.batch() for r in batches]
+    q = [r.q.cuda() for r in batches]
+    y = [torch.full_like(v, 7.0) for v in q]
+    eager = []
+    for k in range(3):
+        S.attend_prepare(caches[k], 16, given[k])
+        S.attend(caches[k], q[k], y[k])
+        torch.cuda.synchronize()
+        check_rows(batches[k], y[k], 128 ** -0.5, y[k], f"batch {k}")
+        eager.append(y[k].clone())
+    graphs, s = [], torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for k in range(3):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            S.attend_prepare(caches[k], 16, given[k])
+            S.attend(caches[k], q[k], y[k])
+    z = [torch.empty_like(v) for v in q]
+    for a in range(3):
+        S.attend_prepare(caches[a], 16, given[a])
+        for b in range(3):
+            y[b].fill_(1.0)
+            graphs[b].replay()
+            z[a].fill_(1.0)
+            S.attend(caches[a], q[a], z[a])
+            torch.cuda.synchronize()
+            assert torch.equal(z[a], eager[a]), (a, b)
+            assert torch.equal(y[b], eager[b]), (a, b)
+    assert S.flags() == 0
+    S.close()
