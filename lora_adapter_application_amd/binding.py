@@ -254,6 +254,7 @@ def lora_slots_create(max_loras: int, max_rank: int, modules: Sequence[Sequence[
 
 
 def lora_slots_destroy(ctx) -> None:
+    _attended.pop(ctx, None)
     _check(load_library().lora_slots_destroy(ctx), ctx)
 
 
@@ -652,12 +653,17 @@ class AttendBatch:
                             _ptr(self.prefix_pages))
 
 
+# by ctx, the batch prepared last (kept alive with it), its tokens and query heads
+_attended = {}
+
+
 def lora_attend_prepare(ctx, cache, q_heads: int, batch: AttendBatch, n_tokens: int,
                         stream=None) -> None:
     """Plan the attention of a batch of n_tokens new tokens, once a step for all layers."""
     s = batch._struct(n_tokens)
     _check(load_library().lora_attend_prepare(ctx, cache, int(q_heads), ctypes.byref(s),
                                               _stream_of(stream, batch.lengths)), ctx)
+    _attended[ctx] = (batch, int(n_tokens), int(q_heads))
 
 
 def lora_attend(ctx, cache, q, y, scale: float, stream=None) -> None:
@@ -730,7 +736,6 @@ class Slots:
         self.device = int(device)
         self._loading = []       # sources of base loads that may still be read
         self._loading_bytes = 0
-        self._attended = None    # the prepared batch, its tokens and query heads
         self.ctx = lora_slots_create(max_loras, max_rank, self.modules,
                                      LORA_BF16 if dtype == "bf16" else LORA_FP32, max_tokens,
                                      device)
@@ -903,7 +908,6 @@ class Slots:
             n_tokens = batch.n_seqs
         self._check_batch(batch)
         lora_attend_prepare(self.ctx, cache.handle, q_heads, batch, n_tokens, stream)
-        self._attended = (batch, int(n_tokens), int(q_heads))
 
     def _check_attend(self, cache, q_heads, q, y, n_tokens):
         for name, t in (("q", q), ("y", y)):
@@ -911,8 +915,9 @@ class Slots:
 
     def attend(self, cache, q, y, scale=None, stream=None):
         """Attention of the prepared batch; scale: default 1 / sqrt(head_dim)."""
-        if self._attended is not None:
-            self._check_attend(cache, self._attended[2], q, y, self._attended[1])
+        last = _attended.get(self.ctx)
+        if last is not None:
+            self._check_attend(cache, last[2], q, y, last[1])
         lora_attend(self.ctx, cache.handle, q, y, cache.head_dim ** -0.5 if scale is None else scale,
                     stream)
 
@@ -1005,10 +1010,10 @@ class Slots:
             if prepare:
                 rc = lib.lora_attend_prepare(ctx, handle, q_heads, ctypes.byref(s), st)
                 if not rc:
-                    self._attended = mine
-            elif self._attended is not None and self._attended[1:] != mine[1:]:
+                    _attended[ctx] = mine
+            elif _attended.get(ctx, mine)[1:] != mine[1:]:
                 raise ValueError("the batch prepared last has %d tokens of %d heads, q %d of %d"
-                                 % (*self._attended[1:], *mine[1:]))
+                                 % (*_attended[ctx][1:], *mine[1:]))
             rc = rc or lib.lora_attend(ctx, handle, qp, yp, factor, st)
             if rc:
                 _check(rc, ctx)

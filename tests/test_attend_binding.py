@@ -1,0 +1,104 @@
+"""What the binding's calls of attention and the cache check for themselves, on the CPU: a library that
+only notes its calls, and tensors without memory."""
+import ctypes
+
+import pytest
+import torch
+
+from lora_adapter_application_amd import binding
+
+
+class Library:
+    """Every entry point succeeds; `calls` has (name, arguments)."""
+
+    def __init__(self):
+        self.calls = []
+        self.made = 0x1000
+
+    def __getattr__(self, name):
+        if not name.startswith("lora_"):
+            raise AttributeError(name)
+
+        def call(*args):
+            self.calls.append((name, args))
+            if name in ("lora_slots_create", "lora_cache_create"):
+                out = args[0] if name == "lora_slots_create" else args[1]
+                self.made += 0x100
+                ctypes.cast(out, ctypes.POINTER(ctypes.c_void_p))[0] = self.made
+            return 0
+        return call
+
+    def names(self):
+        return [n for n, _ in self.calls]
+
+
+class Tensor:
+    """The part of a device tensor that the checks look at."""
+
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=torch.bfloat16, at=0x7000):
+        self.shape, self.dtype, self.at = torch.Size(shape), dtype, at
+        self.device = torch.device("cuda", 0)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.at
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(binding, "load_library", lambda *a: lib)
+    return lib
+
+
+def requests(n):
+    i32 = torch.int32
+    return binding.AttendBatch(Tensor(n, dtype=i32), Tensor(n, 4, dtype=i32))
+
+
+def pool():
+    S = binding.Slots(1, 1, [(64, 64)], "bf16", 64)
+    return S, S.cache(2, 64, 8, 32)
+
+
+STREAM = 7                                                    # so that no current stream is looked up
+
+
+@pytest.mark.parametrize("first", [None, 2])
+def test_rows_are_checked_against_a_plan_made_by_the_entry_point(lib, first):
+    """Whatever the pool's own calls prepared before, or nothing."""
+    S, cache = pool()
+    if first:
+        S.attend_prepare(cache, 4, requests(first), stream=STREAM)
+    binding.lora_attend_prepare(S.ctx, cache.handle, 4, requests(8), 8, STREAM)
+    short, whole = Tensor(2, 256), Tensor(8, 256)
+    late = S.bind_attend(cache, 4, Tensor(2, 256), Tensor(2, 256), requests(2), prepare=False, stream=STREAM)
+    for call in (lambda: S.attend(cache, short, whole, stream=STREAM), lambda: S.attend(cache, whole, short, stream=STREAM), late):
+        with pytest.raises(ValueError):
+            call()
+    assert "lora_attend" not in lib.names()
+    S.attend(cache, whole, whole, stream=STREAM)
+    S.bind_attend(cache, 4, whole, whole, requests(8), prepare=False, stream=STREAM)()
+    assert lib.names().count("lora_attend") == 2
+
+
+def test_a_plan_goes_with_its_pool(lib):
+    S, cache = pool()
+    S.attend_prepare(cache, 4, requests(8), stream=STREAM)
+    at = S.ctx
+    S.close()
+    lib.made = at - 0x100                                     # another pool at the same address
+    S, cache = pool()
+    assert S.ctx == at
+    S.attend(cache, Tensor(2, 256), Tensor(2, 256), stream=STREAM)   # no plan: the library refuses the call
+    assert lib.names()[-1] == "lora_attend"
