@@ -931,6 +931,16 @@ class Slots:
                 _check(rc, self.ctx)
         return call
 
+    def _bound_cache(self, fn, cache, args, refs):
+        """The same of fn(ctx, cache, *args), by the handle that the cache has at the call: none
+        once it is closed, since another cache may have got the old one."""
+        def call():
+            _ = refs
+            rc = fn(self.ctx, cache.handle, *args)
+            if rc:
+                _check(rc, self.ctx)
+        return call
+
     def bind_base(self, modules, x, y, add=None, n_tokens=None, stream=None):
         """base_group with its arguments marshalled and its stream taken once, as bind_step
         does: returns a function that makes the library call."""
@@ -979,17 +989,17 @@ class Slots:
         """cache_store with its arguments marshalled once."""
         n_tok = slots.numel() if n_tokens is None else int(n_tokens)
         self._check_slots(cache, k, v, slots, n_tok)
-        return self._bound(load_library().lora_cache_store,
-                           (cache.handle, _ptr(k), _ptr(v), _ptr(slots), n_tok,
-                            _stream_of(stream, slots)), (cache, k, v, slots))
+        return self._bound_cache(load_library().lora_cache_store, cache,
+                                 (_ptr(k), _ptr(v), _ptr(slots), n_tok, _stream_of(stream, slots)),
+                                 (k, v, slots))
 
     def bind_cache_load(self, cache, slots, k, v, n_tokens=None, stream=None):
         """cache_load with its arguments marshalled once."""
         n_tok = slots.numel() if n_tokens is None else int(n_tokens)
         self._check_slots(cache, k, v, slots, n_tok)
-        return self._bound(load_library().lora_cache_load,
-                           (cache.handle, _ptr(slots), _ptr(k), _ptr(v), n_tok,
-                            _stream_of(stream, slots)), (cache, k, v, slots))
+        return self._bound_cache(load_library().lora_cache_load, cache,
+                                 (_ptr(slots), _ptr(k), _ptr(v), n_tok, _stream_of(stream, slots)),
+                                 (k, v, slots))
 
     def bind_attend(self, cache, q_heads, q, y, batch, scale=None, prepare=True, stream=None):
         """attend_prepare (unless prepare is False: then the batch prepared last is used, as the
@@ -999,14 +1009,14 @@ class Slots:
         self._check_batch(batch)
         lib, st = load_library(), _stream_of(stream, q)
         s = batch._struct(n_tok)
-        ctx, handle, qp, yp = self.ctx, cache.handle, _ptr(q), _ptr(y)
+        qp, yp = _ptr(q), _ptr(y)
         factor = float(cache.head_dim ** -0.5 if scale is None else scale)
-        refs = (cache, q, y, batch, s)
+        refs = (q, y, batch, s)
         mine = (batch, n_tok, int(q_heads))
 
         def call():
             _ = refs
-            rc = 0
+            ctx, handle, rc = self.ctx, cache.handle, 0      # none once closed
             if prepare:
                 rc = lib.lora_attend_prepare(ctx, handle, q_heads, ctypes.byref(s), st)
                 if not rc:

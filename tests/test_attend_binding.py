@@ -102,3 +102,29 @@ def test_a_plan_goes_with_its_pool(lib):
     assert S.ctx == at
     S.attend(cache, Tensor(2, 256), Tensor(2, 256), stream=STREAM)   # no plan: the library refuses the call
     assert lib.names()[-1] == "lora_attend"
+
+
+def bound(S, cache):
+    slots, k = Tensor(8, dtype=torch.int32), Tensor(8, 128)
+    q = Tensor(8, 256)
+    return {"lora_cache_store": S.bind_cache_store(cache, k, k, slots, stream=STREAM),
+            "lora_cache_load": S.bind_cache_load(cache, slots, k, k, stream=STREAM),
+            "lora_attend_prepare": S.bind_attend(cache, 4, q, q, requests(8), stream=STREAM),
+            "lora_attend": S.bind_attend(cache, 4, q, q, requests(8), prepare=False, stream=STREAM)}
+
+
+@pytest.mark.parametrize("name", ["lora_cache_store", "lora_cache_load", "lora_attend_prepare", "lora_attend"])
+def test_bound_calls_after_close(lib, name):
+    """The library gets no address that it has freed: NULL, which it refuses."""
+    S, cache = pool()
+    call = bound(S, cache)[name]
+    call()
+    assert lib.calls[-1][1][:2] == (S.ctx, cache.handle) if "prepare" not in name else True
+    cache.close()
+    lib.calls.clear()
+    call()
+    assert lib.calls[0][0] == name and lib.calls[0][1][1] is None
+    S.close()
+    lib.calls.clear()
+    call()
+    assert lib.calls[0][0] == name and lib.calls[0][1][0] is None
