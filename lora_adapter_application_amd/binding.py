@@ -1048,13 +1048,13 @@ class Slots:
             n, mods, xp = _group(modules, x, "x")
             _, _, yp = _group(modules, y, "y")
             calls.append((n, mods, xp, yp))
-        ctx = self.ctx
         plan = lib.lora_plan_prepare
         apply_group = lib.lora_apply_group_fused if fused else lib.lora_apply_group
         refs = (idx, groups)
 
         def step():
             _ = refs
+            ctx = self.ctx                                   # none once closed
             if prepare:
                 rc = plan(ctx, pidx, n_tokens, st)
                 if rc:

@@ -128,3 +128,15 @@ def test_bound_calls_after_close(lib, name):
     lib.calls.clear()
     call()
     assert lib.calls[0][0] == name and lib.calls[0][1][0] is None
+
+
+def test_a_bound_step_after_close(lib):
+    S, _ = pool()
+    x = Tensor(8, 64)
+    step = S.bind_step([([0], [x], [x])], Tensor(8, dtype=torch.int32), stream=STREAM)
+    step()
+    S.close()
+    lib.calls.clear()
+    step()
+    assert lib.names() == ["lora_plan_prepare", "lora_apply_group"]
+    assert all(args[0] is None for _, args in lib.calls)
