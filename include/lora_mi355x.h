@@ -721,9 +721,10 @@ int lora_attend_prepare(lora_ctx *ctx, const lora_cache *cache, int32_t q_heads,
  *   scale  > 0, e.g. 1 / sqrt(head_dim)
  * The keys and values of the batch's new tokens must be stored before (lora_cache_store on
  * the same stream).  A prefix is read once for all of its requests of few new tokens.  Scores,
- * maxima, sums and outputs are kept in fp32; for their product with the values a bf16 ctx
- * rounds the weights p_s to bf16 (over 8-bit caches to 16 bits, where a request or prefix has
- * no more than 32 rows of a key-value head), and it rounds y once.  The order of the sums goes by the batch, so
+ * maxima, sums and outputs are kept in fp32.  For their product with the values a bf16 ctx takes the
+ * weights p_s as two bf16 (together within 2^-15) where a request or prefix has no more than 32 rows of
+ * a key-value head (rows: its new tokens times the query heads of one), and as one (2^-8) where it has
+ * more; it rounds y once.  The order of the sums goes by the batch, so
  * equal calls give equal bits.  Tokens that a row does not see change nothing, whatever their
  * slots hold.  A token that sees nothing (a request of length 0 without a prefix) gets zeros;
  * rows of q that belong to no request leave their row of y as it is.  A page outside of the
