@@ -6,13 +6,14 @@
 // token and a share of its heads.  A head is cut in items, a pair of 16-byte pieces that turn
 // against each other, a piece of neighbouring pairs, or a piece behind rotary_dim; the items go
 // to a power of two of neighbouring lanes, which keep them in registers while their sums of
-// squares meet in log2 shuffles.  One read and one write of x: bytes bound it, and for few tokens
-// the chain position, sine and cosine, barrier, load, shuffles, store.
+// squares meet in log2 shuffles.  One read and one write of x; for few tokens the chain position, sine
+// and cosine, barrier, load, shuffles, store is what it takes.
 //
-// 64 heads of 128, bf16: 32,556 tokens take 224 us (4.77 TB/s, 0.98 of a copy); 72 heads, 512 tokens
-// 7.4 us; one token 4.5 us, of which the host's call is 3.4.  A lane fetches its next head before the
-// sums of this one; the registers for that leave four waves a SIMD, and more waves spill (bounds of
-// six 546 us, of eight 899).
+// 64 heads of 128, bf16: 32,556 tokens take 224 us (4.77 TB/s, 0.98 of a copy of 2 GiB), 213 over the same
+// tensors again and again, where lora_rotary.hip moves as many bytes in 182: bytes are not all that
+// bounds it.  A lane fetches its next head before the sums of this one; the registers for that leave five
+// waves a SIMD (rotary positions alone have eight), and more spill (bounds of six 546 us, of eight
+// 899).  72 heads, 512 tokens 7.4 us; one token 4.5 us, of which the host's call is 3.4.
 #include <hip/hip_runtime.h>
 
 #include "lora_attend.h"
@@ -191,42 +192,52 @@ __global__ __launch_bounds__(256) void norm_rotary_kernel(NormArgs a, int lanes)
     }
 }
 
+// Where tokens are few, as many workgroups as the chip's 256 CUs hold at once, so that none waits for a
+// second round: what the form's registers leave, 4 to 8 a CU.
 template <typename T, bool HALF, int V, int NI>
-void launch_items(const NormArgs &a, int lanes, dim3 grid, hipStream_t st)
+hipError_t launch_items(const NormArgs &a, int lanes, hipStream_t st)
 {
-    norm_rotary_kernel<T, HALF, V, NI><<<grid, 256, 0, st>>>(a, lanes);
+    static const int hold = [] {
+        int n = 0;
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_rotary_kernel<T, HALF, V, NI>, 256, 0) != hipSuccess) {
+            (void)hipGetLastError();
+            n = 4;
+        }
+        return 256 * (n < 1 ? 1 : n);
+    }();
+    const int passes = (a.rot.total_heads + 256 / lanes - 1) / (256 / lanes);
+    const int split = passes < hold / a.rot.T ? passes : hold / a.rot.T;
+    norm_rotary_kernel<T, HALF, V, NI><<<dim3(a.rot.T, split < 1 ? 1 : split), 256, 0, st>>>(a, lanes);
+    return hipGetLastError();
+}
+
+template <typename T, bool HALF, int V>
+hipError_t launch_half(const NormArgs &a, hipStream_t st)
+{
+    const lora_rotary &rot = a.rot.rot;
+    constexpr int N = V == 1 ? 1 : HALF ? V : V / 2;
+    const int items = rot.rotary_dim / 2 / N + (rot.head_dim - rot.rotary_dim) / V;
+    int lanes = 1;
+    while (lanes < items && lanes < 64)
+        lanes *= 2;
+    const int each = (items + lanes - 1) / lanes;        // at most 8: head_dim is at most 512
+    if (each == 1)
+        return launch_items<T, HALF, V, 1>(a, lanes, st);
+    if (each == 2)
+        return launch_items<T, HALF, V, 2>(a, lanes, st);
+    if constexpr (V == 1) {
+        if (each <= 4)
+            return launch_items<T, HALF, V, 4>(a, lanes, st);
+        if (each <= 8)
+            return launch_items<T, HALF, V, 8>(a, lanes, st);
+    }
+    return hipGetLastError();
 }
 
 template <typename T, int V>
 hipError_t launch(const NormArgs &a, hipStream_t st)
 {
-    const lora_rotary &rot = a.rot.rot;
-    const bool half = rot.layout == LORA_ROTARY_HALF;
-    const int pairs = rot.rotary_dim / 2, N = V == 1 ? 1 : half ? V : V / 2;
-    const int items = pairs / N + (rot.head_dim - rot.rotary_dim) / V;
-    int lanes = 1;
-    while (lanes < items && lanes < 64)
-        lanes *= 2;
-    const int each = (items + lanes - 1) / lanes;        // at most 8: head_dim is at most 512
-    const int passes = (a.rot.total_heads + 256 / lanes - 1) / (256 / lanes);
-    // where tokens are few, as many workgroups as the chip's 256 CUs hold at once, so that none waits for
-    // a second round: 5 each of the kernel with most registers, else 8
-    const int hold = 256 * (sizeof(T) == 2 && half ? 5 : 8);
-    const int split = passes < hold / a.rot.T ? passes : hold / a.rot.T;
-    const dim3 grid(a.rot.T, split < 1 ? 1 : split);
-#define LORA_NORM(NI) half ? launch_items<T, true, V, NI>(a, lanes, grid, st) : launch_items<T, false, V, NI>(a, lanes, grid, st)
-    if (each == 1)
-        LORA_NORM(1);
-    else if (each == 2)
-        LORA_NORM(2);
-    else if constexpr (V == 1) {
-        if (each <= 4)
-            LORA_NORM(4);
-        else
-            LORA_NORM(8);
-    }
-#undef LORA_NORM
-    return hipGetLastError();
+    return a.rot.rot.layout == LORA_ROTARY_HALF ? launch_half<T, true, V>(a, st) : launch_half<T, false, V>(a, st);
 }
 
 }  // namespace
