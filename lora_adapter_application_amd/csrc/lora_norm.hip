@@ -220,18 +220,20 @@ hipError_t launch_half(const NormArgs &a, hipStream_t st)
     int lanes = 1;
     while (lanes < items && lanes < 64)
         lanes *= 2;
-    const int each = (items + lanes - 1) / lanes;        // at most 8: head_dim is at most 512
+    const int each = (items + lanes - 1) / lanes;        // head_dim is at most 512: 1 of 8 elements, 2 of 4, 8 of 1
+    static_assert(LORA_NORM_MAX_DIM == 512, "");
     if (each == 1)
         return launch_items<T, HALF, V, 1>(a, lanes, st);
-    if (each == 2)
-        return launch_items<T, HALF, V, 2>(a, lanes, st);
+    if constexpr (V < 8)
+        if (each == 2)
+            return launch_items<T, HALF, V, 2>(a, lanes, st);
     if constexpr (V == 1) {
         if (each <= 4)
             return launch_items<T, HALF, V, 4>(a, lanes, st);
         if (each <= 8)
             return launch_items<T, HALF, V, 8>(a, lanes, st);
     }
-    return hipGetLastError();
+    return hipErrorInvalidValue;
 }
 
 template <typename T, int V>
