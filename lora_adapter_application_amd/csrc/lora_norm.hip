@@ -46,7 +46,9 @@ __global__ __launch_bounds__(256) void norm_rotary_kernel(NormArgs a, int lanes)
     typedef Pack<T, V> P;
     __shared__ float2 cs[kPairs];
     const RotaryArgs &ro = a.rot;
-    const int t = blockIdx.x;
+    const uint32_t t = blockIdx.z * gridDim.x + blockIdx.x;  // tokens in rows of a grid: one holds 2^32 threads at most
+    if (t >= (uint32_t)ro.T)
+        return;
     const int rd = ro.rot.rotary_dim, pairs = rd >> 1, hd = ro.rot.head_dim;
     // Items of a head: `turning` of them hold N pairs each, in one or two pieces, the rest one piece.
     constexpr bool TWO = HALF || V == 1;                 // a turning item has two pieces
@@ -207,7 +209,9 @@ hipError_t launch_items(const NormArgs &a, int lanes, hipStream_t st)
     }();
     const int passes = (a.rot.total_heads + 256 / lanes - 1) / (256 / lanes);
     const int split = passes < hold / a.rot.T ? passes : hold / a.rot.T;
-    norm_rotary_kernel<T, HALF, V, NI><<<dim3(a.rot.T, split < 1 ? 1 : split), 256, 0, st>>>(a, lanes);
+    const int across = a.rot.T < 1 << 22 ? a.rot.T : 1 << 22;
+    const dim3 grid(across, split < 1 ? 1 : split, (a.rot.T - 1) / across + 1);
+    norm_rotary_kernel<T, HALF, V, NI><<<grid, 256, 0, st>>>(a, lanes);
     return hipGetLastError();
 }
 
