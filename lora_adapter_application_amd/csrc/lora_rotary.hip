@@ -49,7 +49,9 @@ template <typename T, bool HALF, int V>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a)
 {
     __shared__ float2 cs[kPairs];
-    const int t = blockIdx.x;
+    const uint32_t t = blockIdx.z * gridDim.x + blockIdx.x;  // tokens in rows of a grid: one holds 2^32 threads at most
+    if (t >= (uint32_t)a.T)
+        return;
     const int pairs = a.rot.rotary_dim >> 1, hd = a.rot.head_dim, rd = a.rot.rotary_dim;
     const double pos = (double)a.positions[t];
     for (int p = threadIdx.x; p < pairs; p += 256) {
@@ -150,7 +152,8 @@ hipError_t launch(const RotaryArgs &a, hipStream_t st)
     const int passes = (a.total_heads + 256 / pieces - 1) / (256 / pieces);
     // enough workgroups for the chip when tokens are few
     const int split = passes < 1 ? 1 : a.T >= 2048 ? 1 : passes < 2048 / a.T ? passes : 2048 / a.T;
-    const dim3 grid(a.T, split);
+    const int across = a.T < 1 << 22 ? a.T : 1 << 22;
+    const dim3 grid(across, split, (a.T - 1) / across + 1);
     if (half)
         rotary_kernel<T, true, V><<<grid, 256, 0, st>>>(a);
     else

@@ -40,3 +40,21 @@ def test_more_than_2_to_the_24_tokens():
         err = (y[at:at + part].double() - z).abs()
         assert bool((err <= z.abs() * (HALF_STEP[torch.bfloat16] + 32 * U32)).all()), at
     S.close()
+
+
+def test_more_than_2_to_the_24_positions():
+    """The same turn without the norm: whole numbers and signs, exact."""
+    n, dim = (1 << 24) + 5, 8
+    S = binding.Slots(1, 1, [(8, dim)], "bf16", n)
+    rot = binding.lora_rotary_init(dim, 2, "half")
+    rot.turns[0] = 0.25
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randint(-8, 9, (n, dim), generator=gen, device="cuda", dtype=torch.int32).to(torch.bfloat16)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    y = torch.full_like(x, 77.0)
+    S.rotary_group(rot, [0], [x], [y], pos)
+    a, b, quarter = x[:, 0], x[:, 1], pos % 4
+    assert torch.equal(y[:, 0], torch.where(quarter == 0, a, torch.where(quarter == 1, -b, torch.where(quarter == 2, -a, b))))
+    assert torch.equal(y[:, 1], torch.where(quarter == 0, b, torch.where(quarter == 1, a, torch.where(quarter == 2, -b, -a))))
+    assert torch.equal(y[:, 2:], x[:, 2:])
+    S.close()
