@@ -691,7 +691,7 @@ typedef struct {
 /*
  * Cut the attention of a batch into work of equal size, on the device, for lora_attend calls
  * with q_heads query heads and caches of `cache`'s kv_heads, head_dim and page_size (of any
- * kind): once a step for all layers.  q_heads is a multiple of kv_heads; query head h reads
+ * kind, at the best rate of its own): once a step for all layers.  q_heads is a multiple of kv_heads; query head h reads
  * key-value head h / (q_heads / kv_heads).
  * The plan stays valid until the next call of lora_attend_prepare.  It and the parts of lora_attend
  * are kept in the ctx's attention workspace, which grows with the batches prepared.  Under

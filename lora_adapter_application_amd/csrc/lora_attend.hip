@@ -953,7 +953,7 @@ __device__ __forceinline__ f32x16 scaled(f32x16 v, int r, f32x4 f)
 // Two workgroups a CU, so a SIMD has two waves: the scores of one block are formed beside the weights
 // of the block before it, and one wave's exponentials beside the other's products.  Prompts of 64
 // heads over 4096 shared and up to 1024 own tokens: 1210 us (970 TFLOP/s of what rows see; matrix
-// cores busy 0.48 of the time, vector instructions issued 0.50, together what a SIMD issues); 16
+// cores busy 0.48 of the time, vector instructions issued 0.50, LDS reading 0.24: none is full); 16
 // prefixes of 16,384 in int8 under 512 requests: 312 us (880 TFLOP/s).  Not kept: units of 64 tokens
 // at once (spills, 1700 us and more), two chains of sums for the scores (+1%), operands six
 // instructions ahead (none).  Weights are one bf16 here: in two parts, with a second product for what the

@@ -125,13 +125,13 @@ __device__ __forceinline__ Pack<T, 8> load8(const T *p, bool vec)
 // from a multiple of 8 on) they pass through LDS and move as units, whatever their place in the
 // batch; other tokens move an element at a time.  An octet is stored by the window with its first
 // token, which fetches up to 7 tokens behind itself for it, and loaded by every window that it
-// touches.  Prompts go at the rate of memory; single tokens of many requests write 2 bytes to each of
-// a unit's lines.
+// touches.  Prompts go at the rate of memory; single tokens of many requests write every 8th element of a
+// run, 8 dims of bf16 or 16 codes to a line of 128 bytes.
 //
 // Store and load: 13,044 tokens of 32 heads of 128, bf16, 92 and 106 us (4.4 TB/s over both); 32,971
 // of 8 heads, int8, 55 and 44 us (4.2 TB/s); with values moved an element at a time the two cases took
 // 303 and 139 us.  512 single tokens of 8 heads, fp8, 8.2 and 5.4 us: the chain slots, data, maximum,
-// codes, store, and the lines of which a store writes two bytes.
+// codes, store, and the stores of single elements.
 constexpr int kWindow = 32, kAround = 7;
 
 // Workgroups equal mod 8 share an XCD: each XCD takes a run of neighbouring windows, which write
