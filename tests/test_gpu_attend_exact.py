@@ -106,7 +106,10 @@ def test_each_token_counts_once(case):
     rows = r.own_rows()
     bound = want.abs() * (HALF_STEP[TORCH[r.dtype]] * (1 + 4 * U32) + 4 * U32)
     if r.dtype == "bf16" and r.kind == "native":
-        bound += 2.0 ** -39                                   # second parts of weights: 2^-40 of values up to 1
+        # Second parts of weights are 2^-40 of values up to 1, and adding them may round the running sum, which
+        # the tokens counted so far bound, by 2^-23 of it for each block of 32 tokens, over the count.
+        most = max(r.lengths) + max([p[2] for p in r.prefixes] + [0])
+        bound += 2.0 ** -39 + (most / 32 + 8) * 2.0 ** -23
     err, bound = (got - want).abs()[rows], bound[rows]
     assert bool((err <= bound).all()), f"{int((err > bound).sum())} of {err.numel()}, worst {err.max():.3e}"
     # a unit more or less in a sum is out of bounds in most dims (dim 0 has a unit everywhere)
