@@ -130,3 +130,40 @@ def test_a_replayed_graph_leaves_the_eager_plan():
             assert torch.equal(y[b], eager[b]), (a, b)
     assert S.flags() == 0
     S.close()
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("fp32", 256)])
+@pytest.mark.parametrize("planned", ["native", "fp8"])
+def test_layers_of_other_kinds_under_one_plan(dtype, dim, planned):
+    shape = (4, 2, dim, 32, [1, 40, 3], [500, 90, 41], [(0, 2, 300)])
+    layers = [Requests(61, dtype, kind, *shape) for kind in ("native", "fp8", "int8")]
+    S = binding.Slots(1, 1, [(64, 64)], dtype, 4096)
+    caches = [cache_of(S, r) for r in layers]
+    S.attend_prepare(caches[0 if planned == "native" else 1], 4, layers[0].batch())
+    q = layers[0].q.cuda()
+    for r, cache in zip(layers, caches):
+        y = torch.full_like(q, 7.0)
+        before = y.clone()
+        S.attend(cache, q, y)
+        torch.cuda.synchronize()
+        check_rows(r, y, dim ** -0.5, before, r.kind)
+    assert S.flags() == 0
+    S.close()
+
+
+def test_bound_calls_after_close():
+    r = Requests(62, "bf16", "native", 4, 2, 64, 32, [1] * 3, [40, 3, 64])
+    S, cache = r.make()
+    q, y, b = r.q.cuda(), torch.empty_like(r.q).cuda(), r.batch()
+    k, slots = torch.zeros(3, 128, dtype=torch.bfloat16, device="cuda"), torch.arange(3, dtype=torch.int32, device="cuda")
+    calls = [S.bind_cache_store(cache, k, k, slots), S.bind_cache_load(cache, slots, k, k.clone()),
+             S.bind_attend(cache, 4, q, y, b), S.bind_attend(cache, 4, q, y, b, prepare=False)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    for close in (cache.close, S.close):
+        close()
+        for call in calls:
+            with pytest.raises(binding.LoraError) as e:
+                call()
+            assert e.value.status == binding.LORA_ERR_INVALID_ARGUMENT
