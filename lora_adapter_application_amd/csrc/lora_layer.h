@@ -106,6 +106,19 @@ struct RotaryArgs {
     int32_t total_heads;
     const int32_t *positions;
 };
+// Workgroups of a token each are launched for so many tokens at once: a grid holds 2^32 threads a side.
+constexpr int32_t kRotaryTokens = 1 << 22;
+// The part of a call from token `first` on.
+inline RotaryArgs rotary_part(RotaryArgs a, int64_t first, int elem)
+{
+    a.T = a.T - first < kRotaryTokens ? (int32_t)(a.T - first) : kRotaryTokens;
+    a.positions += first;
+    for (int i = 0; i < a.n; ++i) {
+        a.m[i].x = (const char *)a.m[i].x + first * a.m[i].width * elem;
+        a.m[i].y = (char *)a.m[i].y + first * a.m[i].width * elem;
+    }
+    return a;
+}
 hipError_t launch_rotary(bool bf16, bool vec, const RotaryArgs &a, hipStream_t st);
 
 }  // namespace lora

@@ -46,9 +46,7 @@ __global__ __launch_bounds__(256) void norm_rotary_kernel(NormArgs a, int lanes)
     typedef Pack<T, V> P;
     __shared__ float2 cs[kPairs];
     const RotaryArgs &ro = a.rot;
-    const uint32_t t = blockIdx.z * gridDim.x + blockIdx.x;  // tokens in rows of a grid: one holds 2^32 threads at most
-    if (t >= (uint32_t)ro.T)
-        return;
+    const int t = blockIdx.x;
     const int rd = ro.rot.rotary_dim, pairs = rd >> 1, hd = ro.rot.head_dim;
     // Items of a head: `turning` of them hold N pairs each, in one or two pieces, the rest one piece.
     constexpr bool TWO = HALF || V == 1;                 // a turning item has two pieces
@@ -209,9 +207,7 @@ hipError_t launch_items(const NormArgs &a, int lanes, hipStream_t st)
     }();
     const int passes = (a.rot.total_heads + 256 / lanes - 1) / (256 / lanes);
     const int split = passes < hold / a.rot.T ? passes : hold / a.rot.T;
-    const int across = a.rot.T < 1 << 22 ? a.rot.T : 1 << 22;
-    const dim3 grid(across, split < 1 ? 1 : split, (a.rot.T - 1) / across + 1);
-    norm_rotary_kernel<T, HALF, V, NI><<<grid, 256, 0, st>>>(a, lanes);
+    norm_rotary_kernel<T, HALF, V, NI><<<dim3(a.rot.T, split < 1 ? 1 : split), 256, 0, st>>>(a, lanes);
     return hipGetLastError();
 }
 
@@ -246,13 +242,26 @@ hipError_t launch(const NormArgs &a, hipStream_t st)
     return a.rot.rot.layout == LORA_ROTARY_HALF ? launch_half<T, true, V>(a, st) : launch_half<T, false, V>(a, st);
 }
 
-}  // namespace
-
-hipError_t launch_norm_rotary(bool bf16, bool vec, const NormArgs &a, hipStream_t st)
+hipError_t launch_tokens(bool bf16, bool vec, const NormArgs &a, hipStream_t st)
 {
     if (bf16)
         return vec ? launch<uint16_t, 8>(a, st) : launch<uint16_t, 1>(a, st);
     return vec ? launch<float, 4>(a, st) : launch<float, 1>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_norm_rotary(bool bf16, bool vec, const NormArgs &a, hipStream_t st)
+{
+    if (a.rot.T <= kRotaryTokens)
+        return launch_tokens(bf16, vec, a, st);
+    hipError_t e = hipSuccess;
+    for (int64_t first = 0; first < a.rot.T && e == hipSuccess; first += kRotaryTokens) {
+        NormArgs part = a;
+        part.rot = rotary_part(a.rot, first, bf16 ? 2 : 4);
+        e = launch_tokens(bf16, vec, part, st);
+    }
+    return e;
 }
 
 }  // namespace lora

@@ -49,9 +49,7 @@ template <typename T, bool HALF, int V>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a)
 {
     __shared__ float2 cs[kPairs];
-    const uint32_t t = blockIdx.z * gridDim.x + blockIdx.x;  // tokens in rows of a grid: one holds 2^32 threads at most
-    if (t >= (uint32_t)a.T)
-        return;
+    const int t = blockIdx.x;
     const int pairs = a.rot.rotary_dim >> 1, hd = a.rot.head_dim, rd = a.rot.rotary_dim;
     const double pos = (double)a.positions[t];
     for (int p = threadIdx.x; p < pairs; p += 256) {
@@ -152,8 +150,7 @@ hipError_t launch(const RotaryArgs &a, hipStream_t st)
     const int passes = (a.total_heads + 256 / pieces - 1) / (256 / pieces);
     // enough workgroups for the chip when tokens are few
     const int split = passes < 1 ? 1 : a.T >= 2048 ? 1 : passes < 2048 / a.T ? passes : 2048 / a.T;
-    const int across = a.T < 1 << 22 ? a.T : 1 << 22;
-    const dim3 grid(across, split, (a.T - 1) / across + 1);
+    const dim3 grid(a.T, split);
     if (half)
         rotary_kernel<T, true, V><<<grid, 256, 0, st>>>(a);
     else
@@ -161,13 +158,24 @@ hipError_t launch(const RotaryArgs &a, hipStream_t st)
     return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_rotary(bool bf16, bool vec, const RotaryArgs &a, hipStream_t st)
+hipError_t launch_tokens(bool bf16, bool vec, const RotaryArgs &a, hipStream_t st)
 {
     if (bf16)
         return vec ? launch<uint16_t, 8>(a, st) : launch<uint16_t, 1>(a, st);
     return vec ? launch<float, 4>(a, st) : launch<float, 1>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_rotary(bool bf16, bool vec, const RotaryArgs &a, hipStream_t st)
+{
+    if (a.T <= kRotaryTokens)
+        return launch_tokens(bf16, vec, a, st);
+    hipError_t e = hipSuccess;
+    for (int64_t first = 0; first < a.T && e == hipSuccess; first += kRotaryTokens) {
+        e = launch_tokens(bf16, vec, rotary_part(a, first, bf16 ? 2 : 4), st);
+    }
+    return e;
 }
 
 }  // namespace lora
